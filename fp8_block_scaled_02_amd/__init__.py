@@ -21,8 +21,16 @@ Functions carry the names of the C entry points:
 * ``fp8w_quantize_act(x) -> (x_codes, x_scale)`` and
   ``fp8w_gemv_block_w8a8(x_codes, x_scale, codes, scales) -> y`` / ``_mx_w8a8``:
   the W8A8 route (per-tensor fp8 activation, fp8 x fp8 matrix cores)
+* ``fp8w_route_experts(logits, top_k) -> ExpertRouting``: the experts of each
+  token, their weights, and the tokens sorted by expert
+* ``fp8w_gemm_experts(x, codes, scales, offsets, rows) -> y``: products grouped
+  by expert on fp8 weights [E,n,k], plain or with a gated SiLU, and
+  ``fp8w_combine_experts(y, weights, slots) -> out``: the weighted sum of each
+  token's experts
+* ``fp8w_logprobs(logits, targets, top) -> Logprobs``: log probabilities of
+  given tokens, entropy and top alternatives
 
-plus ``Fp8Weight``, a format-tagged weight whose GEMV asserts the format
+plus ``Fp8Experts``, the fp8 weights of a layer's experts, and ``Fp8Weight``, a format-tagged weight whose GEMV asserts the format
 before dispatch (a scale buffer of the wrong format cannot be detected by a
 kernel: "quantize_fp8_bs.rs", Atlas weight_map, module notes).
 """
@@ -31,7 +39,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8w.so")
@@ -76,6 +84,13 @@ SIGNATURES = {
     "fp8w_quant_table_bytes": (_I64, [_I64]),
     "fp8w_quant_plan_init": (_I, [_P, _I64, _I, _P, _P]),
     "fp8w_quantize_grouped": (_I, [_P, _P]),
+    "fp8w_route_experts_workspace_bytes": (_I64, [_I64, _I64]),
+    "fp8w_route_experts": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I, _P, _I, ctypes.c_float, _P, _P, _P, _P, _P,
+                                _P, _I64, _P]),
+    "fp8w_gemm_experts": (_I, [_P, _I64, _P, _P, _I64, _I64, _P, _P, _I, _I64, _I64, _I, _P, _P]),
+    "fp8w_combine_experts": (_I, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _P]),
+    "fp8w_logprobs_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "fp8w_logprobs": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P]),
     "fp8w_block_scale_count": (_I64, [_I64, _I64]),
     "fp8w_mx_scale_count": (_I64, [_I64, _I64]),
     "fp8w_status_string": (ctypes.c_char_p, [_I]),
@@ -655,6 +670,234 @@ def fp8w_quantize_grouped(plan: QuantPlan, stream=None):
     _check(lib().fp8w_quantize_grouped(ctypes.byref(plan.plan), _stream_handle(stream)),
            "fp8w_quantize_grouped")
     return plan.codes, plan.scales
+
+
+# ---------------------------------------------------------------- experts --
+
+SCORE_IDS = {"softmax": 0, "sigmoid": 1}
+ACT_IDS = {"none": 0, "swiglu": 1}
+
+
+class ExpertRouting(NamedTuple):
+    """A router's choice: ``ids`` / ``weights`` / ``slots`` [tokens, top_k],
+    ``rows`` [tokens * top_k] (the token of each slot) and ``offsets``
+    [experts + 1] (expert e's slots)."""
+    ids: object
+    weights: object
+    slots: object
+    rows: object
+    offsets: object
+
+
+class Logprobs(NamedTuple):
+    """``logprob`` [tokens] (None without targets), ``entropy`` [tokens], and
+    ``top_ids`` / ``top_logprobs`` [tokens, top]."""
+    logprob: object
+    entropy: object
+    top_ids: object
+    top_logprobs: object
+
+
+def _logits(t, what: str):
+    """The dtype id and row stride of a [tokens, columns] logits tensor whose
+    rows are contiguous."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what}: must be a GPU tensor (libfp8w has no CPU path)")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise TypeError(f"{what}: dtype {t.dtype} is neither bfloat16 nor float32")
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-d tensor")
+    rows, cols = t.shape
+    stride = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or stride < cols:
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap")
+    return (1 if t.dtype is torch.float32 else 0), stride
+
+
+def _buffer(t, shape, dtype, device, what: str):
+    """An output buffer: a new one, or the caller's after a check."""
+    torch = _torch()
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _require(t, (dtype,), what, len(shape))
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    return t
+
+
+def _launch_stream(stream, *owned):
+    """The stream's handle.  Tensors made for this call belong to the current
+    stream: used on another, they are recorded there, so that their memory is
+    not handed out again before the kernels have run."""
+    torch = _torch()
+    if stream is None:
+        return int(torch.cuda.current_stream().cuda_stream)
+    handle = _stream_handle(stream)
+    if handle != int(torch.cuda.current_stream().cuda_stream):
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(handle)
+        for t in owned:
+            if t is not None:
+                t.record_stream(stream)
+    return handle
+
+
+def fp8w_route_experts(logits, top_k: int, score: str = "softmax", bias=None, renorm: bool = True,
+                       scale: float = 1.0, ids=None, weights=None, slots=None, rows=None, offsets=None,
+                       workspace=None, stream=None) -> ExpertRouting:
+    """Router logits [tokens, experts] (bf16 or f32) -> each token's ``top_k``
+    experts, their weights, and the map that sorts the tokens by expert."""
+    torch = _torch()
+    dtype, stride = _logits(logits, "logits")
+    t, e = logits.shape
+    k = int(top_k)
+    if score not in SCORE_IDS:
+        raise ValueError(f"unknown score {score!r}")
+    if bias is not None:
+        _require(bias, (torch.float32,), "bias", 1)
+        if bias.shape[0] != e:
+            raise ValueError(f"bias: expected shape {(e,)}, got {tuple(bias.shape)}")
+    if k < 1:
+        raise Fp8wError(ERR_SHAPE, "fp8w_route_experts")
+    dev, i32 = logits.device, torch.int32
+    ids = _buffer(ids, (t, k), i32, dev, "ids")
+    weights = _buffer(weights, (t, k), torch.float32, dev, "weights")
+    slots = _buffer(slots, (t, k), i32, dev, "slots")
+    rows = _buffer(rows, (t * k,), i32, dev, "rows")
+    offsets = _buffer(offsets, (e + 1,), i32, dev, "offsets")
+    if workspace is None and t > 32:
+        workspace = torch.empty(int(lib().fp8w_route_experts_workspace_bytes(t, e)), dtype=torch.uint8, device=dev)
+    _check(lib().fp8w_route_experts(
+        logits.data_ptr(), dtype, stride, t, e, k, SCORE_IDS[score], None if bias is None else bias.data_ptr(),
+        1 if renorm else 0, scale, ids.data_ptr(), weights.data_ptr(), slots.data_ptr(), rows.data_ptr(),
+        offsets.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _launch_stream(stream, ids, weights, slots, rows, offsets, workspace)), "fp8w_route_experts")
+    return ExpertRouting(ids, weights, slots, rows, offsets)
+
+
+def fp8w_gemm_experts(x, codes, scales, offsets, rows=None, fmt: str = "block", act: str = "none", y=None,
+                      stream=None):
+    """Products grouped by expert: slot i of expert e (``offsets[e] <= i <
+    offsets[e + 1]``) gets ``x[rows[i]] . deq(W_e)^T``, or with ``act="swiglu"``
+    ``silu(g) * u`` of the products with W_e's two halves of rows.  codes u8
+    [E,n,k]; scales the E scale buffers of ``fmt`` stacked.  Without ``rows``
+    slot i takes x's row i."""
+    torch = _torch()
+    _require(x, _bf16_like(torch), "x", 2)
+    _require(codes, (torch.uint8,), "codes", 3)
+    _require(offsets, (torch.int32,), "offsets", 1)
+    if act not in ACT_IDS:
+        raise ValueError(f"unknown act {act!r}")
+    fid = _format_id(fmt)
+    e, n, k = codes.shape
+    if x.shape[1] != k:
+        raise ValueError(f"fp8w_gemm_experts: x has {x.shape[1]} columns, the weights {k}")
+    want = (e, *scale_shape(fmt, n, k))
+    _require(scales, (_scale_dtype(torch, fmt),), "scales", len(want))
+    if tuple(scales.shape) != want:
+        raise ValueError(f"fp8w_gemm_experts: {fmt} scales must be {want}, got {tuple(scales.shape)}")
+    if offsets.shape[0] != e + 1:
+        raise ValueError(f"offsets: expected shape {(e + 1,)}, got {tuple(offsets.shape)}")
+    if rows is not None:
+        _require(rows, (torch.int32,), "rows", 1)
+    slots = x.shape[0] if rows is None else rows.shape[0]
+    n_out = n // 2 if act == "swiglu" else n
+    if y is None:
+        y = torch.empty((slots, n_out), dtype=torch.bfloat16, device=x.device)
+    else:
+        _require(y, _bf16_like(torch), "y", 2)
+        if tuple(y.shape) != (slots, n_out):
+            raise ValueError(f"y: expected shape {(slots, n_out)}, got {tuple(y.shape)}")
+    _check(lib().fp8w_gemm_experts(x.data_ptr(), x.shape[0], None if rows is None else rows.data_ptr(),
+                                   offsets.data_ptr(), e, slots, codes.data_ptr(), scales.data_ptr(), fid, n, k,
+                                   ACT_IDS[act], y.data_ptr(), _launch_stream(stream, y)), "fp8w_gemm_experts")
+    return y
+
+
+def fp8w_combine_experts(y, weights, slots, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] * y[slots[t, j]] (slots of -1 add nothing)."""
+    torch = _torch()
+    _require(y, _bf16_like(torch), "y", 2)
+    _require(weights, (torch.float32,), "weights", 2)
+    _require(slots, (torch.int32,), "slots", 2)
+    if weights.shape != slots.shape:
+        raise ValueError(f"weights {tuple(weights.shape)} and slots {tuple(slots.shape)} differ in shape")
+    t, k = slots.shape
+    n = y.shape[1]
+    if out is None:
+        out = torch.empty((t, n), dtype=torch.bfloat16, device=y.device)
+    else:
+        _require(out, _bf16_like(torch), "out", 2)
+        if tuple(out.shape) != (t, n):
+            raise ValueError(f"out: expected shape {(t, n)}, got {tuple(out.shape)}")
+    _check(lib().fp8w_combine_experts(y.data_ptr(), y.shape[0], weights.data_ptr(), slots.data_ptr(), t, k, n,
+                                      out.data_ptr(), _launch_stream(stream, out)), "fp8w_combine_experts")
+    return out
+
+
+@dataclass
+class Fp8Experts:
+    """The fp8 weights of a layer's experts: ``codes`` u8 [E,n,k] and the E
+    scale buffers of ``fmt`` (the C ABI's names) stacked."""
+    codes: object
+    scales: object
+    fmt: str
+
+    @classmethod
+    def quantize(cls, w, fmt: str = "block", stream=None) -> "Fp8Experts":
+        """bf16 [E,n,k] weights, each expert quantized by ``fp8w_quantize``."""
+        torch = _torch()
+        _require(w, _bf16_like(torch), "w", 3)
+        e, n, k = w.shape
+        codes = torch.empty((e, n, k), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((e, *scale_shape(fmt, n, k)), dtype=_scale_dtype(torch, fmt), device=w.device)
+        for i in range(e):
+            fp8w_quantize(w[i], fmt, codes[i], scales[i], stream=stream)
+        return cls(codes, scales, fmt)
+
+    def matmul(self, x, offsets, rows=None, act: str = "none", y=None, stream=None):
+        return fp8w_gemm_experts(x, self.codes, self.scales, offsets, rows, self.fmt, act, y, stream)
+
+
+# --------------------------------------------------------------- logprobs --
+
+def fp8w_logprobs(logits, targets=None, top: int = 0, logprob=None, entropy=None, top_ids=None, top_logprobs=None,
+                  workspace=None, stream=None) -> Logprobs:
+    """Log probabilities of ``targets`` (i32 [tokens]) under softmax(logits)
+    (bf16 or f32 [tokens, vocab]), the entropy of each row and its ``top``
+    most likely tokens."""
+    torch = _torch()
+    dtype, stride = _logits(logits, "logits")
+    t, v = logits.shape
+    top = int(top)
+    dev, f32 = logits.device, torch.float32
+    if targets is not None:
+        _require(targets, (torch.int32,), "targets", 1)
+        if targets.shape[0] != t:
+            raise ValueError(f"targets: expected shape {(t,)}, got {tuple(targets.shape)}")
+        logprob = _buffer(logprob, (t,), f32, dev, "logprob")
+    elif logprob is not None:
+        raise ValueError("logprob: given without targets")
+    if top < 0:
+        raise Fp8wError(ERR_SHAPE, "fp8w_logprobs")
+    entropy = _buffer(entropy, (t,), f32, dev, "entropy")
+    top_ids = _buffer(top_ids, (t, top), torch.int32, dev, "top_ids")
+    top_logprobs = _buffer(top_logprobs, (t, top), f32, dev, "top_logprobs")
+    if workspace is None:
+        need = int(lib().fp8w_logprobs_workspace_bytes(t, v, top))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib().fp8w_logprobs(
+        logits.data_ptr(), dtype, stride, t, v, None if targets is None else targets.data_ptr(), top,
+        None if logprob is None else logprob.data_ptr(), entropy.data_ptr(), top_ids.data_ptr() if top else None,
+        top_logprobs.data_ptr() if top else None, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _launch_stream(stream, logprob, entropy, top_ids, top_logprobs, workspace)), "fp8w_logprobs")
+    return Logprobs(logprob, entropy, top_ids, top_logprobs)
 
 
 # ----------------------------------------------------------- tagged weight --

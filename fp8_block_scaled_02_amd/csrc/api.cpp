@@ -556,6 +556,149 @@ FP8W_API fp8w_status fp8w_quantize_grouped(const fp8w_quant_plan* plan, void* st
                                                 plan->blocks, plan->format, static_cast<hipStream_t>(stream)));
 }
 
+// ------------------------------------------------------------- experts --
+
+namespace {
+
+// Workgroups of one launch: the runtime counts a grid's threads in 32 bits.
+constexpr int64_t kMaxBlocks256 = 0xFFFFFFFF / 256;
+constexpr int64_t kMaxBlocks512 = 0xFFFFFFFF / 512;
+
+bool dtype_ok(int d) { return d == FP8W_DTYPE_BF16 || d == FP8W_DTYPE_F32; }
+uint64_t dtype_bytes(int d) { return d == FP8W_DTYPE_F32 ? 4 : 2; }
+
+// Bytes that `rows` rows of `cols` elements with a stride of `stride` span.
+uint64_t strided_bytes(int64_t rows, int64_t cols, int64_t stride, uint64_t element) {
+  return rows < 1 ? 0 : ((uint64_t)(rows - 1) * (uint64_t)stride + (uint64_t)cols) * element;
+}
+
+bool route_shape_ok(int64_t tokens, int64_t experts) {
+  return tokens >= 0 && tokens <= 32 * kMaxBlocks512 && experts >= 1 && experts <= FP8W_MAX_EXPERTS;
+}
+
+}  // namespace
+
+FP8W_API int64_t fp8w_route_experts_workspace_bytes(int64_t tokens, int64_t experts) {
+  return route_shape_ok(tokens, experts) ? fp8w::route_workspace_bytes(tokens, experts) : 0;
+}
+
+FP8W_API fp8w_status fp8w_route_experts(const void* logits, fp8w_dtype dtype, int64_t stride, int64_t tokens,
+                                        int64_t experts, int64_t top_k, fp8w_score score, const float* bias,
+                                        int renorm, float scale, int32_t* ids, float* weights, int32_t* slots,
+                                        int32_t* rows, int32_t* offsets, void* workspace,
+                                        int64_t workspace_bytes, void* stream) {
+  if (!offsets || (tokens != 0 && (!logits || !ids || !weights || !slots || !rows))) return FP8W_ERR_NULL;
+  if (!dtype_ok(dtype) || (score != FP8W_SCORE_SOFTMAX && score != FP8W_SCORE_SIGMOID)) return FP8W_ERR_UNSUPPORTED;
+  if (!route_shape_ok(tokens, experts) || top_k < 1 || top_k > experts || top_k > FP8W_MAX_TOP_K ||
+      tokens * top_k > kMaxDim || stride < experts || stride > kMaxDim)
+    return FP8W_ERR_SHAPE;
+  const int64_t need = fp8w::route_workspace_bytes(tokens, experts);
+  if (need > 0 && !workspace) return FP8W_ERR_NULL;
+  if (need > 0 && workspace_bytes < need) return FP8W_ERR_SHAPE;
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(slots, 4) || !aligned(rows, 4) || !aligned(offsets, 4) || (need > 0 && !aligned(workspace, 4)))
+    return FP8W_ERR_ALIGN;
+  const uint64_t pairs = (uint64_t)(tokens * top_k) * 4;
+  const Span out[6] = {{ids, pairs}, {weights, pairs}, {slots, pairs}, {rows, pairs},
+                       {offsets, (uint64_t)(experts + 1) * 4}, {workspace, (uint64_t)need}};
+  const Span in[2] = {{logits, strided_bytes(tokens, experts, stride, dtype_bytes(dtype))},
+                      {bias, bias ? (uint64_t)experts * 4 : 0}};
+  if (any_overlap(out, 6, in, 2)) return FP8W_ERR_OVERLAP;
+  const fp8w::RouteCall c{logits, bias, ids, weights, slots, rows, offsets, workspace, stride, scale,
+                          (int32_t)tokens, (int32_t)experts, (int32_t)top_k, score, renorm ? 1 : 0,
+                          dtype == FP8W_DTYPE_F32};
+  return from_hip(fp8w::launch_route_experts(c, static_cast<hipStream_t>(stream)));
+}
+
+FP8W_API fp8w_status fp8w_gemm_experts(const uint16_t* x, int64_t x_rows, const int32_t* rows,
+                                       const int32_t* offsets, int64_t experts, int64_t slots,
+                                       const uint8_t* codes, const void* scales, fp8w_format format,
+                                       int64_t n, int64_t k, fp8w_act act, uint16_t* y, void* stream) {
+  if (!offsets || !codes || !scales || (slots != 0 && (!x || !y))) return FP8W_ERR_NULL;
+  if (!format_ok(format) || (act != FP8W_ACT_NONE && act != FP8W_ACT_SWIGLU)) return FP8W_ERR_UNSUPPORTED;
+  const bool swiglu = act == FP8W_ACT_SWIGLU;
+  if (!dims_ok(n, k) || k < 16 || experts < 1 || experts > kMaxDim || slots < 0 || slots > kMaxDim ||
+      x_rows < (slots != 0) || x_rows > kMaxDim || (!rows && x_rows < slots) || (swiglu && n % 2 != 0))
+    return FP8W_ERR_SHAPE;
+  if (k % 16 != 0 || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, scale_align(format)) ||
+      !aligned(y, 8) || !aligned(rows, 4) || !aligned(offsets, 4))
+    return FP8W_ERR_ALIGN;
+  if (slots == 0) return FP8W_OK;
+  const int64_t n_out = swiglu ? n / 2 : n;
+  // products of the sizes stay within 64 bits: three factors below 2^31 do not
+  if ((unsigned __int128)experts * (uint64_t)n * (uint64_t)k >> 62) return FP8W_ERR_SHAPE;
+  const uint64_t sb = scale_bytes(format, n, k);
+  const Span out[1] = {{y, (uint64_t)slots * n_out * 2}};
+  const Span in[5] = {{x, (uint64_t)x_rows * k * 2}, {rows, rows ? (uint64_t)slots * 4 : 0},
+                      {offsets, (uint64_t)(experts + 1) * 4}, {codes, (uint64_t)experts * n * k},
+                      {scales, (uint64_t)experts * sb}};
+  if (any_overlap(out, 1, in, 5)) return FP8W_ERR_OVERLAP;
+  const fp8w::ExpertsCall c{x, rows, offsets, codes, scales, y, (int64_t)sb, (int32_t)x_rows, (int32_t)experts,
+                            (int32_t)slots, (int32_t)n, (int32_t)k, format, swiglu ? 1 : 0};
+  if (fp8w::experts_blocks(experts, slots, n, swiglu) > kMaxBlocks256) return FP8W_ERR_SHAPE;
+  return from_hip(fp8w::launch_gemm_experts(c, static_cast<hipStream_t>(stream)));
+}
+
+FP8W_API fp8w_status fp8w_combine_experts(const uint16_t* y, int64_t slot_rows, const float* weights,
+                                          const int32_t* slots, int64_t tokens, int64_t top_k, int64_t n,
+                                          uint16_t* out, void* stream) {
+  if (tokens != 0 && (!weights || !slots || !out || (slot_rows != 0 && !y))) return FP8W_ERR_NULL;
+  if (tokens < 0 || tokens > kMaxDim || slot_rows < 0 || slot_rows > kMaxDim || n < 1 || n > kMaxDim ||
+      top_k < 1 || top_k > FP8W_MAX_TOP_K || tokens * top_k > kMaxDim)
+    return FP8W_ERR_SHAPE;
+  if (!aligned(y, 2) || !aligned(out, 2) || !aligned(weights, 4) || !aligned(slots, 4)) return FP8W_ERR_ALIGN;
+  if (tokens == 0) return FP8W_OK;
+  const Span o[1] = {{out, (uint64_t)tokens * n * 2}};
+  const Span in[3] = {{y, (uint64_t)slot_rows * n * 2}, {weights, (uint64_t)(tokens * top_k) * 4},
+                      {slots, (uint64_t)(tokens * top_k) * 4}};
+  if (any_overlap(o, 1, in, 3)) return FP8W_ERR_OVERLAP;
+  const bool vec = n % 8 == 0 && aligned(y, 16) && aligned(out, 16);
+  if (fp8w::combine_blocks(tokens, n, vec) > kMaxBlocks256) return FP8W_ERR_SHAPE;
+  return from_hip(fp8w::launch_combine_experts(y, slot_rows, weights, slots, tokens, top_k, n, out, vec,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------ logprobs --
+
+namespace {
+
+bool logprobs_shape_ok(int64_t tokens, int64_t vocab, int64_t top) {
+  return tokens >= 0 && tokens <= kMaxDim && vocab >= 1 && vocab <= kMaxDim - 63 && top >= 0 &&
+         top <= FP8W_MAX_TOP && top <= vocab;
+}
+
+}  // namespace
+
+FP8W_API int64_t fp8w_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t top) {
+  return logprobs_shape_ok(tokens, vocab, top) ? fp8w::logprobs_workspace_bytes(tokens, vocab, top) : 0;
+}
+
+FP8W_API fp8w_status fp8w_logprobs(const void* logits, fp8w_dtype dtype, int64_t stride, int64_t tokens,
+                                   int64_t vocab, const int32_t* targets, int64_t top, float* logprob,
+                                   float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  if (tokens != 0 && (!logits || !targets != !logprob || (top != 0 && (!top_ids || !top_logprobs))))
+    return FP8W_ERR_NULL;
+  if (!dtype_ok(dtype)) return FP8W_ERR_UNSUPPORTED;
+  if (!logprobs_shape_ok(tokens, vocab, top) || stride < vocab || stride > kMaxDim) return FP8W_ERR_SHAPE;
+  const int64_t need = fp8w::logprobs_workspace_bytes(tokens, vocab, top);
+  if (need > 0 && !workspace) return FP8W_ERR_NULL;
+  if (need > 0 && workspace_bytes < need) return FP8W_ERR_SHAPE;
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(targets, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
+      !aligned(top_ids, 4) || !aligned(top_logprobs, 4) || (need > 0 && !aligned(workspace, 8)))
+    return FP8W_ERR_ALIGN;
+  if (tokens == 0) return FP8W_OK;
+  const uint64_t row = (uint64_t)tokens * 4;
+  const Span out[5] = {{logprob, logprob ? row : 0}, {entropy, entropy ? row : 0}, {top_ids, row * top},
+                       {top_logprobs, row * top}, {workspace, (uint64_t)need}};
+  const Span in[2] = {{logits, strided_bytes(tokens, vocab, stride, dtype_bytes(dtype))}, {targets, targets ? row : 0}};
+  if (any_overlap(out, 5, in, 2)) return FP8W_ERR_OVERLAP;
+  if (tokens * fp8w::logprobs_segments(tokens, vocab) > kMaxBlocks512) return FP8W_ERR_SHAPE;
+  const fp8w::LogprobsCall c{logits, targets, logprob, entropy, top_ids, top_logprobs, workspace, stride,
+                             (int32_t)tokens, (int32_t)vocab, (int32_t)top, dtype == FP8W_DTYPE_F32};
+  return from_hip(fp8w::launch_logprobs(c, static_cast<hipStream_t>(stream)));
+}
+
 // ------------------------------------------------------------- helpers --
 
 FP8W_API int64_t fp8w_block_scale_count(int64_t n, int64_t k) {

@@ -83,30 +83,6 @@ __device__ __forceinline__ int lane_fresh() {
   return l;
 }
 
-// 2^(e - 127) as an exact fp32: a normal number for e >= 1, the subnormal
-// 2^-127 for e == 0.
-__device__ __forceinline__ float mx_scale(uint8_t e) {
-  return __uint_as_float(e ? (uint32_t)e << 23 : 0x00400000u);
-}
-
-// Two e4m3 codes (bytes 0,1 or 2,3 of d) -> two bf16 (exact).
-__device__ __forceinline__ bf16x2 cvt_lo(uint32_t d) {
-  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, false);
-}
-__device__ __forceinline__ bf16x2 cvt_hi(uint32_t d) {
-  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true);
-}
-
-// Two e4m3 codes times the MX scale s = 2^(E-127), rounded to bf16, in one
-// instruction.  Measured on MI355X over every code and every e8m0 byte
-// 0..254: bit-identical to rounding fp32(code) * s (exact in fp32) to bf16;
-// byte 255, E8M0's NaN, gives NaN where that product would be infinite (a
-// non-finite weight, outside the contract either way).
-template <bool HI>
-__device__ __forceinline__ bf16x2 cvt_scaled(uint32_t d, float s) {
-  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, s, HI);
-}
-
 __device__ __forceinline__ bf16x2 as_bf16x2(uint32_t d) { return __builtin_bit_cast(bf16x2, d); }
 
 // Non-MX scale formats.  The scale of 128-column block kb for the 128-row
@@ -879,24 +855,6 @@ __device__ __forceinline__ void panel_to_a(const uint4 (&v)[4], unsigned char* b
 #pragma unroll
     for (int c = 0; c < 2; ++c)
       a[b][c] = *reinterpret_cast<const uint4*>(buf + i * kPanelCols + 16 * ((8 * b + 4 * c + g) ^ i));
-}
-
-// 16 e4m3 codes -> the two bf16x8 A operands of one 64-column chunk (first
-// and last 8 K positions of each lane's 16), scaled by s for MX.
-template <bool MX>
-__device__ __forceinline__ void a_operands(uint4 d, float s, bf16x8& A0, bf16x8& A1) {
-  bf16x2 a0, a1, a2, a3, b0, b1, b2, b3;
-  if (MX) {
-    a0 = cvt_scaled<false>(d.x, s), a1 = cvt_scaled<true>(d.x, s);
-    a2 = cvt_scaled<false>(d.y, s), a3 = cvt_scaled<true>(d.y, s);
-    b0 = cvt_scaled<false>(d.z, s), b1 = cvt_scaled<true>(d.z, s);
-    b2 = cvt_scaled<false>(d.w, s), b3 = cvt_scaled<true>(d.w, s);
-  } else {
-    a0 = cvt_lo(d.x), a1 = cvt_hi(d.x), a2 = cvt_lo(d.y), a3 = cvt_hi(d.y);
-    b0 = cvt_lo(d.z), b1 = cvt_hi(d.z), b2 = cvt_lo(d.w), b3 = cvt_hi(d.w);
-  }
-  A0 = bf16x8{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
-  A1 = bf16x8{b0[0], b0[1], b1[0], b1[1], b2[0], b2[1], b3[0], b3[1]};
 }
 
 // acc += the panel's products.  get_b(t, b, c, B0, B1) supplies the x^T

@@ -136,4 +136,61 @@ int64_t read_ceiling_blocks(int64_t bytes, int64_t max_blocks);
 hipError_t launch_read_ceiling(const void* buf, int64_t bytes, uint32_t* out, int64_t blocks,
                                hipStream_t stream);
 
+// Expert routing: see route.hip.  `f32` is the logits' type (else bf16).
+struct RouteCall {
+  const void* logits;
+  const float* bias;        // null: the logits decide
+  int32_t* ids;
+  float* weights;
+  int32_t* slots;
+  int32_t* rows;
+  int32_t* offsets;
+  void* workspace;          // route_workspace_bytes
+  int64_t stride;
+  float scale;
+  int32_t tokens, experts, top_k, score, renorm, f32;
+};
+int route_max_experts();
+int route_max_top_k();
+int64_t route_workspace_bytes(int64_t tokens, int64_t experts);
+hipError_t launch_route_experts(const RouteCall& c, hipStream_t stream);
+
+// out[t] = sum_j weights[t][j] * y[slots[t][j]]; vec: n % 8 == 0 and y, out
+// 16-byte aligned.
+int64_t combine_blocks(int64_t tokens, int64_t n, bool vec);
+hipError_t launch_combine_experts(const uint16_t* y, int64_t slot_rows, const float* weights, const int32_t* slots,
+                                  int64_t tokens, int64_t top_k, int64_t n, uint16_t* out, bool vec,
+                                  hipStream_t stream);
+
+// Products grouped by expert: see experts.hip.
+struct ExpertsCall {
+  const uint16_t* x;        // bf16 [x_rows, k]
+  const int32_t* rows;      // [slots], or null: slot i takes row i
+  const int32_t* offsets;   // [experts + 1]
+  const uint8_t* codes;     // e4m3fn [experts, n, k]
+  const void* scales;       // `experts` scale buffers, back to back
+  uint16_t* y;              // bf16 [slots, n] ([slots, n/2] with swiglu)
+  int64_t scale_bytes;      // of one expert
+  int32_t x_rows, experts, slots, n, k, format, swiglu;
+};
+int64_t experts_blocks(int64_t experts, int64_t slots, int64_t n, bool swiglu);
+hipError_t launch_gemm_experts(const ExpertsCall& c, hipStream_t stream);
+
+// Log probabilities: see logprobs.hip.
+struct LogprobsCall {
+  const void* logits;
+  const int32_t* targets;   // null with logprob
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  void* workspace;          // logprobs_workspace_bytes
+  int64_t stride;
+  int32_t tokens, vocab, top, f32;
+};
+int logprobs_max_top();
+int logprobs_segments(int64_t tokens, int64_t vocab);
+int64_t logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t top);
+hipError_t launch_logprobs(const LogprobsCall& c, hipStream_t stream);
+
 }  // namespace fp8w

@@ -1,0 +1,416 @@
+// logprobs.hip -- log probabilities of given tokens, entropy and the top
+// alternatives of rows of logits, in one pass over the row.
+//
+// With m = max x, z = sum 2^((x - m) log2 e) and u = sum of the same terms
+// times their exponents (x - m) log2 e,
+//   log p(i) = (x_i - m) - ln z,      entropy = ln z - ln 2 * u / z.
+// Each thread keeps (m, z, u) of what it has read and moves them to a new
+// maximum once per 16 values; u is taken relative to m, so logits far from
+// zero lose nothing.  A masked logit (-inf) has its exponent clamped at
+// -300, where the term is zero, so 0 * inf never appears.
+//
+// Top alternatives ride on the same pass.  A value and its place make one
+// 64-bit key (the value's ordered bits, then the complement of the place):
+// larger keys are larger values, lower places first among equals, and no
+// two are equal, so any correct selection gives the same answer.  Each wave
+// keeps a list of keys above a threshold that is never above the top-th key
+// of the row: first the top-th largest of its lanes' maxima, then the
+// top-th key of its list whenever that is cut down, shared among the waves.
+// A wave looks at single values only where a lane's maximum reaches the
+// threshold.  Rows are cut into segments where there are too few of them to
+// fill the chip, and a second launch joins the segments.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device.hpp"
+#include "internal.hpp"
+
+namespace fp8w {
+namespace {
+
+constexpr int kLpThreads = 512;
+constexpr int kLpWaves = kLpThreads / kWave;
+constexpr int kLpBlock = 1024;        // values of one wave step: 16 per lane
+constexpr int kLpMaxTop = 64;
+constexpr int kLpCap = 256;           // keys a wave's list holds (4 per lane)
+constexpr int kLpMaxSegs = 64;
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kMinExp = -300.0f;    // 2^-300 is zero in fp32
+
+// Value bits whose unsigned order is the values' order (-0 equal to +0).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b ^ (uint32_t)(((int32_t)b >> 31) | 0x80000000);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+constexpr uint64_t kFirstKey = (uint64_t)(0x007FFFFFu + 1) << 32;   // above every key of -inf
+
+struct LpStats {
+  float m, z, u;
+};
+
+__device__ __forceinline__ LpStats lp_join(LpStats a, LpStats b) {
+  const float m = __builtin_elementwise_maximum(a.m, b.m);   // NaN stays
+  const float da = __builtin_fmaxf((a.m - m) * kLog2E, kMinExp), db = __builtin_fmaxf((b.m - m) * kLog2E, kMinExp);
+  const float fa = __builtin_amdgcn_exp2f(da), fb = __builtin_amdgcn_exp2f(db);
+  return LpStats{m, a.z * fa + b.z * fb, fa * __builtin_fmaf(da, a.z, a.u) + fb * __builtin_fmaf(db, b.z, b.u)};
+}
+
+struct LpArgs {
+  const void* logits;
+  const int32_t* targets;    // may be null (with logprob)
+  float* logprob;            // may be null
+  float* entropy;            // may be null
+  int32_t* top_ids;
+  float* top_logprobs;
+  LpStats* seg_stats;        // [tokens][segs], segs > 1
+  uint64_t* seg_keys;        // [tokens][segs][top]
+  int64_t stride;            // elements
+  int32_t tokens, vocab, top, segs, seg_values;
+};
+
+// What a row's statistics give; the row holding NaN or +inf has no
+// distribution and gets NaN, the row masked throughout log p = -inf and
+// entropy 0.
+struct LpRow {
+  float m, ln_z;
+  bool bad, empty;
+  __device__ __forceinline__ explicit LpRow(const LpStats& s) {
+    m = s.m;
+    bad = !(s.m < __builtin_inff());
+    empty = s.m == -__builtin_inff();
+    ln_z = __builtin_amdgcn_logf(s.z) * kLn2;
+  }
+  __device__ __forceinline__ float logp(float x) const {
+    if (bad) return __builtin_nanf("");
+    if (empty) return -__builtin_inff();
+    return (x - m) - ln_z;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float lp_load(const void* p, int64_t at) {
+  if constexpr (sizeof(T) == 4) return ld_global<float>(p, (size_t)at * 4);
+  return bf16_lo(ld_global<uint16_t>(p, (size_t)at * 2));
+}
+
+// Target, entropy and top alternatives of row t from its statistics and the
+// `count` keys of its candidates (every live logit, if fewer than top), by
+// the whole workgroup.  `keys` holds 64-bit words in LDS.
+template <typename T>
+__device__ __forceinline__ void lp_finish(const LpArgs& a, int t, const LpStats& s, const uint64_t* keys, int count) {
+  const LpRow row(s);
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    if (a.entropy)
+      a.entropy[t] = row.bad ? __builtin_nanf("") : row.empty ? 0.0f : row.ln_z - kLn2 * (s.u / s.z);
+    if (a.logprob) {
+      const int id = a.targets[t];
+      a.logprob[t] = id >= 0 && id < a.vocab ? row.logp(lp_load<T>(a.logits, (int64_t)t * a.stride + id))
+                                             : __builtin_nanf("");
+    }
+  }
+  for (int i = tid; i < count; i += blockDim.x) {
+    const uint64_t key = keys[i];
+    int rank = 0;
+    for (int j = 0; j < count; ++j) rank += keys[j] > key ? 1 : 0;
+    if (rank < a.top) {
+      const int64_t at = (int64_t)t * a.top + rank;
+      a.top_ids[at] = (int32_t)~(uint32_t)key;
+      a.top_logprobs[at] = row.logp(unordered((uint32_t)(key >> 32)));
+    }
+  }
+  // Fewer live logits than alternatives: the rest are masked tokens, lowest first.
+  if (count < a.top && tid == 0) {
+    int filled = count;
+    for (int id = 0; filled < a.top; ++id) {
+      bool live = false;
+      for (int j = 0; j < count; ++j) live |= (int32_t)~(uint32_t)keys[j] == id;
+      if (!live) {
+        const int64_t at = (int64_t)t * a.top + filled++;
+        a.top_ids[at] = id;
+        a.top_logprobs[at] = row.logp(-__builtin_inff());
+      }
+    }
+  }
+}
+
+// The largest threshold that at least `want` of the wave's keys reach (or 0
+// if there are fewer), stopping as soon as exactly that many do.  Keys: PER
+// a lane.
+template <typename K, int PER>
+__device__ __forceinline__ K wave_threshold(const K (&key)[PER], int want) {
+  K thr = 0;
+  for (int bit = 8 * (int)sizeof(K) - 1; bit >= 0; --bit) {
+    const K cand = thr | ((K)1 << bit);
+    int reach = 0;
+#pragma unroll
+    for (int r = 0; r < PER; ++r) reach += __builtin_popcountll(__ballot(key[r] >= cand));
+    if (reach >= want) {
+      thr = cand;
+      if (reach == want) break;
+    }
+  }
+  return thr;
+}
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// A wave's list of candidates.
+struct LpList {
+  uint64_t* keys;              // LDS, kLpCap words of this wave
+  uint64_t* shared_tau;        // LDS, of the workgroup
+  uint64_t tau;                // keys below it cannot be in the answer
+  int count;
+
+  // Cut the list down to its top `top` keys.
+  __device__ __forceinline__ void cut(int top) {
+    const int lane = threadIdx.x & (kWave - 1);
+    uint64_t k[kLpCap / kWave];
+#pragma unroll
+    for (int r = 0; r < kLpCap / kWave; ++r) k[r] = r * kWave + lane < count ? keys[r * kWave + lane] : 0;
+    const uint64_t thr = wave_threshold(k, top);
+    int kept = 0;
+#pragma unroll
+    for (int r = 0; r < kLpCap / kWave; ++r) {
+      const bool keep = k[r] >= thr && k[r] != 0;
+      const uint64_t who = __ballot(keep);
+      if (keep) keys[kept + __builtin_popcountll(who & ((1ull << lane) - 1))] = k[r];
+      kept += __builtin_popcountll(who);
+    }
+    __builtin_amdgcn_wave_barrier();
+    count = kept;
+    raise(thr);
+  }
+  __device__ __forceinline__ void raise(uint64_t t) {
+    if (t > tau) {
+      tau = t;
+      if ((threadIdx.x & (kWave - 1)) == 0) atomicMax(reinterpret_cast<unsigned long long*>(shared_tau), (unsigned long long)t);
+    }
+  }
+  __device__ __forceinline__ void add(bool want, uint64_t key, int top) {
+    const uint64_t who = __ballot(want);
+    if (!who) return;
+    if (count > kLpCap - kWave) {
+      cut(top);
+      want = want && key >= tau;
+    }
+    const uint64_t now = __ballot(want);
+    const int lane = threadIdx.x & (kWave - 1);
+    if (want) keys[count + __builtin_popcountll(now & ((1ull << lane) - 1))] = key;
+    __builtin_amdgcn_wave_barrier();
+    count += __builtin_popcountll(now);
+  }
+};
+
+// One workgroup per row segment.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kLpThreads) void k_logprobs(LpArgs a) {
+  constexpr int kVec = 16 / sizeof(T);       // values of one 16-byte load
+  constexpr int kLoads = 16 / kVec;
+  __shared__ uint64_t lists[TOP ? kLpWaves * kLpCap : 1];
+  __shared__ uint64_t shared_tau;
+  __shared__ LpStats wave_stats[kLpWaves];
+  __shared__ int kept;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs;
+  if (tid == 0) {
+    shared_tau = kFirstKey;
+    kept = 0;
+  }
+  __syncthreads();
+
+  // Places are counted from the 16-byte boundary at or below the row's
+  // start, so that every load of whole 16 bytes is aligned; `skew` values
+  // there belong to what lies before the row and are never read.
+  const char* row = static_cast<const char*>(a.logits) + (size_t)t * a.stride * sizeof(T);
+  const int skew = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const char* base = row - skew * sizeof(T);
+  const int64_t end = (int64_t)a.vocab + skew;
+  const int64_t lo = (int64_t)seg * a.seg_values;
+  const int64_t hi = lo + a.seg_values < end && seg + 1 < a.segs ? lo + a.seg_values : end;
+
+  LpStats s{-__builtin_inff(), 0.0f, 0.0f};
+  LpList list{lists + wave * kLpCap, &shared_tau, kFirstKey, 0};
+  bool first = true;
+  for (int64_t at = lo + wave * kLpBlock; at < hi; at += kLpWaves * kLpBlock) {
+    float x[16];
+#pragma unroll
+    for (int v = 0; v < kLoads; ++v) {
+      const int64_t p = at + (v * kWave + lane) * kVec;
+      if (p >= skew && p + kVec <= hi) {
+        const uint4 d = ld_stream_u4(base, (size_t)p * sizeof(T));
+        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 2) {
+            x[v * kVec + 2 * i] = bf16_lo(w[i]);
+            x[v * kVec + 2 * i + 1] = bf16_hi(w[i]);
+          } else {
+            x[v * kVec + i] = __uint_as_float(w[i]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          x[v * kVec + i] = p + i >= skew && p + i < hi ? lp_load<T>(base, p + i) : -__builtin_inff();
+      }
+    }
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = __builtin_elementwise_maximum(top, x[i]);
+    const float m = __builtin_elementwise_maximum(s.m, top);
+    const float down = __builtin_fmaxf((s.m - m) * kLog2E, kMinExp), f = __builtin_amdgcn_exp2f(down);
+    float z = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float e = __builtin_fmaxf((x[i] - m) * kLog2E, kMinExp);   // the difference first: m log2 e can overflow
+      const float p = __builtin_amdgcn_exp2f(e);
+      z += p;
+      u = __builtin_fmaf(e, p, u);
+    }
+    s = LpStats{m, __builtin_fmaf(s.z, f, z), __builtin_fmaf(f, __builtin_fmaf(down, s.z, s.u), u)};
+
+    if constexpr (TOP) {
+      const uint32_t mine = top == top ? ordered(top) : 0;
+      if (first) {
+        first = false;
+        const uint32_t k[1] = {mine};
+        list.raise((uint64_t)wave_threshold(k, a.top) << 32);
+      }
+      const uint64_t seen = uniform64(*(volatile uint64_t*)&shared_tau);
+      if (seen > list.tau) list.tau = seen;
+      if (__ballot(mine >= (uint32_t)(list.tau >> 32))) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int64_t p = at + ((i / kVec) * kWave + lane) * kVec + i % kVec;
+          const uint64_t key = ((uint64_t)ordered(x[i]) << 32) | (uint32_t)~(uint32_t)(p - skew);
+          list.add(x[i] == x[i] && key >= list.tau, key, a.top);
+        }
+      }
+    }
+  }
+
+  // The wave's statistics, then the workgroup's.
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const LpStats o{__shfl_xor(s.m, off), __shfl_xor(s.z, off), __shfl_xor(s.u, off)};
+    s = lp_join(s, o);
+  }
+  if (lane == 0) wave_stats[wave] = s;
+  if constexpr (TOP) {
+    if (list.count > a.top) list.cut(a.top);   // at most 64: one key a lane
+  }
+  __syncthreads();
+  s = wave_stats[0];
+#pragma unroll
+  for (int w = 1; w < kLpWaves; ++w) s = lp_join(s, wave_stats[w]);
+  int count = 0;
+  uint64_t* joined = lists;
+  if constexpr (TOP) {
+    const uint64_t key = lane < list.count ? list.keys[lane] : 0;
+    const bool keep = key >= shared_tau;
+    __syncthreads();
+    if (keep) joined[atomicAdd(&kept, 1)] = key;
+    __syncthreads();
+    count = kept;
+  }
+  if (a.segs == 1) {
+    lp_finish<T>(a, t, s, joined, count);
+    return;
+  }
+  const size_t cell = (size_t)blockIdx.x;
+  if (tid == 0) a.seg_stats[cell] = s;
+  if constexpr (TOP) {
+    uint64_t* out = a.seg_keys + cell * a.top;
+    for (int i = tid; i < count; i += kLpThreads) {
+      const uint64_t key = joined[i];
+      int rank = 0;
+      for (int j = 0; j < count; ++j) rank += joined[j] > key ? 1 : 0;
+      if (rank < a.top) out[rank] = key;
+    }
+    for (int i = count + tid; i < a.top; i += kLpThreads) out[i] = 0;
+  }
+}
+
+// Segments of a row joined, one workgroup per row.
+template <typename T>
+__global__ __launch_bounds__(256) void k_logprobs_join(LpArgs a) {
+  __shared__ uint64_t keys[kLpMaxSegs * kLpMaxTop];
+  __shared__ int kept;
+  const int t = blockIdx.x, tid = threadIdx.x;
+  if (tid == 0) kept = 0;
+  __syncthreads();
+  const LpStats* st = a.seg_stats + (size_t)t * a.segs;
+  LpStats s = st[0];
+  for (int i = 1; i < a.segs; ++i) s = lp_join(s, st[i]);
+  if (a.top > 0) {
+    const uint64_t* k = a.seg_keys + (size_t)t * a.segs * a.top;
+    uint64_t tau = 1;                       // a segment's last key is no larger than the row's
+    for (int i = 0; i < a.segs; ++i) {
+      const uint64_t last = k[(size_t)i * a.top + a.top - 1];
+      tau = last > tau ? last : tau;
+    }
+    for (int i = tid; i < a.segs * a.top; i += 256)
+      if (k[i] >= tau) keys[atomicAdd(&kept, 1)] = k[i];
+  }
+  __syncthreads();
+  lp_finish<T>(a, t, s, keys, kept);
+}
+
+template <typename T>
+hipError_t lp_launch(const LpArgs& a, hipStream_t stream) {
+  const unsigned blocks = (unsigned)((int64_t)a.tokens * a.segs);
+  if (a.top > 0)
+    k_logprobs<T, true><<<blocks, kLpThreads, 0, stream>>>(a);
+  else
+    k_logprobs<T, false><<<blocks, kLpThreads, 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.segs == 1) return e;
+  k_logprobs_join<T><<<a.tokens, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+// Values of a segment: whole steps of all the workgroup's waves.
+constexpr int64_t kLpSegUnit = kLpBlock * kLpWaves;
+
+}  // namespace
+
+int logprobs_max_top() { return kLpMaxTop; }
+
+int logprobs_segments(int64_t tokens, int64_t vocab) {
+  if (tokens < 1) return 1;
+  const int64_t units = (vocab + 7 + kLpSegUnit - 1) / kLpSegUnit;
+  int64_t want = (512 + tokens - 1) / tokens;
+  if (want > units) want = units;
+  if (want > kLpMaxSegs) want = kLpMaxSegs;
+  if (want <= 1) return 1;
+  const int64_t per = (units + want - 1) / want;
+  return (int)((units + per - 1) / per);
+}
+
+int64_t logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t top) {
+  const int64_t segs = logprobs_segments(tokens, vocab);
+  return segs <= 1 ? 0 : tokens * segs * (8 * top + (int64_t)sizeof(LpStats));
+}
+
+hipError_t launch_logprobs(const LogprobsCall& c, hipStream_t stream) {
+  const int segs = logprobs_segments(c.tokens, c.vocab);
+  const int64_t units = (c.vocab + 7 + kLpSegUnit - 1) / kLpSegUnit;
+  const int64_t per = (units + segs - 1) / segs * kLpSegUnit;
+  LpArgs a{c.logits, c.targets, c.logprob, c.entropy, c.top_ids, c.top_logprobs, nullptr, nullptr, c.stride,
+           c.tokens, c.vocab, c.top, segs, segs == 1 ? 0 : (int32_t)per};
+  if (segs > 1) {   // the keys first: 8-byte words
+    a.seg_keys = static_cast<uint64_t*>(c.workspace);
+    a.seg_stats = reinterpret_cast<LpStats*>(a.seg_keys + (size_t)c.tokens * segs * c.top);
+  }
+  return c.f32 ? lp_launch<float>(a, stream) : lp_launch<uint16_t>(a, stream);
+}
+
+}  // namespace fp8w

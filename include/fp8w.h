@@ -12,6 +12,16 @@
  *               activations (fp8 x fp8 matrix-core products)
  *   GEMM        the same product for any m, through dequantize + a dense
  *               bf16 GEMM (the large-M / prefill route)
+ * the operators that a mixture-of-experts layer and a scored answer put
+ * around those products:
+ *
+ *   routing     router logits -> the experts of each token, their weights,
+ *               and the tokens sorted by expert
+ *   experts     products grouped by expert with ragged sizes, plain or with
+ *               a gated SiLU, and the weighted sum of a token's experts
+ *   logprobs    lm_head logits -> log probability of given tokens, entropy,
+ *               top alternatives
+ *
  * and a measurement aid: a read-only pass over device memory with the
  * GEMV's loads (fp8w_read_ceiling).
  *
@@ -474,6 +484,137 @@ fp8w_status fp8w_quant_plan_init(const fp8w_quant_desc* descs, int64_t count, fp
  * graph; the buffers the descriptors named must still be live.
  * Errors: NULL, SHAPE (a plan not produced by fp8w_quant_plan_init), HIP. */
 fp8w_status fp8w_quantize_grouped(const fp8w_quant_plan* plan, void* stream);
+
+/* ------------------------------------------------------------- experts -- */
+
+/* Type of a logits buffer. */
+typedef enum fp8w_dtype {
+  FP8W_DTYPE_BF16 = 0,
+  FP8W_DTYPE_F32 = 1
+} fp8w_dtype;
+
+/* What turns a router's logit into a score. */
+typedef enum fp8w_score {
+  FP8W_SCORE_SOFTMAX = 0,     /* exp(l - max) / sum over the experts */
+  FP8W_SCORE_SIGMOID = 1      /* 1 / (1 + exp(-l))                   */
+} fp8w_score;
+
+/* What the grouped products write. */
+typedef enum fp8w_act {
+  FP8W_ACT_NONE = 0,
+  FP8W_ACT_SWIGLU = 1         /* silu(g) * u of W's two halves of rows */
+} fp8w_act;
+
+/* Largest number of experts and of choices a token (fp8w_route_experts,
+ * fp8w_combine_experts). */
+#define FP8W_MAX_EXPERTS 1024
+#define FP8W_MAX_TOP_K 64
+
+/* A router's choice, and the tokens sorted by it.
+ *   logits  : bf16 or f32 [tokens, experts], row stride `stride` elements   input
+ *   bias    : f32 [experts] or NULL                                        input
+ *   ids     : i32 [tokens, top_k]  experts of each token, best first       output
+ *   weights : f32 [tokens, top_k]                                          output
+ *   slots   : i32 [tokens, top_k]  place of (token, choice) in the order   output
+ *   rows    : i32 [tokens * top_k] token of each slot                      output
+ *   offsets : i32 [experts + 1]    expert e's slots: offsets[e] up to
+ *                                  offsets[e + 1]                          output
+ * A token's experts are those of the largest logits or, with a bias, of the
+ * largest score + bias (computed in fp64), ties to the lower index.  The
+ * weight is the score without the bias, over the sum of the chosen scores if
+ * `renorm`, times `scale`, in fp32.  Slots are sorted by expert, then by
+ * token.  An expert whose logit is -inf or NaN is never chosen: a token with
+ * fewer than top_k others has id -1, weight 0 and slot -1 for what is
+ * missing, and rows past offsets[experts] are -1.  Logits of +inf give
+ * unspecified weights.
+ * workspace: fp8w_route_experts_workspace_bytes(tokens, experts) bytes
+ * (0 up to 32 tokens), 4-byte aligned.  tokens may be 0 (offsets are then
+ * all 0 and the other buffers are not touched).  One launch up to 32 tokens,
+ * two above.  Requires 1 <= experts <= 1024, 1 <= top_k <= min(experts, 64),
+ * stride >= experts, tokens * top_k <= 2^31 - 1.
+ * Errors: NULL, SHAPE (also: workspace too small), UNSUPPORTED (dtype,
+ * score), ALIGN, OVERLAP, HIP. */
+int64_t fp8w_route_experts_workspace_bytes(int64_t tokens, int64_t experts);
+fp8w_status fp8w_route_experts(const void* logits, fp8w_dtype dtype, int64_t stride, int64_t tokens,
+                               int64_t experts, int64_t top_k, fp8w_score score, const float* bias,
+                               int renorm, float scale, int32_t* ids, float* weights, int32_t* slots,
+                               int32_t* rows, int32_t* offsets, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* Products grouped by expert.  For every slot i of expert e, offsets[e] <= i
+ * < offsets[e + 1]:
+ *   y[i] = x[rows[i]] . deq(W_e)^T                     act NONE,   [slots, n]
+ *   y[i] = silu(g) * u, g and u the products with W_e's
+ *          rows 0..n/2 and n/2..n                      act SWIGLU, [slots, n/2]
+ * fp32 accumulation, rounded to bf16 once at the end.
+ *   x       : bf16 [x_rows, k], 16-byte aligned               input
+ *   rows    : i32 [slots] or NULL (slot i takes x's row i)    input
+ *   offsets : i32 [experts + 1], ascending                    input
+ *   codes   : u8 [experts, n, k], 16-byte aligned             input
+ *   scales  : `experts` scale buffers of [n, k] in `format`, each of
+ *             fp8w_scale_bytes(format, n, k) bytes, back to back   input
+ *   y       : bf16, 8-byte aligned                            output
+ * The groups' sizes are read on the device, any split of any part of the
+ * slots: an expert may have none, and slots outside [offsets[0],
+ * offsets[experts]) are not written.  rows and offsets that point outside
+ * their ranges are not followed: a slot of such a row gets the products of a
+ * row of zeros, offsets are cut to [0, slots].
+ * Each product meets the bound of fp8w_gemv (|y - y_ref| <= 2^-7 * sum |x|
+ * |deq| + 1e-6).
+ * Requires k >= 16, k % 16 == 0, n >= 1 (SWIGLU: n even), slots >= 0 (0: no
+ * launch), experts >= 1, x_rows >= 1 (x_rows >= slots without rows).
+ * Errors: NULL, SHAPE, UNSUPPORTED (format, act), ALIGN, OVERLAP, HIP. */
+fp8w_status fp8w_gemm_experts(const uint16_t* x, int64_t x_rows, const int32_t* rows,
+                              const int32_t* offsets, int64_t experts, int64_t slots,
+                              const uint8_t* codes, const void* scales, fp8w_format format,
+                              int64_t n, int64_t k, fp8w_act act, uint16_t* y, void* stream);
+
+/* The weighted sum of each token's experts:
+ *   out[t] = bf16_rne( sum_j weights[t][j] * y[slots[t][j]] ), fp32, j ascending.
+ *   y       : bf16 [slot_rows, n]          input
+ *   weights : f32 [tokens, top_k]          input
+ *   slots   : i32 [tokens, top_k]          input
+ *   out     : bf16 [tokens, n]             output
+ * A slot outside [0, slot_rows) (a choice that was not made) adds nothing,
+ * whatever its weight.  tokens may be 0.  16-byte loads where n % 8 == 0 and
+ * y and out are 16-byte aligned.  Requires n >= 1, 1 <= top_k <= 64.
+ * Errors: NULL, SHAPE, ALIGN, OVERLAP, HIP. */
+fp8w_status fp8w_combine_experts(const uint16_t* y, int64_t slot_rows, const float* weights,
+                                 const int32_t* slots, int64_t tokens, int64_t top_k, int64_t n,
+                                 uint16_t* out, void* stream);
+
+/* ------------------------------------------------------------ logprobs -- */
+
+/* Largest number of alternatives a row. */
+#define FP8W_MAX_TOP 64
+
+/* Log probabilities of given tokens under softmax(logits), with the
+ * entropy and the `top` most likely alternatives of each row.
+ *   logits       : bf16 or f32 [tokens, vocab], row stride `stride` elements  input
+ *   targets      : i32 [tokens] or NULL                                      input
+ *   logprob      : f32 [tokens], NULL exactly when targets is                output
+ *   entropy      : f32 [tokens] or NULL, in nats                             output
+ *   top_ids      : i32 [tokens, top], most likely first, ties to the lower
+ *                  token (NULL when top is 0)                                output
+ *   top_logprobs : f32 [tokens, top] (NULL when top is 0)                    output
+ * fp32 throughout.  Masked tokens (-inf) have log probability -inf and add
+ * nothing to the entropy; as alternatives they come last, lowest first.  A
+ * row masked throughout has log probability -inf everywhere and entropy 0.
+ * A row that holds NaN or +inf has NaN for its log probabilities and
+ * entropy (NaN ranks with the masked).  A target outside [0, vocab) gives
+ * NaN and is not followed.
+ * workspace: fp8w_logprobs_workspace_bytes(tokens, vocab, top) bytes, 8-byte
+ * aligned (0 where there are enough rows to fill the chip: one launch; else
+ * rows are cut into segments and a second launch joins them).  tokens may be
+ * 0.  Requires 1 <= vocab <= 2^31 - 64, 0 <= top <= min(vocab, 64),
+ * stride >= vocab.
+ * Errors: NULL, SHAPE (also: workspace too small), UNSUPPORTED (dtype),
+ * ALIGN, OVERLAP, HIP. */
+int64_t fp8w_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t top);
+fp8w_status fp8w_logprobs(const void* logits, fp8w_dtype dtype, int64_t stride, int64_t tokens,
+                          int64_t vocab, const int32_t* targets, int64_t top, float* logprob,
+                          float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
+                          int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------- helpers -- */
 
