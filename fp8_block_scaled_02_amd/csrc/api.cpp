@@ -635,7 +635,7 @@ FP8W_API fp8w_status fp8w_gemm_experts(const uint16_t* x, int64_t x_rows, const 
   if (any_overlap(out, 1, in, 5)) return FP8W_ERR_OVERLAP;
   const fp8w::ExpertsCall c{x, rows, offsets, codes, scales, y, (int64_t)sb, (int32_t)x_rows, (int32_t)experts,
                             (int32_t)slots, (int32_t)n, (int32_t)k, format, swiglu ? 1 : 0};
-  if (fp8w::experts_blocks(experts, slots, n, swiglu, format) > kMaxBlocks256) return FP8W_ERR_SHAPE;
+  if (fp8w::experts_blocks(experts, slots, n, k, swiglu, format) > kMaxBlocks256) return FP8W_ERR_SHAPE;
   return from_hip(fp8w::launch_gemm_experts(c, static_cast<hipStream_t>(stream)));
 }
 

@@ -67,6 +67,12 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
+// Two fp32 -> two bf16, a in the low half, by the hardware conversion (round
+// to nearest even, NaN stays NaN).
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
 // e4m3fn codes by the hardware conversion (v_cvt_pk_fp8_f32: round to
 // nearest even, OCP e4m3fn on gfx950, sign kept, -0 -> 0x80) after clamping
 // to [-448, 448], which is the saturation.  Measured on MI355X over every

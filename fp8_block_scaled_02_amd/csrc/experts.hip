@@ -9,6 +9,9 @@
 // synchronization): every workgroup finds its expert in the offsets.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
+
+#include <type_traits>
 
 #include "device.hpp"
 #include "internal.hpp"
@@ -16,90 +19,105 @@
 namespace fp8w {
 namespace {
 
-// A run of at most `height` slots of one expert.
-struct ExpertTile {
-  int expert;   // -1: past the last tile
-  int slot0, count;
-};
-
-// Tile `index` of all experts' runs of `height` slots, in expert order.  The
-// offsets are kept inside [0, slots], so what a wrong offset names is still
-// in bounds.  By a whole wave; the answer is the same in every lane.
-__device__ __forceinline__ ExpertTile expert_tile(const int32_t* offsets, int experts, int slots, int height, int index) {
-  const int lane = threadIdx.x & (kWave - 1);
-  int before = 0;
-  for (int e0 = 0; e0 < experts; e0 += kWave) {
-    const int e = e0 + lane;
-    int from = 0, to = 0;
-    if (e < experts) {
-      from = min(max(ld_global<int32_t>(offsets, (size_t)e * 4), 0), slots);
-      to = min(max(ld_global<int32_t>(offsets, (size_t)e * 4 + 4), 0), slots);
-    }
-    const int tiles = to > from ? (to - from + height - 1) / height : 0;
-    int upto = tiles;
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const int up = __shfl_up(upto, off);
-      if (lane >= off) upto += up;
-    }
-    const int first = before + upto - tiles;
-    const uint64_t mine = __ballot(index >= first && index < first + tiles);
-    if (mine) {
-      const int l = __builtin_ctzll(mine);
-      const int slot0 = from + (index - first) * height;
-      ExpertTile t;
-      t.expert = e0 + l;
-      t.slot0 = __builtin_amdgcn_readlane(slot0, l);
-      t.count = __builtin_amdgcn_readlane(min(height, to - slot0), l);
-      return t;
-    }
-    before += __builtin_amdgcn_readlane(upto, kWave - 1);
-  }
-  return ExpertTile{-1, 0, 0};
-}
-
-// A workgroup's tile: `group` of n_groups along n, a run of slots of one
-// expert.  Workgroups go round the 8 XCDs in turn, and each XCD has its own
-// L2: it gets one contiguous eighth of the tiles, in which a run's groups
-// follow one another, so that an expert's weights and rows are read by one
-// XCD, or two.
+// A workgroup's tile: a run of at most `height` slots of one expert, and
+// `group` of the n_groups along n.
 struct TileAt {
-  int expert, slot0, count, group;
+  int expert;   // -1: no tile is left for this workgroup
+  int slot0, count, group;
 };
-__device__ __forceinline__ int count_tiles(const int32_t* offsets, int experts, int slots, int height) {
-  const int lane = threadIdx.x & (kWave - 1);
-  int mine = 0;
-  for (int e = lane; e < experts; e += kWave) {
-    const int from = min(max(ld_global<int32_t>(offsets, (size_t)e * 4), 0), slots);
-    const int to = min(max(ld_global<int32_t>(offsets, (size_t)e * 4 + 4), 0), slots);
-    mine += to > from ? (to - from + height - 1) / height : 0;
-  }
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) mine += __shfl_xor(mine, off);
-  return __builtin_amdgcn_readfirstlane(mine);
-}
-__device__ __forceinline__ TileAt tile_at(const int32_t* offsets, int experts, int slots, int height, int n_groups) {
-  const int64_t tiles = (int64_t)count_tiles(offsets, experts, slots, height) * n_groups;
-  const int64_t share = (tiles + 7) / 8;
-  const int64_t place = blockIdx.x >> 3, id = (blockIdx.x & 7) * share + place;
-  if (place >= share || id >= tiles) return TileAt{-1, 0, 0, 0};
-  const int run = (int)(id / n_groups);
-  const ExpertTile t = expert_tile(offsets, experts, slots, height, run);
-  return TileAt{t.expert, t.slot0, t.count, (int)(id - (int64_t)run * n_groups)};
+
+// Inclusive sums over the wave: sums along each row of 16 lanes by lane
+// shifts, then the rows' totals by lane reads.
+__device__ __forceinline__ int wave_prefix(int v) {
+#define FP8W_ROW_SHR_ADD(n) v += __builtin_amdgcn_update_dpp(0, v, 0x110 + (n), 0xF, 0xF, false)
+  FP8W_ROW_SHR_ADD(1);
+  FP8W_ROW_SHR_ADD(2);
+  FP8W_ROW_SHR_ADD(4);
+  FP8W_ROW_SHR_ADD(8);
+#undef FP8W_ROW_SHR_ADD
+  const int a = __builtin_amdgcn_readlane(v, 15), b = __builtin_amdgcn_readlane(v, 31), c = __builtin_amdgcn_readlane(v, 47);
+  const int row = (threadIdx.x & (kWave - 1)) >> 4;
+  return v + (row > 0 ? a : 0) + (row > 1 ? b : 0) + (row > 2 ? c : 0);
 }
 
-__device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// This workgroup's tile, found by each of its waves (the answer is the same
+// in every lane).  The experts' runs follow one another, each in n_groups
+// tiles.  The offsets are kept inside [0, slots], so that what a wrong offset
+// names is still in bounds.
+//
+// Workgroups go round the 8 XCDs in turn, and each XCD has its own L2: it
+// gets one contiguous eighth of the tiles, so that an expert's weights and
+// rows are read by one XCD, or two.  That takes the number of tiles, so all
+// offsets are read: 256 experts a pass, every load of a pass at once.
+__device__ __forceinline__ TileAt tile_at(const int32_t* offsets, int experts, int slots, int height, int n_groups) {
+  constexpr int kPass = 4;
+  const int lane = threadIdx.x & (kWave - 1);
+  int from[kPass], tiles[kPass], upto[kPass], last[kPass];
+  const auto pass = [&](int e0, int before) {   // runs of the pass's experts; the runs up to its end
+#pragma unroll
+    for (int r = 0; r < kPass; ++r) {
+      const int e = e0 + r * kWave + lane;
+      from[r] = ld_global<int32_t>(offsets, (size_t)min(e, experts) * 4);
+      last[r] = ld_global<int32_t>(offsets, (size_t)min(e + 1, experts) * 4);
+    }
+#pragma unroll
+    for (int r = 0; r < kPass; ++r) {
+      from[r] = min(max(from[r], 0), slots);
+      last[r] = min(max(last[r], 0), slots);
+      tiles[r] = last[r] > from[r] ? (last[r] - from[r] + height - 1) / height : 0;
+      upto[r] = wave_prefix(tiles[r]) + before;
+      before = __builtin_amdgcn_readlane(upto[r], kWave - 1);
+    }
+    return before;
+  };
+  int total = 0;
+  for (int e0 = 0; e0 < experts; e0 += kPass * kWave) total = pass(e0, total);
+  const int64_t share = ((int64_t)total * n_groups + 7) / 8;
+  const int64_t place = blockIdx.x >> 3, id = (blockIdx.x & 7) * share + place;
+  if (place >= share || id >= (int64_t)total * n_groups) return TileAt{-1, 0, 0, 0};
+  const int run = (int)((uint32_t)id / (uint32_t)n_groups);
+  TileAt t{-1, 0, 0, (int)((uint32_t)id - (uint32_t)run * (uint32_t)n_groups)};
+  int before = 0;
+  for (int e0 = 0; e0 < experts && t.expert < 0; e0 += kPass * kWave) {
+    if (experts > kPass * kWave) before = pass(e0, before);
+#pragma unroll
+    for (int r = 0; r < kPass; ++r) {
+      const int first = upto[r] - tiles[r];
+      const uint64_t mine = __ballot(run >= first && run < upto[r]);
+      if (mine) {
+        const int l = __builtin_ctzll(mine);
+        const int slot0 = from[r] + (run - first) * height;
+        t.expert = e0 + r * kWave + l;
+        t.slot0 = __builtin_amdgcn_readlane(slot0, l);
+        t.count = __builtin_amdgcn_readlane(min(height, last[r] - slot0), l);
+      }
+    }
+  }
+  return t;
+}
+
+// silu(g) * u within a few units of the last place of fp32: exp(-g) as 2^t
+// times a first-order correction for what rounding t = -g log2 e lost, and
+// the hardware reciprocal (an IEEE division of every output cost as many
+// instructions as a third of the products at k = 2048).
+__device__ __forceinline__ float silu_times(float g, float u) {
+  constexpr float kLog2E = 0x1.715476p+0f, kLog2ELow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float a = -__builtin_fmaxf(g, -200.0f);   // beyond, 2^t is infinite and the result zero
+  const float t = a * kLog2E;
+  const float lost = __builtin_fmaf(a, kLog2ELow, __builtin_fmaf(a, kLog2E, -t));
+  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(lost, kLn2, 1.0f);
+  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
 
 // The simple kernel: one wave takes 16 weight rows (with SWIGLU 16 of each
 // half) against 16 slots, operands straight from memory.
 template <bool SWIGLU>
 __global__ __launch_bounds__(256) void k_experts_simple(ExpertsCall c, int n_groups) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int group = blockIdx.x % n_groups;
-  const ExpertTile tile = expert_tile(c.offsets, c.experts, c.slots, 16, blockIdx.x / n_groups);
+  const TileAt tile = tile_at(c.offsets, c.experts, c.slots, 16, n_groups);
   if (tile.expert < 0) return;
   const int n_out = SWIGLU ? c.n / 2 : c.n;
-  const int n0 = (group * 4 + wave) * 16;
+  const int n0 = (tile.group * 4 + wave) * 16;
   if (n0 >= n_out) return;
   const int i = lane & 15, g = lane >> 4;
   const int slot = tile.slot0 + min(i, tile.count - 1);
@@ -162,181 +180,321 @@ __global__ __launch_bounds__(256) void k_experts_simple(ExpertsCall c, int n_gro
   }
 }
 
-// The tiled kernel: 256 weight rows against 16 * MT slots of one expert.
+// The lane index, recomputed at every call (an opaque v_mbcnt pair), so that
+// nothing derived from it is kept in registers from one use to the next.
+__device__ __forceinline__ int lane_fresh() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
+}
+
+// 16 bytes a lane from memory to LDS at `to` + 16 * lane (`to` uniform).
+__device__ __forceinline__ void stage16(const void* from, unsigned char* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+// s_waitcnt vmcnt(n) lgkmcnt(0), n < 64, then the workgroup's barrier.  The
+// LDS reads before it have returned, so that what they read may be
+// overwritten after it; and all but the wave's last n loads have landed.
+template <int N>
+__device__ __forceinline__ void land_and_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// These 16 values are computed here, not where the compiler would rather.
+__device__ __forceinline__ void settle(float (&v)[16]) {
+  asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7]),
+               "+v"(v[8]), "+v"(v[9]), "+v"(v[10]), "+v"(v[11]), "+v"(v[12]), "+v"(v[13]), "+v"(v[14]), "+v"(v[15]));
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32_unaligned __attribute__((aligned(1)));
+
+// The wide kernel: 256 weight rows against 32 * MT slots of one expert on
+// the 32x32x16 MFMA, four waves of 64 rows (SWIGLU: 32 of each half), two
+// workgroups a CU.
 //
-// Four waves take 64 weight rows each (SWIGLU: 32 of each half) against all
-// the slots, so a wave's weights belong to it alone: they go from memory to
-// its registers in the MFMA A layout (a lane holds row l%16, bytes 16(l/16)
-// of each 64) one 128-column block ahead, and become bf16 there once for all
-// slot tiles.  x is staged in LDS, two buffers, in 16-byte units XOR-swizzled
-// by row % 16, so that both the writes and the B operand reads spread over
-// the banks; one barrier a block.  Block scales multiply the fp32 sums of
-// each 128-column block, MX scales the codes as they become bf16 (exact).
+// Everything reaches LDS by loads that write it directly, in whole 128-byte
+// lines (in the MFMA A layout a load instruction would touch 64 bytes of 16
+// rows or 32 of 32, which took as long as the products themselves).
+//   * Weights: a wave's 64 rows of a 128-column block are its own 8 KB.  At
+//     the start of a block it takes them into registers in the A layout and
+//     asks for the next block at once: a block's time to arrive.
+//   * x: 64 columns of the slots for all four waves, three buffers, asked
+//     for two steps ahead; one barrier a step.
+// The waits name how many younger loads may still be on their way; a wait
+// for everything would put the memory's latency into every step.
+//
+// A lane's 16 bytes of codes are two MFMA steps of 8 columns each, so step
+// (p, s) takes columns 32p + 16(l/32) + 8s of the step, for weights and x
+// alike.  LDS rows are 128 bytes, their 16-byte units XOR-swizzled by row / 2,
+// so that any 16 consecutive rows fall into 16 different bank groups.
+//
+// A block scale multiplies its sums every 64 columns (a full block's sums
+// would need as many registers as the accumulators); MX scales multiply the
+// codes as they become bf16 (exact); row and tensor scales the results.
 template <int FMT, bool SWIGLU, int MT>
-__global__ __launch_bounds__(256, MT > 4 ? 1 : 2) void k_experts_tile(ExpertsCall c, int n_groups) {
+__global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_groups) {
   constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
   constexpr bool kMx = FMT == kFmtMx;
-  constexpr int kSlots = 16 * MT;
-  __shared__ __attribute__((aligned(16))) unsigned char xs[2][kSlots * 256];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int i = lane & 15, g = lane >> 4;
+  constexpr int kSlots = 32 * MT;
+  constexpr int kXLoads = MT;          // x loads of a wave and step (1 KB each)
+  // separate arrays: the compiler then knows that reads of one need not wait
+  // for what is on its way into another
+  __shared__ __attribute__((aligned(16))) unsigned char ws[4 * 64 * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs0[kSlots * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs1[kSlots * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs2[kSlots * 128];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int i = lane & 31, hh = lane >> 5;
   const TileAt at = tile_at(c.offsets, c.experts, c.slots, kSlots, n_groups);
   if (at.expert < 0) return;
   const int n_out = SWIGLU ? c.n / 2 : c.n;
   const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32;
 
-  // weight row of 16-row tile t that lane i loads, cut to the last row
   const int n0 = at.group * (SWIGLU ? 128 : 256) + wave * (SWIGLU ? 32 : 64);
   const uint8_t* codes = c.codes + (size_t)at.expert * c.n * k;
   const char* scales = static_cast<const char*>(c.scales) + (size_t)at.expert * c.scale_bytes;
-  const auto out_row = [&](int t) { return n0 + 16 * (SWIGLU ? t & 1 : t); };
-  const auto half = [&](int t) { return SWIGLU && t >= 2 ? n_out : 0; };
-  const uint8_t* wp[4];
-  const char* sp[4];
+  // 32-row tile t of the wave: outputs from out_row(t), weight rows half(t) on
+  const auto out_row = [&](int t) { return n0 + (SWIGLU ? 0 : 32 * t); };
+  const auto half = [&](int t) { return SWIGLU && t == 1 ? n_out : 0; };
+  unsigned char* wl = ws + wave * 64 * 128;
+
+  // Load j of a wave's weights brings rows 8j + l/8; LDS place l%8 of a row
+  // holds its unit (l%8) ^ (row / 2 % 8), so j odd the unit of j even ^ 4.
+  // Offsets pass through empty asm statements where they are used, and the
+  // uncommon path starts from a fresh lane index: combined addresses of every
+  // load would otherwise be kept in registers for the whole kernel.
+  const bool whole_rows = n0 + (SWIGLU ? 32 : 64) <= n_out;
+  const int wu = (lane & 7) ^ (lane >> 4);
+  uint32_t wlane[2] = {(uint32_t)(lane >> 3) * (uint32_t)k + 16 * wu, (uint32_t)(lane >> 3) * (uint32_t)k + 16 * (wu ^ 4)};
+  const auto request_w = [&](int kb) {
+    asm volatile("" : "+v"(wlane[0]), "+v"(wlane[1])::"memory");
+    if (whole_rows && kb * 128 + 128 <= k) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int row = min(out_row(t) + i, n_out - 1) + half(t);
-    wp[t] = codes + (size_t)row * k + 16 * g;
-    if (kMx) sp[t] = scales + (size_t)row * ng;
-    // a lane's four sums are rows 4g.. of the tile: one scale block (the
-    // halves start on a multiple of 4)
-    if (kBlock) sp[t] = scales + (size_t)((min(out_row(t) + 4 * g, n_out - 1) + half(t)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t* from = codes + (size_t)(out_row(j >> 2) + 8 * (j & 3) + half(j >> 2)) * k + kb * 128;
+        stage16(from + wlane[j & 1], wl + j * 1024);
+      }
+    } else {
+      const int l = lane_fresh();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {   // rows past the end: the last one; columns past it: column 0
+        const int row = min(out_row(j >> 2) + 8 * (j & 3) + (l >> 3), n_out - 1) + half(j >> 2);
+        const int col = kb * 128 + 16 * ((l & 7) ^ (l >> 4) ^ (j & 1) * 4);
+        stage16(codes + (size_t)row * k + (col < k ? col : 0), wl + j * 1024);
+      }
+    }
+    asm volatile("" ::: "memory");
+  };
+  // x rows a wave stages: 8 (MT * wave + j) + l/8, the same places (row / 2 % 8
+  // = 4 (row / 8 % 2) + l/16)
+  const char* xp[kXLoads];
+#pragma unroll
+  for (int j = 0; j < kXLoads; ++j) {
+    const int slot = at.slot0 + min(8 * (kXLoads * wave + j) + (lane >> 3), at.count - 1);
+    const int row = c.rows ? ld_global<int32_t>(c.rows, (size_t)slot * 4) : slot;
+    xp[j] = reinterpret_cast<const char*>(c.x + (size_t)(row >= 0 && row < c.x_rows ? row : 0) * k) +
+            16 * (wu ^ ((kXLoads * wave + j) & 1) * 4);
   }
-  // x rows this thread stages: slot 16q + tid/16, unit tid%16
-  const uint16_t* xp[MT];
+  const auto request_x = [&](int step, unsigned char* to) {
+    asm volatile("" ::: "memory");
+    if (step * 64 + 64 <= k) {
+#pragma unroll
+      for (int j = 0; j < kXLoads; ++j) stage16(xp[j] + (size_t)step * 128, to + (kXLoads * wave + j) * 1024);
+    } else {
+      const int l = lane_fresh();
+#pragma unroll
+      for (int j = 0; j < kXLoads; ++j) {
+        const int unit = (l & 7) ^ (l >> 4) ^ ((kXLoads * wave + j) & 1) * 4;
+        stage16(xp[j] + (step * 64 + 8 * unit < k ? step * 128 : -16 * unit), to + (kXLoads * wave + j) * 1024);
+      }
+    }
+    asm volatile("" ::: "memory");
+  };
+  // whether the slots a lane will store, 32q + i, have a row of x
+  uint32_t live = 0;
 #pragma unroll
   for (int q = 0; q < MT; ++q) {
-    const int slot = at.slot0 + min(16 * q + tid / 16, at.count - 1);
+    const int slot = at.slot0 + min(32 * q + i, at.count - 1);
     const int row = c.rows ? ld_global<int32_t>(c.rows, (size_t)slot * 4) : slot;
-    xp[q] = c.x + (size_t)(row >= 0 && row < c.x_rows ? row : 0) * k + 8 * (tid & 15);
+    live |= row >= 0 && row < c.x_rows ? 1u << q : 0u;
   }
 
-  uint4 wr[4][2], xr[MT];
-  float sc[4];
-  uint8_t ex[4][2];
-  const auto request = [&](int kb) {
-    const bool whole = kb * 128 + 128 <= k;
+  // scales of the next block: a float a tile (32 rows lie in one scale
+  // block; scalar loads), or the lane's row's four MX exponents
+  const char* sp[2];
+  float sc[2] = {1.0f, 1.0f};
+  uint32_t ex[2] = {0, 0};
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < 2; ++t) {
+    if (kBlock) sp[t] = scales + (size_t)((min(out_row(t), n_out - 1) + half(t)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
+    if (kMx) sp[t] = scales + (size_t)(min(out_row(t) + i, n_out - 1) + half(t)) * ng;
+  }
+  const auto request_s = [&](int kb) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (whole || kb * 128 + 64 * h + 16 * g < k)
-          wr[t][h] = ld_global_u4(wp[t], (size_t)kb * 128 + 64 * h);
-        else
-          wr[t][h] = make_uint4(0, 0, 0, 0);
-        if (kMx) ex[t][h] = ld_global<uint8_t>(sp[t], (size_t)min(4 * kb + 2 * h + (g >> 1), ng - 1));
-      }
-      if (FMT == kFmtBlock) sc[t] = ld_global<float>(sp[t], (size_t)kb * 4);
-      if (FMT == kFmtBlockBf16) sc[t] = bf16_lo(ld_global<uint16_t>(sp[t], (size_t)kb * 2));
-    }
-#pragma unroll
-    for (int q = 0; q < MT; ++q) {
-      if (whole || kb * 128 + 8 * (tid & 15) < k)
-        xr[q] = ld_global_u4(xp[q], (size_t)kb * 256);
-      else
-        xr[q] = make_uint4(0, 0, 0, 0);
+    for (int t = 0; t < 2; ++t) {
+      if (FMT == kFmtBlock) sc[t] = reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(sp[t]))[kb];
+      if (FMT == kFmtBlockBf16)
+        sc[t] = bf16_lo(reinterpret_cast<const __attribute__((address_space(4))) uint16_t*>(reinterpret_cast<uintptr_t>(sp[t]))[kb]);
+      // four bytes that end with the row's last, where the block has fewer
+      if (kMx) ex[t] = ld_global<u32_unaligned>(sp[t], (size_t)min(4 * kb, ng - 4));
     }
   };
-  const auto stage = [&](int buf) {
+
+  // the sums: single registers where scales are applied to them, else the
+  // MFMA's own
+  std::conditional_t<kBlock, float[16], f32x16> acc[2][MT];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int q = 0; q < MT; ++q)
-      *reinterpret_cast<uint4*>(&xs[buf][(16 * q + tid / 16) * 256 + 16 * ((tid & 15) ^ (tid / 16))]) = xr[q];
-  };
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[t][q][v] = 0.0f;
 
-  f32x4 acc[4][MT];
+  uint4 wr[2][4];                  // tile, 32-column pair of the block
+  float s[2] = {1.0f, 1.0f};
+  uint32_t e[2] = {0, 0};
+  const auto take_w = [&](int kb) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int q = 0; q < MT; ++q) acc[t][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  request(0);
-  stage(0);
-  __syncthreads();
-#pragma unroll 1
-  for (int kb = 0; kb < nkb; ++kb) {
-    bf16x8 a[4][4];
-    float s[4];
+      for (int p = 0; p < 4; ++p)
+        wr[t][p] = *reinterpret_cast<const uint4*>(&wl[(32 * t + i) * 128 + 16 * ((2 * p + hh) ^ (i >> 1 & 7))]);
+    if (kb * 128 + 128 > k) {
+      const int from = kb * 128 + 16 * (lane_fresh() >> 5);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      s[t] = kBlock ? sc[t] : 1.0f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        a_operands<kMx>(wr[t][h], kMx ? mx_scale(ex[t][h]) : 1.0f, a[t][2 * h], a[t][2 * h + 1]);
+      for (int p = 0; p < 4; ++p)
+        if (from + 32 * p >= k) wr[0][p] = wr[1][p] = make_uint4(0, 0, 0, 0);
     }
-    if (kb + 1 < nkb) request(kb + 1);
-    const unsigned char* xb = xs[kb & 1];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      s[t] = sc[t];
+      e[t] = kMx ? ex[t] >> 8 * (4 * kb - min(4 * kb, ng - 4)) : 0;
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0): the codes are in registers
+    const int next = kb + 1 < nkb ? kb + 1 : 0;   // the last block asks for one nobody takes
+    request_s(next);
+    request_w(next);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // 64 columns.  Scaled sums are settled after every 32 slots: left alone
+  // the compiler starts all products first, each with sums of its own, and
+  // spills.
+  const auto step = [&](int h, const unsigned char* xb) {
+    bf16x8 a[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        a_operands<kMx>(wr[t][2 * h + p], kMx ? mx_scale((uint8_t)(e[t] >> 8 * (2 * h + p))) : 1.0f, a[t][2 * p], a[t][2 * p + 1]);
 #pragma unroll
     for (int q = 0; q < MT; ++q) {
       bf16x8 b[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        b[u] = *reinterpret_cast<const bf16x8*>(&xb[(16 * q + i) * 256 + 16 * ((8 * (u >> 1) + 2 * g + (u & 1)) ^ i)]);
-      f32x4 part[4];
+        b[u] = *reinterpret_cast<const bf16x8*>(&xb[(32 * q + i) * 128 + 16 * ((4 * (u >> 1) + 2 * hh + (u & 1)) ^ (i >> 1 & 7))]);
+      f32x16 part[2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) part[t] = kBlock ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t][q];
+      for (int t = 0; t < 2; ++t) {
+        if constexpr (kBlock) {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) part[t][v] = 0.0f;
+        } else {
+          part[t] = acc[t][q];
+        }
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][u], b[u], part[t], 0, 0, 0);
+        for (int t = 0; t < 2; ++t) part[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[t][u], b[u], part[t], 0, 0, 0);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (kBlock) {
+      for (int t = 0; t < 2; ++t) {
+        if constexpr (kBlock) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[t][q][v] = __builtin_fmaf(s[t], part[t][v], acc[t][q][v]);
+          for (int v = 0; v < 16; ++v) acc[t][q][v] = __builtin_fmaf(s[t], part[t][v], acc[t][q][v]);
+          settle(acc[t][q]);
         } else {
           acc[t][q] = part[t];
         }
       }
+      if (kBlock) __builtin_amdgcn_sched_barrier(0);
     }
-    if (kb + 1 < nkb) {
-      stage((kb + 1) & 1);
-      __syncthreads();
-    }
-  }
+  };
+  // A block of 128 columns: x steps 2kb and 2kb + 1 are in x0 and x1, and
+  // the two after them go to x2 and x0.
+  const auto block = [&](int kb, unsigned char* x0, unsigned char* x1, unsigned char* x2) {
+    take_w(kb);
+    request_x(2 * kb + 2 < 2 * nkb ? 2 * kb + 2 : 0, x2);
+    step(0, x0);
+    land_and_meet<8 + kXLoads>();                 // younger than x1's: weights and x2's
+    request_x(2 * kb + 3 < 2 * nkb ? 2 * kb + 3 : 0, x0);
+    step(1, x1);
+    land_and_meet<kXLoads>();                     // the weights and x2's have landed
+  };
 
-  // rows 4g .. 4g + 3 of each tile, for slot 16q + l%16
-  float os[4][4];
-  if (FMT == kFmtRow) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        os[t][v] = ld_global<float>(scales, (size_t)(min(out_row(t) + 4 * g + v, n_out - 1) + half(t)) * 4);
+  request_s(0);
+  request_w(0);
+  request_x(0, xs0);
+  request_x(1, xs1);
+  land_and_meet<kXLoads>();
+  int kb = 0;
+#pragma unroll 1
+  for (; kb + 2 < nkb; kb += 3) {
+    block(kb, xs0, xs1, xs2);
+    block(kb + 1, xs2, xs0, xs1);
+    block(kb + 2, xs1, xs2, xs0);
   }
+  if (kb < nkb) block(kb, xs0, xs1, xs2);
+  if (kb + 1 < nkb) block(kb + 1, xs2, xs0, xs1);
+  vm_wait_all();   // nothing may land in LDS that is no longer ours
+
   const float whole_scale = FMT == kFmtTensor ? ld_global<float>(scales, 0) : 1.0f;
 #pragma unroll
-  for (int q = 0; q < MT; ++q) {
-    if (16 * q + i >= at.count) continue;
-    const int slot = at.slot0 + 16 * q + i;
-    bool live = true;
-    if (c.rows) {
-      const int row = ld_global<int32_t>(c.rows, (size_t)slot * 4);
-      live = row >= 0 && row < c.x_rows;   // else the products of zeros
-    }
+  for (int v4 = 0; v4 < 4; ++v4) {
+    // rows 8 v4 + 4 (l / 32) .. + 3 of each tile
+    float os[2][4];
+    if (FMT == kFmtRow) {
 #pragma unroll
-    for (int t = 0; t < (SWIGLU ? 2 : 4); ++t) {
-      const int n = out_row(t) + 4 * g;
-      uint32_t r[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        float o = acc[t][q][v];
-        if (FMT == kFmtRow) o *= os[t][v];
-        if (FMT == kFmtTensor) o *= whole_scale;
-        if (SWIGLU) {
-          float u = acc[(t + 2) & 3][q][v];
-          if (FMT == kFmtRow) u *= os[(t + 2) & 3][v];
-          if (FMT == kFmtTensor) u *= whole_scale;
-          o = silu_times(o, u);
-        }
-        r[v] = live ? f32_to_bf16_rne(o) : 0;
-      }
-      const size_t to = ((size_t)slot * n_out + n) * 2;
-      if (n_out % 4 == 0) {
-        if (n < n_out) st_global<u32x2>(c.y, to, u32x2{r[0] | (r[1] << 16), r[2] | (r[3] << 16)});
-      } else {
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          if (n + v < n_out) st_global<uint16_t>(c.y, to + 2 * v, (uint16_t)r[v]);
+          os[t][v] = ld_global<float>(scales, (size_t)(min(out_row(t) + 8 * v4 + 4 * hh + v, n_out - 1) + half(t)) * 4);
+    }
+#pragma unroll
+    for (int q = 0; q < MT; ++q) {
+      if (32 * q + i >= at.count) continue;
+      const int slot = at.slot0 + 32 * q + i;
+#pragma unroll
+      for (int t = 0; t < (SWIGLU ? 1 : 2); ++t) {
+        const int n = out_row(t) + 8 * v4 + 4 * hh;
+        float r[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float o = acc[t][q][4 * v4 + v];
+          if (FMT == kFmtRow) o *= os[t][v];
+          if (FMT == kFmtTensor) o *= whole_scale;
+          if (SWIGLU) {
+            float u = acc[1][q][4 * v4 + v];
+            if (FMT == kFmtRow) u *= os[1][v];
+            if (FMT == kFmtTensor) u *= whole_scale;
+            o = silu_times(o, u);
+          }
+          r[v] = live >> q & 1 ? o : 0.0f;   // else the products of zeros
+        }
+        const size_t to = ((size_t)slot * n_out + n) * 2;
+        if (n_out % 4 == 0) {
+          if (n < n_out) st_global<u32x2>(c.y, to, u32x2{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])});
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (n + v < n_out) st_global<uint16_t>(c.y, to + 2 * v, (uint16_t)bf16_pair(r[v], 0.0f));
+        }
       }
     }
   }
@@ -353,53 +511,60 @@ int64_t max_tiles(int64_t slots, int64_t experts, int64_t height) {
 
 namespace {
 
-// The kernel of a call, by its sizes.  Slot tiles of 16 * mt, or 0 for the
-// simple kernel: halves that do not start on a multiple of 4 rows would put
-// a lane's four sums in two scale blocks.
-int experts_mt(int64_t experts, int64_t slots, int64_t n, bool swiglu, int format) {
+// The kernel of a call, by its sizes.
+struct ExpertsPlan {
+  int height;   // slots of a run; 16: the simple kernel
+  int width;    // outputs of a group
+};
+
+// Halves that do not start on a multiple of 32 rows would put a wide tile's
+// rows in two scale blocks, and rows of fewer than four MX exponents cannot
+// be read four at a time: the simple kernel.  Otherwise the run's height
+// goes by the rows an expert has on average.
+ExpertsPlan experts_plan(int64_t experts, int64_t slots, int64_t n, int64_t k, bool swiglu, int format) {
   const bool block = format == kFmtBlock || format == kFmtBlockBf16;
-  if (swiglu && block && (n / 2) % 4 != 0) return 0;
   const int64_t average = slots / (experts < slots ? experts : slots);
-  return average >= 96 ? 8 : average >= 40 ? 4 : average >= 12 ? 2 : 1;
+  if ((swiglu && block && (n / 2) % 32 != 0) || (format == kFmtMx && k <= 96)) return {16, 64};
+  return {getenv("WMT") ? 32 * atoi(getenv("WMT")) : average >= 128 ? 128 : average >= 48 ? 64 : 32, swiglu ? 128 : 256};
 }
 
-int64_t experts_groups(int mt, int64_t n, bool swiglu) {
-  const int64_t n_out = swiglu ? n / 2 : n, width = mt == 0 ? 64 : swiglu ? 128 : 256;
-  return (n_out + width - 1) / width;
+int64_t experts_groups(const ExpertsPlan& p, int64_t n, bool swiglu) {
+  return ((swiglu ? n / 2 : n) + p.width - 1) / p.width;
 }
 
 template <int FMT, bool SWIGLU>
-void launch_tile(const ExpertsCall& c, int mt, unsigned blocks, int groups, hipStream_t stream) {
-  switch (mt) {
-    case 8: k_experts_tile<FMT, SWIGLU, 8><<<blocks, 256, 0, stream>>>(c, groups); break;
-    case 4: k_experts_tile<FMT, SWIGLU, 4><<<blocks, 256, 0, stream>>>(c, groups); break;
-    case 2: k_experts_tile<FMT, SWIGLU, 2><<<blocks, 256, 0, stream>>>(c, groups); break;
-    default: k_experts_tile<FMT, SWIGLU, 1><<<blocks, 256, 0, stream>>>(c, groups); break;
+void launch_plan(const ExpertsCall& c, const ExpertsPlan& p, unsigned blocks, int groups, hipStream_t stream) {
+  switch (p.height) {
+    case 128: k_experts_wide<FMT, SWIGLU, 4><<<blocks, 256, 0, stream>>>(c, groups); break;
+    case 64: k_experts_wide<FMT, SWIGLU, 2><<<blocks, 256, 0, stream>>>(c, groups); break;
+    default: k_experts_wide<FMT, SWIGLU, 1><<<blocks, 256, 0, stream>>>(c, groups); break;
   }
 }
 
 template <int FMT>
-void launch_act(const ExpertsCall& c, int mt, unsigned blocks, int groups, hipStream_t stream) {
+void launch_act(const ExpertsCall& c, const ExpertsPlan& p, unsigned blocks, int groups, hipStream_t stream) {
   if (c.swiglu)
-    launch_tile<FMT, true>(c, mt, blocks, groups, stream);
+    launch_plan<FMT, true>(c, p, blocks, groups, stream);
   else
-    launch_tile<FMT, false>(c, mt, blocks, groups, stream);
+    launch_plan<FMT, false>(c, p, blocks, groups, stream);
+}
+
+// Workgroups of one launch, a multiple of 8 (a share for every XCD).
+int64_t plan_blocks(const ExpertsPlan& p, int64_t experts, int64_t slots, int64_t n, bool swiglu) {
+  return (max_tiles(slots, experts, p.height) * experts_groups(p, n, swiglu) + 7) / 8 * 8;
 }
 
 }  // namespace
 
-// Workgroups of one launch, a multiple of 8 (a share for every XCD).
-int64_t experts_blocks(int64_t experts, int64_t slots, int64_t n, bool swiglu, int format) {
-  const int mt = experts_mt(experts, slots, n, swiglu, format);
-  const int64_t tiles = max_tiles(slots, experts, mt == 0 ? 16 : 16 * mt) * experts_groups(mt, n, swiglu);
-  return (tiles + 7) / 8 * 8;
+int64_t experts_blocks(int64_t experts, int64_t slots, int64_t n, int64_t k, bool swiglu, int format) {
+  return plan_blocks(experts_plan(experts, slots, n, k, swiglu, format), experts, slots, n, swiglu);
 }
 
 hipError_t launch_gemm_experts(const ExpertsCall& c, hipStream_t stream) {
-  const int mt = experts_mt(c.experts, c.slots, c.n, c.swiglu, c.format);
-  const int groups = (int)experts_groups(mt, c.n, c.swiglu);
-  const unsigned blocks = (unsigned)experts_blocks(c.experts, c.slots, c.n, c.swiglu, c.format);
-  if (mt == 0) {
+  const ExpertsPlan p = experts_plan(c.experts, c.slots, c.n, c.k, c.swiglu, c.format);
+  const int groups = (int)experts_groups(p, c.n, c.swiglu);
+  const unsigned blocks = (unsigned)plan_blocks(p, c.experts, c.slots, c.n, c.swiglu);
+  if (p.height == 16) {
     if (c.swiglu)
       k_experts_simple<true><<<blocks, 256, 0, stream>>>(c, groups);
     else
@@ -407,11 +572,11 @@ hipError_t launch_gemm_experts(const ExpertsCall& c, hipStream_t stream) {
     return hipGetLastError();
   }
   switch (c.format) {
-    case kFmtBlock: launch_act<kFmtBlock>(c, mt, blocks, groups, stream); break;
-    case kFmtMx: launch_act<kFmtMx>(c, mt, blocks, groups, stream); break;
-    case kFmtBlockBf16: launch_act<kFmtBlockBf16>(c, mt, blocks, groups, stream); break;
-    case kFmtRow: launch_act<kFmtRow>(c, mt, blocks, groups, stream); break;
-    default: launch_act<kFmtTensor>(c, mt, blocks, groups, stream); break;
+    case kFmtBlock: launch_act<kFmtBlock>(c, p, blocks, groups, stream); break;
+    case kFmtMx: launch_act<kFmtMx>(c, p, blocks, groups, stream); break;
+    case kFmtBlockBf16: launch_act<kFmtBlockBf16>(c, p, blocks, groups, stream); break;
+    case kFmtRow: launch_act<kFmtRow>(c, p, blocks, groups, stream); break;
+    default: launch_act<kFmtTensor>(c, p, blocks, groups, stream); break;
   }
   return hipGetLastError();
 }

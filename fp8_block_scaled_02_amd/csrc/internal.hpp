@@ -173,7 +173,7 @@ struct ExpertsCall {
   int64_t scale_bytes;      // of one expert
   int32_t x_rows, experts, slots, n, k, format, swiglu;
 };
-int64_t experts_blocks(int64_t experts, int64_t slots, int64_t n, bool swiglu, int format);
+int64_t experts_blocks(int64_t experts, int64_t slots, int64_t n, int64_t k, bool swiglu, int format);
 hipError_t launch_gemm_experts(const ExpertsCall& c, hipStream_t stream);
 
 // Log probabilities: see logprobs.hip.

@@ -386,7 +386,7 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* y, int64_t slot
   if constexpr (VEC == 8) {
     u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f32_to_bf16_rne(acc[2 * i]) | (f32_to_bf16_rne(acc[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) v[i] = bf16_pair(acc[2 * i], acc[2 * i + 1]);
     st_global<u32x4>(out, to, v);
   } else {
     st_global<uint16_t>(out, to, (uint16_t)f32_to_bf16_rne(acc[0]));
