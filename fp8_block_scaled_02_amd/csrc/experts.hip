@@ -266,53 +266,44 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
 
   // Load j of a wave's weights brings rows 8j + l/8; LDS place l%8 of a row
   // holds its unit (l%8) ^ (row / 2 % 8), so j odd the unit of j even ^ 4.
-  // Offsets pass through empty asm statements where they are used, and the
-  // uncommon path starts from a fresh lane index: combined addresses of every
-  // load would otherwise be kept in registers for the whole kernel.
-  const bool whole_rows = n0 + (SWIGLU ? 32 : 64) <= n_out;
+  // Rows past the end are the last one, columns past it column 0 (whose
+  // products the zeroed weights of take_w drop).  No branches: a load that
+  // two paths share is one the compiler takes to write any of the arrays.
+  // Offsets pass through an empty asm statement where they are used: the
+  // addresses of all loads would otherwise be kept in registers throughout.
   const int wu = (lane & 7) ^ (lane >> 4);
-  uint32_t wlane[2] = {(uint32_t)(lane >> 3) * (uint32_t)k + 16 * wu, (uint32_t)(lane >> 3) * (uint32_t)k + 16 * (wu ^ 4)};
-  const auto request_w = [&](int kb) {
-    asm volatile("" : "+v"(wlane[0]), "+v"(wlane[1])::"memory");
-    if (whole_rows && kb * 128 + 128 <= k) {
+  uint32_t wrow = (uint32_t)(lane >> 3) * (uint32_t)k;
+  int wcol = 16 * wu;
+  const auto request_w = [&](int kb) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(wrow), "+v"(wcol)::"memory");
+    const int c0 = kb * 128 + wcol, c1 = kb * 128 + (wcol ^ 64);
+    const uint32_t col[2] = {(uint32_t)(c0 < k ? c0 : 0), (uint32_t)(c1 < k ? c1 : 0)};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint8_t* from = codes + (size_t)(out_row(j >> 2) + 8 * (j & 3) + half(j >> 2)) * k + kb * 128;
-        stage16(from + wlane[j & 1], wl + j * 1024);
-      }
-    } else {
-      const int l = lane_fresh();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {   // rows past the end: the last one; columns past it: column 0
-        const int row = min(out_row(j >> 2) + 8 * (j & 3) + (l >> 3), n_out - 1) + half(j >> 2);
-        const int col = kb * 128 + 16 * ((l & 7) ^ (l >> 4) ^ (j & 1) * 4);
-        stage16(codes + (size_t)row * k + (col < k ? col : 0), wl + j * 1024);
-      }
+    for (int j = 0; j < 8; ++j) {
+      const int row = min(out_row(j >> 2) + 8 * (j & 3), n_out - 1);
+      const uint32_t within = (uint32_t)min(n_out - 1 - row, 7) * (uint32_t)k;
+      stage16(codes + (size_t)(row + half(j >> 2)) * k + (min(wrow, within) + col[j & 1]), wl + j * 1024);
     }
     asm volatile("" ::: "memory");
   };
   // x rows a wave stages: 8 (MT * wave + j) + l/8, the same places (row / 2 % 8
   // = 4 (row / 8 % 2) + l/16)
-  const char* xp[kXLoads];
+  uint32_t xrow[kXLoads];
 #pragma unroll
   for (int j = 0; j < kXLoads; ++j) {
     const int slot = at.slot0 + min(8 * (kXLoads * wave + j) + (lane >> 3), at.count - 1);
     const int row = c.rows ? ld_global<int32_t>(c.rows, (size_t)slot * 4) : slot;
-    xp[j] = reinterpret_cast<const char*>(c.x + (size_t)(row >= 0 && row < c.x_rows ? row : 0) * k) +
-            16 * (wu ^ ((kXLoads * wave + j) & 1) * 4);
+    xrow[j] = row >= 0 && row < c.x_rows ? row : 0;
   }
-  const auto request_x = [&](int step, unsigned char* to) {
-    asm volatile("" ::: "memory");
-    if (step * 64 + 64 <= k) {
+  int xcol = 8 * (wu ^ (kXLoads * wave & 1) * 4);
+  const auto request_x = [&](int step, unsigned char* to) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(xcol)::"memory");
+    const int c0 = step * 64 + xcol, c1 = step * 64 + (xcol ^ 32);
+    const uint32_t col[2] = {(uint32_t)(c0 < k ? 2 * c0 : 0), (uint32_t)(c1 < k ? 2 * c1 : 0)};
 #pragma unroll
-      for (int j = 0; j < kXLoads; ++j) stage16(xp[j] + (size_t)step * 128, to + (kXLoads * wave + j) * 1024);
-    } else {
-      const int l = lane_fresh();
-#pragma unroll
-      for (int j = 0; j < kXLoads; ++j) {
-        const int unit = (l & 7) ^ (l >> 4) ^ ((kXLoads * wave + j) & 1) * 4;
-        stage16(xp[j] + (step * 64 + 8 * unit < k ? step * 128 : -16 * unit), to + (kXLoads * wave + j) * 1024);
-      }
+    for (int j = 0; j < kXLoads; ++j) {
+      asm volatile("" : "+v"(xrow[j]));
+      stage16(reinterpret_cast<const char*>(c.x) + ((uint64_t)xrow[j] * (uint32_t)(2 * k) + col[j & 1]), to + (kXLoads * wave + j) * 1024);
     }
     asm volatile("" ::: "memory");
   };
@@ -335,7 +326,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
     if (kBlock) sp[t] = scales + (size_t)((min(out_row(t), n_out - 1) + half(t)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
     if (kMx) sp[t] = scales + (size_t)(min(out_row(t) + i, n_out - 1) + half(t)) * ng;
   }
-  const auto request_s = [&](int kb) {
+  const auto request_s = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (FMT == kFmtBlock) sc[t] = reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(sp[t]))[kb];
@@ -359,7 +350,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
   uint4 wr[2][4];                  // tile, 32-column pair of the block
   float s[2] = {1.0f, 1.0f};
   uint32_t e[2] = {0, 0};
-  const auto take_w = [&](int kb) {
+  const auto take_w = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -386,19 +377,23 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
   // 64 columns.  Scaled sums are settled after every 32 slots: left alone
   // the compiler starts all products first, each with sums of its own, and
   // spills.
-  const auto step = [&](int h, const unsigned char* xb) {
-    bf16x8 a[2][4];
+  const auto step = [&](int h, const unsigned char* xb) __attribute__((always_inline)) {
+    const auto read_b = [&](int q, int u) __attribute__((always_inline)) {
+      return *reinterpret_cast<const bf16x8*>(&xb[(32 * q + i) * 128 + 16 * ((4 * (u >> 1) + 2 * hh + (u & 1)) ^ (i >> 1 & 7))]);
+    };
+    bf16x8 a[2][4], b[4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int u = 0; u < 4; ++u) b[u] = read_b(0, u);
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
         a_operands<kMx>(wr[t][2 * h + p], kMx ? mx_scale((uint8_t)(e[t] >> 8 * (2 * h + p))) : 1.0f, a[t][2 * p], a[t][2 * p + 1]);
 #pragma unroll
     for (int q = 0; q < MT; ++q) {
-      bf16x8 b[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        b[u] = *reinterpret_cast<const bf16x8*>(&xb[(32 * q + i) * 128 + 16 * ((4 * (u >> 1) + 2 * hh + (u & 1)) ^ (i >> 1 & 7))]);
+      // No slots left, in the last run of an expert.  (With block scales the
+      // branches cost registers that are not there.)
+      if (!kBlock && q > 0 && 32 * q >= at.count) break;
       f32x16 part[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -410,9 +405,14 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 4; ++u) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) part[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[t][u], b[u], part[t], 0, 0, 0);
+        // the operand's register is free: the next 32 slots' into it, three
+        // products ahead of their use
+        if (q + 1 < MT) b[u] = read_b(q + 1, u);
+        if (q + 1 < MT || u < 3) __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if constexpr (kBlock) {
@@ -423,12 +423,11 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
           acc[t][q] = part[t];
         }
       }
-      if (kBlock) __builtin_amdgcn_sched_barrier(0);
     }
   };
   // A block of 128 columns: x steps 2kb and 2kb + 1 are in x0 and x1, and
   // the two after them go to x2 and x0.
-  const auto block = [&](int kb, unsigned char* x0, unsigned char* x1, unsigned char* x2) {
+  const auto block = [&](int kb, unsigned char* x0, unsigned char* x1, unsigned char* x2) __attribute__((always_inline)) {
     take_w(kb);
     request_x(2 * kb + 2 < 2 * nkb ? 2 * kb + 2 : 0, x2);
     step(0, x0);
@@ -454,47 +453,58 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
   if (kb + 1 < nkb) block(kb + 1, xs2, xs0, xs1);
   vm_wait_all();   // nothing may land in LDS that is no longer ours
 
-  const float whole_scale = FMT == kFmtTensor ? ld_global<float>(scales, 0) : 1.0f;
+  // A lane holds slot 32q + l%32 and, for each v4, rows 8 v4 + 4 (l / 32) .. + 3
+  // of each tile.  32 slots at a time go through the wave's own LDS (rows of
+  // 64 outputs, 32 with SWIGLU, units swizzled as above), so that they reach
+  // memory as whole lines: 8-byte stores from here took 50 us on 134 MB.
+  constexpr int kCols = SWIGLU ? 32 : 64;           // outputs of a slot and wave
+  constexpr int kUnits = kCols / 8;
+  float os[2][16];
+  if (FMT == kFmtRow || FMT == kFmtTensor) {
 #pragma unroll
-  for (int v4 = 0; v4 < 4; ++v4) {
-    // rows 8 v4 + 4 (l / 32) .. + 3 of each tile
-    float os[2][4];
-    if (FMT == kFmtRow) {
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int v = 0; v < 16; ++v) {
+        const int row = min(out_row(t) + 8 * (v >> 2) + 4 * hh + (v & 3), n_out - 1) + half(t);
+        os[t][v] = ld_global<float>(scales, FMT == kFmtRow ? (size_t)row * 4 : 0);
+      }
+  }
+  const bool vec = n_out % 8 == 0 && reinterpret_cast<uintptr_t>(c.y) % 16 == 0;
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          os[t][v] = ld_global<float>(scales, (size_t)(min(out_row(t) + 8 * v4 + 4 * hh + v, n_out - 1) + half(t)) * 4);
-    }
+  for (int q = 0; q < MT; ++q) {
+    if (32 * q >= at.count) break;
+    unsigned char* out = wl + (q & 1) * 4096;
 #pragma unroll
-    for (int q = 0; q < MT; ++q) {
-      if (32 * q + i >= at.count) continue;
-      const int slot = at.slot0 + 32 * q + i;
+    for (int t = 0; t < (SWIGLU ? 1 : 2); ++t)
 #pragma unroll
-      for (int t = 0; t < (SWIGLU ? 1 : 2); ++t) {
-        const int n = out_row(t) + 8 * v4 + 4 * hh;
+      for (int v4 = 0; v4 < 4; ++v4) {
         float r[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           float o = acc[t][q][4 * v4 + v];
-          if (FMT == kFmtRow) o *= os[t][v];
-          if (FMT == kFmtTensor) o *= whole_scale;
+          if (FMT == kFmtRow || FMT == kFmtTensor) o *= os[t][4 * v4 + v];
           if (SWIGLU) {
             float u = acc[1][q][4 * v4 + v];
-            if (FMT == kFmtRow) u *= os[1][v];
-            if (FMT == kFmtTensor) u *= whole_scale;
+            if (FMT == kFmtRow || FMT == kFmtTensor) u *= os[1][4 * v4 + v];
             o = silu_times(o, u);
           }
           r[v] = live >> q & 1 ? o : 0.0f;   // else the products of zeros
         }
-        const size_t to = ((size_t)slot * n_out + n) * 2;
-        if (n_out % 4 == 0) {
-          if (n < n_out) st_global<u32x2>(c.y, to, u32x2{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])});
-        } else {
+        *reinterpret_cast<u32x2*>(out + i * 2 * kCols + 16 * ((4 * t + v4) ^ (i >> 1 & (kUnits - 1))) + 8 * hh) =
+            u32x2{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])};
+      }
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (n + v < n_out) st_global<uint16_t>(c.y, to + 2 * v, (uint16_t)bf16_pair(r[v], 0.0f));
-        }
+    for (int j = 0; j < kUnits / 2; ++j) {
+      const int r = j * (kWave / kUnits) + lane / kUnits, u = lane % kUnits, n = out_row(0) + 8 * u;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(out + r * 2 * kCols + 16 * (u ^ (r >> 1 & (kUnits - 1))));
+      if (32 * q + r >= at.count || n >= n_out) continue;
+      const size_t to = ((size_t)(at.slot0 + 32 * q + r) * n_out + n) * 2;
+      if (vec) {
+        st_global<u32x4>(c.y, to, v);
+      } else {
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+          if (n + w < n_out) st_global<uint16_t>(c.y, to + 2 * w, (uint16_t)(v[w >> 1] >> 16 * (w & 1)));
       }
     }
   }
