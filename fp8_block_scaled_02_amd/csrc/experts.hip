@@ -510,6 +510,160 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
   }
 }
 
+// The streaming kernel, for experts of a few slots: 32 weight rows (SWIGLU:
+// 16 of each half) against 16 slots, bound by the weights' way from HBM.
+//
+// The four waves share k: wave w takes the 128-column blocks w, w + 4, ...,
+// up to four at a time, all of whose weights (4 KB a block, in whole lines)
+// and operands of x it asks for at once, and waits for once.  Nothing is
+// shared between waves until their sums meet in LDS at the end, so there is
+// no barrier before that; two workgroups a CU keep 128 KB on its way.
+template <int FMT, bool SWIGLU>
+__global__ __launch_bounds__(256, 2) void k_experts_stream(ExpertsCall c, int n_groups) {
+  constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
+  constexpr bool kMx = FMT == kFmtMx;
+  constexpr int kRound = 4;                        // blocks of a wave at a time
+  __shared__ __attribute__((aligned(16))) unsigned char ws[4 * kRound * 4096];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int i = lane & 15, g = lane >> 4;
+  const TileAt at = tile_at(c.offsets, c.experts, c.slots, 16, n_groups);
+  if (at.expert < 0) return;
+  const int n_out = SWIGLU ? c.n / 2 : c.n;
+  const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32;
+  const int n0 = at.group * (SWIGLU ? 16 : 32);
+  const uint8_t* codes = c.codes + (size_t)at.expert * c.n * k;
+  const char* scales = static_cast<const char*>(c.scales) + (size_t)at.expert * c.scale_bytes;
+  const auto out_row = [&](int t) { return n0 + (SWIGLU ? 0 : 16 * t); };
+  const auto half = [&](int t) { return SWIGLU && t == 1 ? n_out : 0; };
+  unsigned char* wl = ws + wave * kRound * 4096;
+
+  // Load j of a block brings rows 8j + l/8 (tile j / 2); LDS place l%8 of a
+  // row holds its unit (l%8) ^ (row / 2 % 8).  Rows past the end are the
+  // last one, columns past it column 0, and zero weights.
+  const uint8_t* wp[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    wp[j] = codes + (size_t)(min(out_row(j >> 1) + 8 * (j & 1) + (lane >> 3), n_out - 1) + half(j >> 1)) * k;
+  const int wunit = (lane & 7) ^ (lane >> 4);   // j odd: ^ 4
+  const auto request_w = [&](int kb, unsigned char* to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = kb * 128 + 16 * (wunit ^ (j & 1) * 4);
+      stage16(wp[j] + (col < k ? col : 0), to + j * 1024);
+    }
+  };
+  const int rounds = (nkb + 4 * kRound - 1) / (4 * kRound);
+  // the first round's weights before anything that takes a second look-up
+#pragma unroll
+  for (int j = 0; j < kRound; ++j)
+    if (wave + 4 * j < nkb) request_w(wave + 4 * j, wl + j * 4096);
+
+  const int slot = at.slot0 + min(i, at.count - 1);
+  const int row = c.rows ? ld_global<int32_t>(c.rows, (size_t)slot * 4) : slot;
+  const bool live = row >= 0 && row < c.x_rows;
+  const uint16_t* xp = c.x + (size_t)(live ? row : 0) * k;
+  const char* sp[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    // a lane's four sums are rows 4g .. of the tile: one scale block (the
+    // halves start on a multiple of 4)
+    if (kBlock) sp[t] = scales + (size_t)((min(out_row(t) + 4 * g, n_out - 1) + half(t)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
+    if (kMx) sp[t] = scales + (size_t)(min(out_row(t) + i, n_out - 1) + half(t)) * ng;
+  }
+
+  f32x4 acc[2] = {};
+#pragma unroll 1
+  for (int r = 0; r < rounds; ++r) {
+    const int kb0 = wave + 4 * kRound * r;
+    uint4 x[kRound][4];
+    float sc[kRound][2];
+    uint32_t ex[kRound][2];
+#pragma unroll
+    for (int j = 0; j < kRound; ++j) {
+      const int kb = min(kb0 + 4 * j, nkb - 1);    // past the end: loaded, not used
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int col = kb * 128 + 64 * (u >> 1) + 16 * g + 8 * (u & 1);
+        x[j][u] = ld_global_u4(xp, (size_t)(col < k ? col : 0) * 2);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (FMT == kFmtBlock) sc[j][t] = ld_global<float>(sp[t], (size_t)kb * 4);
+        if (FMT == kFmtBlockBf16) sc[j][t] = bf16_lo(ld_global<uint16_t>(sp[t], (size_t)kb * 2));
+        if (kMx) ex[j][t] = ld_global<u32_unaligned>(sp[t], (size_t)min(4 * kb, ng - 4)) >> 8 * (4 * kb - min(4 * kb, ng - 4));
+      }
+    }
+    vm_wait_all();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < kRound; ++j) {
+      const int kb = kb0 + 4 * j;
+      if (kb >= nkb) break;
+      const unsigned char* wb = wl + j * 4096;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 part = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 w = *reinterpret_cast<const uint4*>(wb + (16 * t + i) * 128 + 16 * ((4 * h + g) ^ (i >> 1)));
+          if (kb * 128 + 64 * h + 16 * g >= k) w = make_uint4(0, 0, 0, 0);
+          bf16x8 a0, a1;
+          a_operands<kMx>(w, kMx ? mx_scale((uint8_t)(ex[j][t] >> 8 * (2 * h + (g >> 1)))) : 1.0f, a0, a1);
+          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, x[j][2 * h]), part, 0, 0, 0);
+          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, x[j][2 * h + 1]), part, 0, 0, 0);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(kBlock ? sc[j][t] : 1.0f, part[v], acc[t][v]);
+      }
+    }
+    if (r + 1 < rounds) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the codes have been read
+#pragma unroll
+      for (int j = 0; j < kRound; ++j)
+        if (kb0 + 4 * kRound + 4 * j < nkb) request_w(kb0 + 4 * kRound + 4 * j, wl + j * 4096);
+    }
+  }
+
+  // the waves' sums meet, each in its own part of LDS; wave t finishes tile t
+#pragma unroll
+  for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(wl + (t * kWave + lane) * 16) = acc[t];
+  __syncthreads();
+  const auto total = [&](int t) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(ws + (t * kWave + lane) * 16);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      const f32x4 o = *reinterpret_cast<const f32x4*>(ws + w * kRound * 4096 + (t * kWave + lane) * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += o[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = min(out_row(t) + 4 * g + j, n_out - 1) + half(t);
+      if (FMT == kFmtRow) v[j] *= ld_global<float>(scales, (size_t)row * 4);
+      if (FMT == kFmtTensor) v[j] *= ld_global<float>(scales, 0);
+    }
+    return v;
+  };
+  if (wave >= (SWIGLU ? 1 : 2) || i >= at.count) return;
+  f32x4 v = total(wave);
+  if (SWIGLU) {
+    const f32x4 u = total(1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = silu_times(v[j], u[j]);
+  }
+  if (!live) v = f32x4{};   // the products of zeros
+  const int n = out_row(wave) + 4 * g;
+  const size_t to = ((size_t)slot * n_out + n) * 2;
+  if (n_out % 4 == 0) {
+    if (n < n_out) st_global<u32x2>(c.y, to, u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < n_out) st_global<uint16_t>(c.y, to + 2 * j, (uint16_t)bf16_pair(v[j], 0.0f));
+  }
+}
+
 // Runs of `height` slots that any split of the slots over the experts can
 // have: each expert ends with at most one run that is not full.
 int64_t max_tiles(int64_t slots, int64_t experts, int64_t height) {
@@ -523,19 +677,22 @@ namespace {
 
 // The kernel of a call, by its sizes.
 struct ExpertsPlan {
-  int height;   // slots of a run; 16: the simple kernel
+  enum Kind { kSimple, kStream, kWide } kind;
+  int height;   // slots of a run
   int width;    // outputs of a group
 };
 
-// Halves that do not start on a multiple of 32 rows would put a wide tile's
-// rows in two scale blocks, and rows of fewer than four MX exponents cannot
-// be read four at a time: the simple kernel.  Otherwise the run's height
-// goes by the rows an expert has on average.
+// By the slots an expert has on average: the streaming kernel, or a wide
+// tile's height.  Halves that do not start on a multiple of 32 rows (4 for
+// the streaming kernel) would put a lane's sums in two scale blocks, and rows
+// of fewer than four MX exponents cannot be read four at a time.
 ExpertsPlan experts_plan(int64_t experts, int64_t slots, int64_t n, int64_t k, bool swiglu, int format) {
   const bool block = format == kFmtBlock || format == kFmtBlockBf16;
   const int64_t average = slots / (experts < slots ? experts : slots);
-  if ((swiglu && block && (n / 2) % 32 != 0) || (format == kFmtMx && k <= 96)) return {16, 64};
-  return {getenv("WMT") ? 32 * atoi(getenv("WMT")) : average >= 128 ? 128 : average >= 48 ? 64 : 32, swiglu ? 128 : 256};
+  const int64_t split = swiglu && block ? n / 2 : 0;
+  if (split % 4 != 0 || (format == kFmtMx && k <= 96)) return {ExpertsPlan::kSimple, 16, 64};
+  if (getenv("STR") ? atoi(getenv("STR")) : average <= 8 || split % 32 != 0) return {ExpertsPlan::kStream, 16, swiglu ? 16 : 32};
+  return {ExpertsPlan::kWide, getenv("WMT") ? 32 * atoi(getenv("WMT")) : average >= 128 ? 128 : average >= 48 ? 64 : 32, swiglu ? 128 : 256};
 }
 
 int64_t experts_groups(const ExpertsPlan& p, int64_t n, bool swiglu) {
@@ -544,6 +701,10 @@ int64_t experts_groups(const ExpertsPlan& p, int64_t n, bool swiglu) {
 
 template <int FMT, bool SWIGLU>
 void launch_plan(const ExpertsCall& c, const ExpertsPlan& p, unsigned blocks, int groups, hipStream_t stream) {
+  if (p.kind == ExpertsPlan::kStream) {
+    k_experts_stream<FMT, SWIGLU><<<blocks, 256, 0, stream>>>(c, groups);
+    return;
+  }
   switch (p.height) {
     case 128: k_experts_wide<FMT, SWIGLU, 4><<<blocks, 256, 0, stream>>>(c, groups); break;
     case 64: k_experts_wide<FMT, SWIGLU, 2><<<blocks, 256, 0, stream>>>(c, groups); break;
@@ -574,7 +735,7 @@ hipError_t launch_gemm_experts(const ExpertsCall& c, hipStream_t stream) {
   const ExpertsPlan p = experts_plan(c.experts, c.slots, c.n, c.k, c.swiglu, c.format);
   const int groups = (int)experts_groups(p, c.n, c.swiglu);
   const unsigned blocks = (unsigned)plan_blocks(p, c.experts, c.slots, c.n, c.swiglu);
-  if (p.height == 16) {
+  if (p.kind == ExpertsPlan::kSimple) {
     if (c.swiglu)
       k_experts_simple<true><<<blocks, 256, 0, stream>>>(c, groups);
     else
