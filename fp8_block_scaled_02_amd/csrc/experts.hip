@@ -40,20 +40,24 @@ __device__ __forceinline__ int wave_prefix(int v) {
   return v + (row > 0 ? a : 0) + (row > 1 ? b : 0) + (row > 2 ? c : 0);
 }
 
-// This workgroup's tile, found by each of its waves (the answer is the same
-// in every lane).  The experts' runs follow one another, each in n_groups
-// tiles.  The offsets are kept inside [0, slots], so that what a wrong offset
-// names is still in bounds.
+// The runs of all experts, in expert order, each in n_groups tiles, held by a
+// wave (the answers are the same in every lane).  The offsets are kept inside
+// [0, slots], so that what a wrong offset names is still in bounds.
 //
 // Workgroups go round the 8 XCDs in turn, and each XCD has its own L2: it
 // gets one contiguous eighth of the tiles, so that an expert's weights and
 // rows are read by one XCD, or two.  That takes the number of tiles, so all
 // offsets are read: 256 experts a pass, every load of a pass at once.
-__device__ __forceinline__ TileAt tile_at(const int32_t* offsets, int experts, int slots, int height, int n_groups) {
-  constexpr int kPass = 4;
-  const int lane = threadIdx.x & (kWave - 1);
-  int from[kPass], tiles[kPass], upto[kPass], last[kPass];
-  const auto pass = [&](int e0, int before) {   // runs of the pass's experts; the runs up to its end
+constexpr int kRunsFew = 256;   // experts of one pass
+template <bool FEW>
+struct Runs {
+  static constexpr int kPass = kRunsFew / kWave;
+  const int32_t* offsets;
+  int experts, slots, height, n_groups, total;
+  int from[kPass], last[kPass], upto[kPass];   // of experts e0 + 64 r + lane
+
+  __device__ __forceinline__ int pass(int e0, int before) {   // returns the runs up to the pass's end
+    const int lane = threadIdx.x & (kWave - 1);
 #pragma unroll
     for (int r = 0; r < kPass; ++r) {
       const int e = e0 + r * kWave + lane;
@@ -62,38 +66,61 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* offsets, int experts, i
     }
 #pragma unroll
     for (int r = 0; r < kPass; ++r) {
+      if (e0 + r * kWave >= experts) {
+        from[r] = last[r] = 0;
+        upto[r] = before;
+        continue;
+      }
       from[r] = min(max(from[r], 0), slots);
       last[r] = min(max(last[r], 0), slots);
-      tiles[r] = last[r] > from[r] ? (last[r] - from[r] + height - 1) / height : 0;
-      upto[r] = wave_prefix(tiles[r]) + before;
+      upto[r] = wave_prefix(tiles(r)) + before;
       before = __builtin_amdgcn_readlane(upto[r], kWave - 1);
     }
     return before;
-  };
-  int total = 0;
-  for (int e0 = 0; e0 < experts; e0 += kPass * kWave) total = pass(e0, total);
-  const int64_t share = ((int64_t)total * n_groups + 7) / 8;
-  const int64_t place = blockIdx.x >> 3, id = (blockIdx.x & 7) * share + place;
-  if (place >= share || id >= (int64_t)total * n_groups) return TileAt{-1, 0, 0, 0};
-  const int run = (int)((uint32_t)id / (uint32_t)n_groups);
-  TileAt t{-1, 0, 0, (int)((uint32_t)id - (uint32_t)run * (uint32_t)n_groups)};
-  int before = 0;
-  for (int e0 = 0; e0 < experts && t.expert < 0; e0 += kPass * kWave) {
-    if (experts > kPass * kWave) before = pass(e0, before);
-#pragma unroll
-    for (int r = 0; r < kPass; ++r) {
-      const int first = upto[r] - tiles[r];
-      const uint64_t mine = __ballot(run >= first && run < upto[r]);
-      if (mine) {
-        const int l = __builtin_ctzll(mine);
-        const int slot0 = from[r] + (run - first) * height;
-        t.expert = e0 + r * kWave + l;
-        t.slot0 = __builtin_amdgcn_readlane(slot0, l);
-        t.count = __builtin_amdgcn_readlane(min(height, last[r] - slot0), l);
-      }
+  }
+  __device__ __forceinline__ int tiles(int r) const {
+    return last[r] > from[r] ? (last[r] - from[r] + height - 1) / height : 0;
+  }
+  __device__ __forceinline__ Runs(const int32_t* o, int e, int s, int h, int g)
+      : offsets(o), experts(e), slots(s), height(h), n_groups(g), total(0) {
+    if constexpr (FEW) {
+      total = pass(0, 0);
+    } else {
+      for (int e0 = 0; e0 < experts; e0 += kPass * kWave) total = pass(e0, total);
     }
   }
-  return t;
+  // Tile `place` of this workgroup's XCD.
+  __device__ __forceinline__ TileAt at(int64_t place) {
+    const int64_t share = ((int64_t)total * n_groups + 7) / 8;
+    const int64_t id = (blockIdx.x & 7) * share + place;
+    if (place >= share || id >= (int64_t)total * n_groups) return TileAt{-1, 0, 1, 0};
+    const int run = (int)((uint32_t)id / (uint32_t)n_groups);
+    TileAt t{-1, 0, 1, (int)((uint32_t)id - (uint32_t)run * (uint32_t)n_groups)};
+    int before = 0;
+    for (int e0 = 0; e0 < (FEW ? 1 : experts) && t.expert < 0; e0 += kPass * kWave) {
+      if constexpr (!FEW) before = pass(e0, before);
+#pragma unroll
+      for (int r = 0; r < kPass; ++r) {
+        if (e0 + r * kWave >= experts) break;
+        const int first = upto[r] - tiles(r);
+        const uint64_t mine = __ballot(run >= first && run < upto[r]);
+        if (mine) {
+          const int l = __builtin_ctzll(mine);
+          const int slot0 = from[r] + (run - first) * height;
+          t.expert = e0 + r * kWave + l;
+          t.slot0 = __builtin_amdgcn_readlane(slot0, l);
+          t.count = __builtin_amdgcn_readlane(min(height, last[r] - slot0), l);
+        }
+      }
+    }
+    return t;
+  }
+};
+
+// The only tile of a workgroup.
+__device__ __forceinline__ TileAt tile_at(const int32_t* offsets, int experts, int slots, int height, int n_groups) {
+  if (experts <= kRunsFew) return Runs<true>(offsets, experts, slots, height, n_groups).at(blockIdx.x >> 3);
+  return Runs<false>(offsets, experts, slots, height, n_groups).at(blockIdx.x >> 3);
 }
 
 // silu(g) * u within a few units of the last place of fp32: exp(-g) as 2^t
@@ -510,157 +537,153 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
   }
 }
 
-// The streaming kernel, for experts of a few slots: 32 weight rows (SWIGLU:
-// 16 of each half) against 16 slots, bound by the weights' way from HBM.
+// The streaming kernel, for experts of a few slots: 16 * NT weight rows
+// (SWIGLU: half of them of each half) against 16 slots, bound by the weights'
+// way from HBM.
 //
 // The four waves share k: wave w takes the 128-column blocks w, w + 4, ...,
-// up to four at a time, all of whose weights (4 KB a block, in whole lines)
-// and operands of x it asks for at once, and waits for once.  Nothing is
-// shared between waves until their sums meet in LDS at the end, so there is
-// no barrier before that; two workgroups a CU keep 128 KB on its way.
-template <int FMT, bool SWIGLU>
-__global__ __launch_bounds__(256, 2) void k_experts_stream(ExpertsCall c, int n_groups) {
+// one at a time: its weights (2 KB a 16-row tile, in whole lines, to the
+// wave's own LDS) and operands of x are asked for together and waited for
+// once.  Nothing is shared between waves until their sums meet in LDS at the
+// end.  What keeps the memory busy is the number of workgroups a CU holds,
+// eight of 16 KB, each at another point of its way from look-up to sums:
+// four blocks at a time and two workgroups a CU took 65 us for 281 MB (32
+// tokens on 128 experts), two and four 54 us, one and eight 52 us; a ring of
+// two blocks in flight a wave 54 us.  NT = 4: 52 us, but 10.5 us for one
+// token against 8.5 us.
+template <int FMT, bool SWIGLU, int NT>
+__global__ __launch_bounds__(256, 16 / NT) void k_experts_stream(ExpertsCall c, int n_groups) {
   constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
   constexpr bool kMx = FMT == kFmtMx;
-  constexpr int kRound = 4;                        // blocks of a wave at a time
-  __shared__ __attribute__((aligned(16))) unsigned char ws[4 * kRound * 4096];
+  constexpr int kOut = SWIGLU ? NT / 2 : NT;       // 16-row tiles of outputs
+  __shared__ __attribute__((aligned(16))) unsigned char ws[4][NT * 2048];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int i = lane & 15, g = lane >> 4;
   const TileAt at = tile_at(c.offsets, c.experts, c.slots, 16, n_groups);
   if (at.expert < 0) return;
   const int n_out = SWIGLU ? c.n / 2 : c.n;
   const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32;
-  const int n0 = at.group * (SWIGLU ? 16 : 32);
+  const int n0 = at.group * 16 * kOut;
   const uint8_t* codes = c.codes + (size_t)at.expert * c.n * k;
   const char* scales = static_cast<const char*>(c.scales) + (size_t)at.expert * c.scale_bytes;
-  const auto out_row = [&](int t) { return n0 + (SWIGLU ? 0 : 16 * t); };
-  const auto half = [&](int t) { return SWIGLU && t == 1 ? n_out : 0; };
-  unsigned char* wl = ws + wave * kRound * 4096;
+  const auto out_row = [&](int t) { return n0 + 16 * (t % kOut); };
+  const auto half = [&](int t) { return t >= kOut ? n_out : 0; };
+  unsigned char* wl = ws[wave];
 
   // Load j of a block brings rows 8j + l/8 (tile j / 2); LDS place l%8 of a
   // row holds its unit (l%8) ^ (row / 2 % 8).  Rows past the end are the
   // last one, columns past it column 0, and zero weights.
-  const uint8_t* wp[4];
+  const uint8_t* wp[2 * NT];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 2 * NT; ++j)
     wp[j] = codes + (size_t)(min(out_row(j >> 1) + 8 * (j & 1) + (lane >> 3), n_out - 1) + half(j >> 1)) * k;
   const int wunit = (lane & 7) ^ (lane >> 4);   // j odd: ^ 4
-  const auto request_w = [&](int kb, unsigned char* to) __attribute__((always_inline)) {
+  const auto request_w = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2 * NT; ++j) {
       const int col = kb * 128 + 16 * (wunit ^ (j & 1) * 4);
-      stage16(wp[j] + (col < k ? col : 0), to + j * 1024);
+      stage16(wp[j] + (col < k ? col : 0), wl + j * 1024);
     }
   };
-  const int rounds = (nkb + 4 * kRound - 1) / (4 * kRound);
-  // the first round's weights before anything that takes a second look-up
-#pragma unroll
-  for (int j = 0; j < kRound; ++j)
-    if (wave + 4 * j < nkb) request_w(wave + 4 * j, wl + j * 4096);
+  // the first weights before anything that takes a second look-up
+  if (wave < nkb) request_w(wave);
 
   const int slot = at.slot0 + min(i, at.count - 1);
   const int row = c.rows ? ld_global<int32_t>(c.rows, (size_t)slot * 4) : slot;
   const bool live = row >= 0 && row < c.x_rows;
   const uint16_t* xp = c.x + (size_t)(live ? row : 0) * k;
-  const char* sp[2];
+  const char* sp[NT];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < NT; ++t) {
     // a lane's four sums are rows 4g .. of the tile: one scale block (the
     // halves start on a multiple of 4)
     if (kBlock) sp[t] = scales + (size_t)((min(out_row(t) + 4 * g, n_out - 1) + half(t)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
     if (kMx) sp[t] = scales + (size_t)(min(out_row(t) + i, n_out - 1) + half(t)) * ng;
   }
 
-  f32x4 acc[2] = {};
+  f32x4 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-  for (int r = 0; r < rounds; ++r) {
-    const int kb0 = wave + 4 * kRound * r;
-    uint4 x[kRound][4];
-    float sc[kRound][2];
-    uint32_t ex[kRound][2];
+  for (int kb = wave; kb < nkb; kb += 4) {
+    uint4 x[4];
+    float sc[NT];
+    uint32_t ex[NT];
 #pragma unroll
-    for (int j = 0; j < kRound; ++j) {
-      const int kb = min(kb0 + 4 * j, nkb - 1);    // past the end: loaded, not used
+    for (int u = 0; u < 4; ++u) {
+      const int col = kb * 128 + 64 * (u >> 1) + 16 * g + 8 * (u & 1);
+      x[u] = ld_global_u4(xp, (size_t)(col < k ? col : 0) * 2);
+    }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int col = kb * 128 + 64 * (u >> 1) + 16 * g + 8 * (u & 1);
-        x[j][u] = ld_global_u4(xp, (size_t)(col < k ? col : 0) * 2);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (FMT == kFmtBlock) sc[j][t] = ld_global<float>(sp[t], (size_t)kb * 4);
-        if (FMT == kFmtBlockBf16) sc[j][t] = bf16_lo(ld_global<uint16_t>(sp[t], (size_t)kb * 2));
-        if (kMx) ex[j][t] = ld_global<u32_unaligned>(sp[t], (size_t)min(4 * kb, ng - 4)) >> 8 * (4 * kb - min(4 * kb, ng - 4));
-      }
+    for (int t = 0; t < NT; ++t) {
+      if (FMT == kFmtBlock) sc[t] = ld_global<float>(sp[t], (size_t)kb * 4);
+      if (FMT == kFmtBlockBf16) sc[t] = bf16_lo(ld_global<uint16_t>(sp[t], (size_t)kb * 2));
+      // four bytes that end with the row's last, where the block has fewer
+      if (kMx) ex[t] = ld_global<u32_unaligned>(sp[t], (size_t)min(4 * kb, ng - 4)) >> 8 * (4 * kb - min(4 * kb, ng - 4));
     }
     vm_wait_all();
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int j = 0; j < kRound; ++j) {
-      const int kb = kb0 + 4 * j;
-      if (kb >= nkb) break;
-      const unsigned char* wb = wl + j * 4096;
+    for (int t = 0; t < NT; ++t) {
+      f32x4 part = {};
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4 part = {};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 w = *reinterpret_cast<const uint4*>(wb + (16 * t + i) * 128 + 16 * ((4 * h + g) ^ (i >> 1)));
-          if (kb * 128 + 64 * h + 16 * g >= k) w = make_uint4(0, 0, 0, 0);
-          bf16x8 a0, a1;
-          a_operands<kMx>(w, kMx ? mx_scale((uint8_t)(ex[j][t] >> 8 * (2 * h + (g >> 1)))) : 1.0f, a0, a1);
-          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, x[j][2 * h]), part, 0, 0, 0);
-          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, x[j][2 * h + 1]), part, 0, 0, 0);
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(kBlock ? sc[j][t] : 1.0f, part[v], acc[t][v]);
+      for (int h = 0; h < 2; ++h) {
+        uint4 w = *reinterpret_cast<const uint4*>(wl + (16 * t + i) * 128 + 16 * ((4 * h + g) ^ (i >> 1)));
+        if (kb * 128 + 64 * h + 16 * g >= k) w = make_uint4(0, 0, 0, 0);
+        bf16x8 a0, a1;
+        a_operands<kMx>(w, kMx ? mx_scale((uint8_t)(ex[t] >> 8 * (2 * h + (g >> 1)))) : 1.0f, a0, a1);
+        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, x[2 * h]), part, 0, 0, 0);
+        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, x[2 * h + 1]), part, 0, 0, 0);
       }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(kBlock ? sc[t] : 1.0f, part[v], acc[t][v]);
     }
-    if (r + 1 < rounds) {
+    if (kb + 4 < nkb) {
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the codes have been read
-#pragma unroll
-      for (int j = 0; j < kRound; ++j)
-        if (kb0 + 4 * kRound + 4 * j < nkb) request_w(kb0 + 4 * kRound + 4 * j, wl + j * 4096);
+      request_w(kb + 4);
     }
   }
 
-  // the waves' sums meet, each in its own part of LDS; wave t finishes tile t
+  // the waves' sums meet, each in its own part of LDS; wave t finishes the
+  // outputs of tiles t, t + 4, ...
 #pragma unroll
-  for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(wl + (t * kWave + lane) * 16) = acc[t];
+  for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(wl + (t * kWave + lane) * 16) = acc[t];
   __syncthreads();
   const auto total = [&](int t) {
-    f32x4 v = *reinterpret_cast<const f32x4*>(ws + (t * kWave + lane) * 16);
+    f32x4 v = *reinterpret_cast<const f32x4*>(ws[0] + (t * kWave + lane) * 16);
 #pragma unroll
     for (int w = 1; w < 4; ++w) {
-      const f32x4 o = *reinterpret_cast<const f32x4*>(ws + w * kRound * 4096 + (t * kWave + lane) * 16);
+      const f32x4 o = *reinterpret_cast<const f32x4*>(ws[w] + (t * kWave + lane) * 16);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] += o[j];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = min(out_row(t) + 4 * g + j, n_out - 1) + half(t);
-      if (FMT == kFmtRow) v[j] *= ld_global<float>(scales, (size_t)row * 4);
+      const int r = min(out_row(t) + 4 * g + j, n_out - 1) + half(t);
+      if (FMT == kFmtRow) v[j] *= ld_global<float>(scales, (size_t)r * 4);
       if (FMT == kFmtTensor) v[j] *= ld_global<float>(scales, 0);
     }
     return v;
   };
-  if (wave >= (SWIGLU ? 1 : 2) || i >= at.count) return;
-  f32x4 v = total(wave);
-  if (SWIGLU) {
-    const f32x4 u = total(1);
+  if (i >= at.count) return;
+  for (int t = wave; t < kOut; t += 4) {
+    f32x4 v = total(t);
+    if (SWIGLU) {
+      const f32x4 u = total(t + kOut);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = silu_times(v[j], u[j]);
-  }
-  if (!live) v = f32x4{};   // the products of zeros
-  const int n = out_row(wave) + 4 * g;
-  const size_t to = ((size_t)slot * n_out + n) * 2;
-  if (n_out % 4 == 0) {
-    if (n < n_out) st_global<u32x2>(c.y, to, u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
-  } else {
+      for (int j = 0; j < 4; ++j) v[j] = silu_times(v[j], u[j]);
+    }
+    if (!live) v = f32x4{};   // the products of zeros
+    const int n = out_row(t) + 4 * g;
+    const size_t to = ((size_t)slot * n_out + n) * 2;
+    if (n_out % 4 == 0) {
+      if (n < n_out) st_global<u32x2>(c.y, to, u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n + j < n_out) st_global<uint16_t>(c.y, to + 2 * j, (uint16_t)bf16_pair(v[j], 0.0f));
+      for (int j = 0; j < 4; ++j)
+        if (n + j < n_out) st_global<uint16_t>(c.y, to + 2 * j, (uint16_t)bf16_pair(v[j], 0.0f));
+    }
   }
 }
 
@@ -675,6 +698,8 @@ int64_t max_tiles(int64_t slots, int64_t experts, int64_t height) {
 
 namespace {
 
+constexpr int kStreamTiles = 2;   // 16-row weight tiles of a streaming workgroup
+
 // The kernel of a call, by its sizes.
 struct ExpertsPlan {
   enum Kind { kSimple, kStream, kWide } kind;
@@ -683,15 +708,15 @@ struct ExpertsPlan {
 };
 
 // By the slots an expert has on average: the streaming kernel, or a wide
-// tile's height.  Halves that do not start on a multiple of 32 rows (4 for
-// the streaming kernel) would put a lane's sums in two scale blocks, and rows
-// of fewer than four MX exponents cannot be read four at a time.
+// tile's height.  Halves that do not start on a multiple of 32 rows would
+// put a tile's rows in two scale blocks, and rows of fewer than four MX
+// exponents cannot be read four at a time: the simple kernel.
 ExpertsPlan experts_plan(int64_t experts, int64_t slots, int64_t n, int64_t k, bool swiglu, int format) {
   const bool block = format == kFmtBlock || format == kFmtBlockBf16;
   const int64_t average = slots / (experts < slots ? experts : slots);
   const int64_t split = swiglu && block ? n / 2 : 0;
   if (split % 4 != 0 || (format == kFmtMx && k <= 96)) return {ExpertsPlan::kSimple, 16, 64};
-  if (getenv("STR") ? atoi(getenv("STR")) : average <= 8 || split % 32 != 0) return {ExpertsPlan::kStream, 16, swiglu ? 16 : 32};
+  if (getenv("STR") ? atoi(getenv("STR")) : average <= 8 || split % 32 != 0) return {ExpertsPlan::kStream, 16, 16 * (swiglu ? kStreamTiles / 2 : kStreamTiles)};
   return {ExpertsPlan::kWide, getenv("WMT") ? 32 * atoi(getenv("WMT")) : average >= 128 ? 128 : average >= 48 ? 64 : 32, swiglu ? 128 : 256};
 }
 
@@ -702,7 +727,7 @@ int64_t experts_groups(const ExpertsPlan& p, int64_t n, bool swiglu) {
 template <int FMT, bool SWIGLU>
 void launch_plan(const ExpertsCall& c, const ExpertsPlan& p, unsigned blocks, int groups, hipStream_t stream) {
   if (p.kind == ExpertsPlan::kStream) {
-    k_experts_stream<FMT, SWIGLU><<<blocks, 256, 0, stream>>>(c, groups);
+    k_experts_stream<FMT, SWIGLU, kStreamTiles><<<blocks, 256, 0, stream>>>(c, groups);
     return;
   }
   switch (p.height) {
