@@ -9,7 +9,6 @@
 // synchronization): every workgroup finds its expert in the offsets.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include <type_traits>
 
@@ -241,14 +240,14 @@ __device__ __forceinline__ void settle(float (&v)[16]) {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32_unaligned __attribute__((aligned(1)));
 
-// The wide kernel: 256 weight rows against 32 * MT slots of one expert on
-// the 32x32x16 MFMA, four waves of 64 rows (SWIGLU: 32 of each half), two
-// workgroups a CU.
+// The wide kernel: 128 * TW weight rows against 32 * MT slots of one expert
+// on the 32x32x16 MFMA, four waves of 32 * TW rows (SWIGLU: half of them of
+// each half), two (TW = 2) or four workgroups a CU.
 //
 // Everything reaches LDS by loads that write it directly, in whole 128-byte
 // lines (in the MFMA A layout a load instruction would touch 64 bytes of 16
 // rows or 32 of 32, which took as long as the products themselves).
-//   * Weights: a wave's 64 rows of a 128-column block are its own 8 KB.  At
+//   * Weights: a wave's rows of a 128-column block are its own 4 * TW KB.  At
 //     the start of a block it takes them into registers in the A layout and
 //     asks for the next block at once: a block's time to arrive.
 //   * x: 64 columns of the slots for all four waves, three buffers, asked
@@ -264,15 +263,18 @@ typedef uint32_t u32_unaligned __attribute__((aligned(1)));
 // A block scale multiplies its sums every 64 columns (a full block's sums
 // would need as many registers as the accumulators); MX scales multiply the
 // codes as they become bf16 (exact); row and tensor scales the results.
-template <int FMT, bool SWIGLU, int MT>
-__global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_groups) {
+template <int FMT, bool SWIGLU, int MT, int TW>
+__global__ __launch_bounds__(256, TW == 2 ? 2 : 4) void k_experts_wide(ExpertsCall c, int n_groups) {
   constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
   constexpr bool kMx = FMT == kFmtMx;
   constexpr int kSlots = 32 * MT;
+  constexpr int kRows = 32 * TW;       // weight rows of a wave
+  constexpr int kCols = SWIGLU ? kRows / 2 : kRows;   // outputs of a slot and wave
   constexpr int kXLoads = MT;          // x loads of a wave and step (1 KB each)
+  constexpr int kWLoads = 4 * TW;      // weight loads of a wave and block
   // separate arrays: the compiler then knows that reads of one need not wait
   // for what is on its way into another
-  __shared__ __attribute__((aligned(16))) unsigned char ws[4 * 64 * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char ws[4 * kRows * 128];
   __shared__ __attribute__((aligned(16))) unsigned char xs0[kSlots * 128];
   __shared__ __attribute__((aligned(16))) unsigned char xs1[kSlots * 128];
   __shared__ __attribute__((aligned(16))) unsigned char xs2[kSlots * 128];
@@ -283,13 +285,14 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
   const int n_out = SWIGLU ? c.n / 2 : c.n;
   const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32;
 
-  const int n0 = at.group * (SWIGLU ? 128 : 256) + wave * (SWIGLU ? 32 : 64);
+  const int n0 = (at.group * 4 + wave) * kCols;
   const uint8_t* codes = c.codes + (size_t)at.expert * c.n * k;
   const char* scales = static_cast<const char*>(c.scales) + (size_t)at.expert * c.scale_bytes;
-  // 32-row tile t of the wave: outputs from out_row(t), weight rows half(t) on
-  const auto out_row = [&](int t) { return n0 + (SWIGLU ? 0 : 32 * t); };
-  const auto half = [&](int t) { return SWIGLU && t == 1 ? n_out : 0; };
-  unsigned char* wl = ws + wave * 64 * 128;
+  // Row r of the wave's (r may be uniform or a lane's): output out_row(r),
+  // weight row half(r) further on.
+  const auto out_row = [&](int r) { return n0 + r % kCols; };
+  const auto half = [&](int r) { return r >= kCols ? n_out : 0; };
+  unsigned char* wl = ws + wave * kRows * 128;
 
   // Load j of a wave's weights brings rows 8j + l/8; LDS place l%8 of a row
   // holds its unit (l%8) ^ (row / 2 % 8), so j odd the unit of j even ^ 4.
@@ -306,10 +309,10 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
     const int c0 = kb * 128 + wcol, c1 = kb * 128 + (wcol ^ 64);
     const uint32_t col[2] = {(uint32_t)(c0 < k ? c0 : 0), (uint32_t)(c1 < k ? c1 : 0)};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int row = min(out_row(j >> 2) + 8 * (j & 3), n_out - 1);
+    for (int j = 0; j < kWLoads; ++j) {
+      const int row = min(out_row(8 * j), n_out - 1);
       const uint32_t within = (uint32_t)min(n_out - 1 - row, 7) * (uint32_t)k;
-      stage16(codes + (size_t)(row + half(j >> 2)) * k + (min(wrow, within) + col[j & 1]), wl + j * 1024);
+      stage16(codes + (size_t)(row + half(8 * j)) * k + (min(wrow, within) + col[j & 1]), wl + j * 1024);
     }
     asm volatile("" ::: "memory");
   };
@@ -343,19 +346,23 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
     live |= row >= 0 && row < c.x_rows ? 1u << q : 0u;
   }
 
-  // scales of the next block: a float a tile (32 rows lie in one scale
-  // block; scalar loads), or the lane's row's four MX exponents
-  const char* sp[2];
-  float sc[2] = {1.0f, 1.0f};
-  uint32_t ex[2] = {0, 0};
+  // scales of the next block: a float a run of rows that lie in one scale
+  // block (a half's, or a 32-row tile; scalar loads), or the four MX exponents
+  // of the lane's row in each tile
+  constexpr int kScales = kMx ? TW : SWIGLU ? 2 : TW;
+  const auto scale_of = [](int t, int v) { return SWIGLU && TW == 1 ? v >> 3 : t; };   // of sum v of tile t
+  const char* sp[kScales];
+  float sc[kScales];
+  uint32_t ex[kScales];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    if (kBlock) sp[t] = scales + (size_t)((min(out_row(t), n_out - 1) + half(t)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
-    if (kMx) sp[t] = scales + (size_t)(min(out_row(t) + i, n_out - 1) + half(t)) * ng;
+  for (int t = 0; t < kScales; ++t) {
+    const int first = t * (kRows / kScales);
+    if (kBlock) sp[t] = scales + (size_t)((min(out_row(first), n_out - 1) + half(first)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
+    if (kMx) sp[t] = scales + (size_t)(min(out_row(32 * t + i), n_out - 1) + half(32 * t + i)) * ng;
   }
   const auto request_s = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < kScales; ++t) {
       if (FMT == kFmtBlock) sc[t] = reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(sp[t]))[kb];
       if (FMT == kFmtBlockBf16)
         sc[t] = bf16_lo(reinterpret_cast<const __attribute__((address_space(4))) uint16_t*>(reinterpret_cast<uintptr_t>(sp[t]))[kb]);
@@ -366,20 +373,20 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
 
   // the sums: single registers where scales are applied to them, else the
   // MFMA's own
-  std::conditional_t<kBlock, float[16], f32x16> acc[2][MT];
+  std::conditional_t<kBlock, float[16], f32x16> acc[TW][MT];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int t = 0; t < TW; ++t)
 #pragma unroll
     for (int q = 0; q < MT; ++q)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[t][q][v] = 0.0f;
 
-  uint4 wr[2][4];                  // tile, 32-column pair of the block
-  float s[2] = {1.0f, 1.0f};
-  uint32_t e[2] = {0, 0};
+  uint4 wr[TW][4];                 // tile, 32-column pair of the block
+  float s[kScales];
+  uint32_t e[TW];
   const auto take_w = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < TW; ++t)
 #pragma unroll
       for (int p = 0; p < 4; ++p)
         wr[t][p] = *reinterpret_cast<const uint4*>(&wl[(32 * t + i) * 128 + 16 * ((2 * p + hh) ^ (i >> 1 & 7))]);
@@ -387,12 +394,14 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
       const int from = kb * 128 + 16 * (lane_fresh() >> 5);
 #pragma unroll
       for (int p = 0; p < 4; ++p)
-        if (from + 32 * p >= k) wr[0][p] = wr[1][p] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < TW; ++t)
+          if (from + 32 * p >= k) wr[t][p] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t] = sc[t];
-      e[t] = kMx ? ex[t] >> 8 * (4 * kb - min(4 * kb, ng - 4)) : 0;
+    for (int t = 0; t < kScales; ++t) {
+      if (kBlock) s[t] = sc[t];
+      if (kMx) e[t] = ex[t] >> 8 * (4 * kb - min(4 * kb, ng - 4));
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0): the codes are in registers
@@ -408,22 +417,22 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
     const auto read_b = [&](int q, int u) __attribute__((always_inline)) {
       return *reinterpret_cast<const bf16x8*>(&xb[(32 * q + i) * 128 + 16 * ((4 * (u >> 1) + 2 * hh + (u & 1)) ^ (i >> 1 & 7))]);
     };
-    bf16x8 a[2][4], b[4];
+    bf16x8 a[TW][4], b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) b[u] = read_b(0, u);
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TW; ++t)
         a_operands<kMx>(wr[t][2 * h + p], kMx ? mx_scale((uint8_t)(e[t] >> 8 * (2 * h + p))) : 1.0f, a[t][2 * p], a[t][2 * p + 1]);
 #pragma unroll
     for (int q = 0; q < MT; ++q) {
       // No slots left, in the last run of an expert.  (With block scales the
       // branches cost registers that are not there.)
       if (!kBlock && q > 0 && 32 * q >= at.count) break;
-      f32x16 part[2];
+      f32x16 part[TW];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TW; ++t) {
         if constexpr (kBlock) {
 #pragma unroll
           for (int v = 0; v < 16; ++v) part[t][v] = 0.0f;
@@ -434,17 +443,17 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) part[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[t][u], b[u], part[t], 0, 0, 0);
+        for (int t = 0; t < TW; ++t) part[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[t][u], b[u], part[t], 0, 0, 0);
         // the operand's register is free: the next 32 slots' into it, three
         // products ahead of their use
         if (q + 1 < MT) b[u] = read_b(q + 1, u);
         if (q + 1 < MT || u < 3) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TW; ++t) {
         if constexpr (kBlock) {
 #pragma unroll
-          for (int v = 0; v < 16; ++v) acc[t][q][v] = __builtin_fmaf(s[t], part[t][v], acc[t][q][v]);
+          for (int v = 0; v < 16; ++v) acc[t][q][v] = __builtin_fmaf(s[scale_of(t, v)], part[t][v], acc[t][q][v]);
           settle(acc[t][q]);
         } else {
           acc[t][q] = part[t];
@@ -458,7 +467,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
     take_w(kb);
     request_x(2 * kb + 2 < 2 * nkb ? 2 * kb + 2 : 0, x2);
     step(0, x0);
-    land_and_meet<8 + kXLoads>();                 // younger than x1's: weights and x2's
+    land_and_meet<kWLoads + kXLoads>();           // younger than x1's: weights and x2's
     request_x(2 * kb + 3 < 2 * nkb ? 2 * kb + 3 : 0, x0);
     step(1, x1);
     land_and_meet<kXLoads>();                     // the weights and x2's have landed
@@ -482,47 +491,42 @@ __global__ __launch_bounds__(256, 2) void k_experts_wide(ExpertsCall c, int n_gr
 
   // A lane holds slot 32q + l%32 and, for each v4, rows 8 v4 + 4 (l / 32) .. + 3
   // of each tile.  32 slots at a time go through the wave's own LDS (rows of
-  // 64 outputs, 32 with SWIGLU, units swizzled as above), so that they reach
-  // memory as whole lines: 8-byte stores from here took 50 us on 134 MB.
-  constexpr int kCols = SWIGLU ? 32 : 64;           // outputs of a slot and wave
+  // kCols outputs, units swizzled as above), so that they reach memory as
+  // whole lines: 8-byte stores from here took 50 us on 134 MB.
   constexpr int kUnits = kCols / 8;
-  float os[2][16];
+  float os[TW][16];
   if (FMT == kFmtRow || FMT == kFmtTensor) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < TW; ++t)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int row = min(out_row(t) + 8 * (v >> 2) + 4 * hh + (v & 3), n_out - 1) + half(t);
-        os[t][v] = ld_global<float>(scales, FMT == kFmtRow ? (size_t)row * 4 : 0);
+        const int r = 32 * t + 8 * (v >> 2) + 4 * hh + (v & 3);
+        os[t][v] = ld_global<float>(scales, FMT == kFmtRow ? (size_t)(min(out_row(r), n_out - 1) + half(r)) * 4 : 0);
       }
   }
   const bool vec = n_out % 8 == 0 && reinterpret_cast<uintptr_t>(c.y) % 16 == 0;
 #pragma unroll
   for (int q = 0; q < MT; ++q) {
     if (32 * q >= at.count) break;
-    unsigned char* out = wl + (q & 1) * 4096;
+    unsigned char* out = wl + (q & 1) * 64 * kCols;
 #pragma unroll
-    for (int t = 0; t < (SWIGLU ? 1 : 2); ++t)
+    for (int u = 0; u < kUnits; ++u) {   // outputs 8u + 4 (l / 32) .. + 3 of the wave's
+      const auto sum = [&](int r, int v) {   // of row r + 4 (l / 32) + v
+        const int t = r / 32, w = r % 32 / 2 + v;
+        return FMT == kFmtRow || FMT == kFmtTensor ? acc[t][q][w] * os[t][w] : acc[t][q][w];
+      };
+      float r[4];
 #pragma unroll
-      for (int v4 = 0; v4 < 4; ++v4) {
-        float r[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          float o = acc[t][q][4 * v4 + v];
-          if (FMT == kFmtRow || FMT == kFmtTensor) o *= os[t][4 * v4 + v];
-          if (SWIGLU) {
-            float u = acc[1][q][4 * v4 + v];
-            if (FMT == kFmtRow || FMT == kFmtTensor) u *= os[1][4 * v4 + v];
-            o = silu_times(o, u);
-          }
-          r[v] = live >> q & 1 ? o : 0.0f;   // else the products of zeros
-        }
-        *reinterpret_cast<u32x2*>(out + i * 2 * kCols + 16 * ((4 * t + v4) ^ (i >> 1 & (kUnits - 1))) + 8 * hh) =
-            u32x2{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])};
+      for (int v = 0; v < 4; ++v) {
+        const float o = SWIGLU ? silu_times(sum(8 * u, v), sum(8 * u + kCols, v)) : sum(8 * u, v);
+        r[v] = live >> q & 1 ? o : 0.0f;   // else the products of zeros
       }
+      *reinterpret_cast<u32x2*>(out + i * 2 * kCols + 16 * (u ^ (i >> 1 & (kUnits - 1))) + 8 * hh) =
+          u32x2{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])};
+    }
 #pragma unroll
     for (int j = 0; j < kUnits / 2; ++j) {
-      const int r = j * (kWave / kUnits) + lane / kUnits, u = lane % kUnits, n = out_row(0) + 8 * u;
+      const int r = j * (kWave / kUnits) + lane / kUnits, u = lane % kUnits, n = n0 + 8 * u;
       const u32x4 v = *reinterpret_cast<const u32x4*>(out + r * 2 * kCols + 16 * (u ^ (r >> 1 & (kUnits - 1))));
       if (32 * q + r >= at.count || n >= n_out) continue;
       const size_t to = ((size_t)(at.slot0 + 32 * q + r) * n_out + n) * 2;
@@ -702,22 +706,32 @@ constexpr int kStreamTiles = 2;   // 16-row weight tiles of a streaming workgrou
 
 // The kernel of a call, by its sizes.
 struct ExpertsPlan {
-  enum Kind { kSimple, kStream, kWide } kind;
+  enum Kind { kSimple, kStream, kNarrow, kWide } kind;
   int height;   // slots of a run
   int width;    // outputs of a group
 };
 
-// By the slots an expert has on average: the streaming kernel, or a wide
-// tile's height.  Halves that do not start on a multiple of 32 rows would
-// put a tile's rows in two scale blocks, and rows of fewer than four MX
-// exponents cannot be read four at a time: the simple kernel.
+// By the slots an expert has on average, from sweeps on MI355X (E = 64, 4
+// choices, gate and up 2048 x 2048, block scales; us at 2 / 4 / 8 / 12 slots
+// an expert, and down 2048 x 2048, row scales, at 24 / 48 / 96 / 160 / 256):
+//   streaming          36  44  54  65     88 141 250 395 615
+//   128 x 64 tiles     43  51  55  56     62  69  98 134 190
+//   256 x 128 tiles    68  74  78  78     59  78  97 121 163
+// With 8 experts of 4096 x 2048 the narrow tiles' lead lasts (24 .. 256
+// slots: 17 / 21 / 25 / 35 / 54 us against 25 / 32 / 34 / 35 / 54 us).
+//
+// Halves that do not start on a multiple of 32 rows would put a tile's rows
+// in two scale blocks (the streaming kernel asks for 4), and rows of fewer
+// than four MX exponents cannot be read four at a time.
 ExpertsPlan experts_plan(int64_t experts, int64_t slots, int64_t n, int64_t k, bool swiglu, int format) {
   const bool block = format == kFmtBlock || format == kFmtBlockBf16;
   const int64_t average = slots / (experts < slots ? experts : slots);
   const int64_t split = swiglu && block ? n / 2 : 0;
+  const int outputs = swiglu ? 1 : 2;   // of two weight rows
   if (split % 4 != 0 || (format == kFmtMx && k <= 96)) return {ExpertsPlan::kSimple, 16, 64};
-  if (getenv("STR") ? atoi(getenv("STR")) : average <= 8 || split % 32 != 0) return {ExpertsPlan::kStream, 16, 16 * (swiglu ? kStreamTiles / 2 : kStreamTiles)};
-  return {ExpertsPlan::kWide, getenv("WMT") ? 32 * atoi(getenv("WMT")) : average >= 128 ? 128 : average >= 48 ? 64 : 32, swiglu ? 128 : 256};
+  if (average <= 8 || split % 32 != 0) return {ExpertsPlan::kStream, 16, 8 * kStreamTiles * outputs};
+  if (average <= 128) return {ExpertsPlan::kNarrow, 64, 64 * outputs};
+  return {ExpertsPlan::kWide, 128, 128 * outputs};
 }
 
 int64_t experts_groups(const ExpertsPlan& p, int64_t n, bool swiglu) {
@@ -726,14 +740,10 @@ int64_t experts_groups(const ExpertsPlan& p, int64_t n, bool swiglu) {
 
 template <int FMT, bool SWIGLU>
 void launch_plan(const ExpertsCall& c, const ExpertsPlan& p, unsigned blocks, int groups, hipStream_t stream) {
-  if (p.kind == ExpertsPlan::kStream) {
-    k_experts_stream<FMT, SWIGLU, kStreamTiles><<<blocks, 256, 0, stream>>>(c, groups);
-    return;
-  }
-  switch (p.height) {
-    case 128: k_experts_wide<FMT, SWIGLU, 4><<<blocks, 256, 0, stream>>>(c, groups); break;
-    case 64: k_experts_wide<FMT, SWIGLU, 2><<<blocks, 256, 0, stream>>>(c, groups); break;
-    default: k_experts_wide<FMT, SWIGLU, 1><<<blocks, 256, 0, stream>>>(c, groups); break;
+  switch (p.kind) {
+    case ExpertsPlan::kStream: k_experts_stream<FMT, SWIGLU, kStreamTiles><<<blocks, 256, 0, stream>>>(c, groups); break;
+    case ExpertsPlan::kNarrow: k_experts_wide<FMT, SWIGLU, 2, 1><<<blocks, 256, 0, stream>>>(c, groups); break;
+    default: k_experts_wide<FMT, SWIGLU, 4, 2><<<blocks, 256, 0, stream>>>(c, groups); break;
   }
 }
 
