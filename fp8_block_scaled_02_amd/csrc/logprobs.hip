@@ -17,7 +17,9 @@
 // of the row: first the top-th largest of its lanes' maxima, then the
 // top-th key of its list whenever that is cut down, shared among the waves.
 // A wave looks at single values only where a lane's maximum reaches the
-// threshold.  Rows are cut into segments where there are too few of them to
+// threshold: the values of four such lanes at a time go through LDS to one
+// lane each, so that the wave tests 64 values of interest at once and the
+// step itself pays one comparison a lane.  Rows are cut into segments where there are too few of them to
 // fill the chip, and a second launch joins the segments.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -97,26 +99,37 @@ __device__ __forceinline__ float lp_load(const void* p, int64_t at) {
   return bf16_lo(ld_global<uint16_t>(p, (size_t)at * 2));
 }
 
-// Target, entropy and top alternatives of row t from its statistics and the
-// `count` keys of its candidates (every live logit, if fewer than top), by
-// the whole workgroup.  `keys` holds 64-bit words in LDS.
+// The given token's logit (any value if there is none, or it is outside).
 template <typename T>
-__device__ __forceinline__ void lp_finish(const LpArgs& a, int t, const LpStats& s, const uint64_t* keys, int count) {
+__device__ __forceinline__ float lp_target(const LpArgs& a, int t) {
+  if (!a.logprob) return 0.0f;
+  const int id = a.targets[t];
+  return id >= 0 && id < a.vocab ? lp_load<T>(a.logits, (int64_t)t * a.stride + id) : __builtin_nanf("");
+}
+
+// How many of the keys (LDS) are larger.
+__device__ __forceinline__ int lp_rank(const uint64_t* keys, int count, uint64_t key) {
+  int rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < count; ++j) rank += keys[j] > key ? 1 : 0;
+  return rank;
+}
+
+// Target, entropy and top alternatives of row t from its statistics, its
+// given token's logit (thread 0) and the `count` keys of its candidates
+// (every live logit, if fewer than top), by the whole workgroup.
+__device__ __forceinline__ void lp_finish(const LpArgs& a, int t, const LpStats& s, float target, const uint64_t* keys,
+                                          int count) {
   const LpRow row(s);
   const int tid = threadIdx.x;
   if (tid == 0) {
     if (a.entropy)
       a.entropy[t] = row.bad ? __builtin_nanf("") : row.empty ? 0.0f : row.ln_z - kLn2 * (s.u / s.z);
-    if (a.logprob) {
-      const int id = a.targets[t];
-      a.logprob[t] = id >= 0 && id < a.vocab ? row.logp(lp_load<T>(a.logits, (int64_t)t * a.stride + id))
-                                             : __builtin_nanf("");
-    }
+    if (a.logprob) a.logprob[t] = target == target ? row.logp(target) : __builtin_nanf("");
   }
   for (int i = tid; i < count; i += blockDim.x) {
     const uint64_t key = keys[i];
-    int rank = 0;
-    for (int j = 0; j < count; ++j) rank += keys[j] > key ? 1 : 0;
+    const int rank = lp_rank(keys, count, key);
     if (rank < a.top) {
       const int64_t at = (int64_t)t * a.top + rank;
       a.top_ids[at] = (int32_t)~(uint32_t)key;
@@ -138,11 +151,23 @@ __device__ __forceinline__ void lp_finish(const LpArgs& a, int t, const LpStats&
   }
 }
 
-// The largest threshold that at least `want` of the wave's keys reach (or 0
-// if there are fewer), stopping as soon as exactly that many do.  Keys: PER
-// a lane.
+// The largest of a lane's values where some are NaN, as ordered bits (rows
+// with NaN still rank the others).
+__device__ __forceinline__ uint32_t lp_nan_max(const float (&x)[16]) {
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t o = x[i] == x[i] ? ordered(x[i]) : 0;
+    best = o > best ? o : best;
+  }
+  return best;
+}
+
+// A threshold that at least `want` of the wave's keys reach (0 if there are
+// fewer), built from the top bit down until no more than `enough` reach it.
+// Keys: PER a lane.
 template <typename K, int PER>
-__device__ __forceinline__ K wave_threshold(const K (&key)[PER], int want) {
+__device__ __forceinline__ K wave_threshold(const K (&key)[PER], int want, int enough) {
   K thr = 0;
   for (int bit = 8 * (int)sizeof(K) - 1; bit >= 0; --bit) {
     const K cand = thr | ((K)1 << bit);
@@ -151,7 +176,7 @@ __device__ __forceinline__ K wave_threshold(const K (&key)[PER], int want) {
     for (int r = 0; r < PER; ++r) reach += __builtin_popcountll(__ballot(key[r] >= cand));
     if (reach >= want) {
       thr = cand;
-      if (reach == want) break;
+      if (reach <= enough) break;
     }
   }
   return thr;
@@ -169,13 +194,13 @@ struct LpList {
   uint64_t tau;                // keys below it cannot be in the answer
   int count;
 
-  // Cut the list down to its top `top` keys.
-  __device__ __forceinline__ void cut(int top) {
+  // Cut the list down to its largest keys: `top` at least, `enough` at most.
+  __device__ __forceinline__ void cut(int top, int enough) {
     const int lane = threadIdx.x & (kWave - 1);
     uint64_t k[kLpCap / kWave];
 #pragma unroll
     for (int r = 0; r < kLpCap / kWave; ++r) k[r] = r * kWave + lane < count ? keys[r * kWave + lane] : 0;
-    const uint64_t thr = wave_threshold(k, top);
+    const uint64_t thr = wave_threshold(k, top, enough);
     int kept = 0;
 #pragma unroll
     for (int r = 0; r < kLpCap / kWave; ++r) {
@@ -198,7 +223,7 @@ struct LpList {
     const uint64_t who = __ballot(want);
     if (!who) return;
     if (count > kLpCap - kWave) {
-      cut(top);
+      cut(top, kLpCap / 4 > top + 8 ? kLpCap / 4 : top + 8);
       want = want && key >= tau;
     }
     const uint64_t now = __ballot(want);
@@ -211,18 +236,22 @@ struct LpList {
 
 // One workgroup per row segment.
 template <typename T, bool TOP>
-__global__ __launch_bounds__(kLpThreads) void k_logprobs(LpArgs a) {
+__global__ __launch_bounds__(kLpThreads, 8) void k_logprobs(LpArgs a) {
   constexpr int kVec = 16 / sizeof(T);       // values of one 16-byte load
   constexpr int kLoads = 16 / kVec;
   __shared__ uint64_t lists[TOP ? kLpWaves * kLpCap : 1];
+  __shared__ __attribute__((aligned(16))) float picked[TOP ? kLpWaves : 1][kWave];   // 16 values of four lanes
+  __shared__ int picked_lane[TOP ? kLpWaves : 1][4];
   __shared__ uint64_t shared_tau;
   __shared__ LpStats wave_stats[kLpWaves];
   __shared__ int kept;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs;
+  float target = 0.0f;
   if (tid == 0) {
     shared_tau = kFirstKey;
     kept = 0;
+    target = lp_target<T>(a, t);
   }
   __syncthreads();
 
@@ -239,29 +268,8 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(LpArgs a) {
   LpStats s{-__builtin_inff(), 0.0f, 0.0f};
   LpList list{lists + wave * kLpCap, &shared_tau, kFirstKey, 0};
   bool first = true;
-  for (int64_t at = lo + wave * kLpBlock; at < hi; at += kLpWaves * kLpBlock) {
-    float x[16];
-#pragma unroll
-    for (int v = 0; v < kLoads; ++v) {
-      const int64_t p = at + (v * kWave + lane) * kVec;
-      if (p >= skew && p + kVec <= hi) {
-        const uint4 d = ld_stream_u4(base, (size_t)p * sizeof(T));
-        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (sizeof(T) == 2) {
-            x[v * kVec + 2 * i] = bf16_lo(w[i]);
-            x[v * kVec + 2 * i + 1] = bf16_hi(w[i]);
-          } else {
-            x[v * kVec + i] = __uint_as_float(w[i]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          x[v * kVec + i] = p + i >= skew && p + i < hi ? lp_load<T>(base, p + i) : -__builtin_inff();
-      }
-    }
+  // 1024 values from `at` on, 16 a lane: load v holds those of place (v * 64 + lane) * kVec.
+  const auto consume = [&](const float (&x)[16], int64_t at) __attribute__((always_inline)) {
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = __builtin_elementwise_maximum(top, x[i]);
@@ -278,23 +286,87 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(LpArgs a) {
     s = LpStats{m, __builtin_fmaf(s.z, f, z), __builtin_fmaf(f, __builtin_fmaf(down, s.z, s.u), u)};
 
     if constexpr (TOP) {
-      const uint32_t mine = top == top ? ordered(top) : 0;
+      const uint32_t mine = top == top ? ordered(top) : lp_nan_max(x);
       if (first) {
         first = false;
         const uint32_t k[1] = {mine};
-        list.raise((uint64_t)wave_threshold(k, a.top) << 32);
+        list.raise((uint64_t)wave_threshold(k, a.top, a.top + 8) << 32);
       }
       const uint64_t seen = uniform64(*(volatile uint64_t*)&shared_tau);
       if (seen > list.tau) list.tau = seen;
-      if (__ballot(mine >= (uint32_t)(list.tau >> 32))) {
+      uint64_t hit = __ballot(mine >= (uint32_t)(list.tau >> 32));
+      while (hit) {
+        const int r = __builtin_popcountll(hit & ((1ull << lane) - 1));
+        if ((hit >> lane & 1) && r < 4) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int64_t p = at + ((i / kVec) * kWave + lane) * kVec + i % kVec;
-          const uint64_t key = ((uint64_t)ordered(x[i]) << 32) | (uint32_t)~(uint32_t)(p - skew);
-          list.add(x[i] == x[i] && key >= list.tau, key, a.top);
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4*>(&picked[wave][16 * r + 4 * i]) = f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+          picked_lane[wave][r] = lane;
+        }
+        const int n = __builtin_popcountll(hit);
+        asm volatile("" ::: "memory");
+        const float v = picked[wave][lane];
+        const int from = picked_lane[wave][lane >> 4], i = lane & 15;
+        asm volatile("" ::: "memory");
+        const int64_t p = at + ((i / kVec) * kWave + from) * kVec + i % kVec;
+        const uint64_t key = ((uint64_t)ordered(v) << 32) | (uint32_t)~(uint32_t)(p - skew);
+        list.add(lane >> 4 < n && v == v && key >= list.tau, key, a.top);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) hit &= hit - 1;
+      }
+    }
+  };
+
+  // Whole blocks by 16-byte loads, the next one's on their way while one is
+  // consumed; the row's edges value by value.
+  constexpr int kStride = kLpWaves * kLpBlock;
+  const auto whole = [&](int64_t at) { return at >= skew && at + kLpBlock <= hi; };
+  const int64_t mine0 = lo + wave * kLpBlock;
+  const int64_t safe = whole(mine0) ? mine0 : mine0 + kStride;   // a whole block of this wave, if it has one
+  uint4 raw[kLoads];
+  const auto request = [&](int64_t at) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < kLoads; ++v) raw[v] = ld_stream_u4(base, (size_t)(at + (v * kWave + lane) * kVec) * sizeof(T));
+  };
+  const auto widened = [&](float (&x)[16]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < kLoads; ++v) {
+      const uint32_t w[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+          x[v * kVec + 2 * i] = bf16_lo(w[i]);
+          x[v * kVec + 2 * i + 1] = bf16_hi(w[i]);
+        } else {
+          x[v * kVec + i] = __uint_as_float(w[i]);
         }
       }
     }
+  };
+  const bool has_whole = whole(safe);
+  if (has_whole) request(safe);
+#pragma unroll 1
+  for (int64_t at = safe; has_whole && whole(at); at += kStride) {
+    float x[16];
+    widened(x);
+    request(whole(at + kStride) ? at + kStride : safe);   // the last round reads a block again: no branch
+    consume(x, at);
+  }
+#pragma unroll 1
+  for (int64_t at = mine0; at < hi; at += kStride) {
+    if (whole(at)) {   // on to the edge behind the whole blocks
+      at += (hi - kLpBlock - at) / kStride * kStride;
+      continue;
+    }
+    float x[16];
+#pragma unroll
+    for (int v = 0; v < kLoads; ++v)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int64_t p = at + (v * kWave + lane) * kVec + i;
+        x[v * kVec + i] = p >= skew && p < hi ? lp_load<T>(base, p) : -__builtin_inff();
+      }
+    consume(x, at);
   }
 
   // The wave's statistics, then the workgroup's.
@@ -305,7 +377,7 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(LpArgs a) {
   }
   if (lane == 0) wave_stats[wave] = s;
   if constexpr (TOP) {
-    if (list.count > a.top) list.cut(a.top);   // at most 64: one key a lane
+    if (list.count > a.top) list.cut(a.top, a.top < 56 ? a.top + 8 : 64);   // at most 64: one key a lane
   }
   __syncthreads();
   s = wave_stats[0];
@@ -322,7 +394,7 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(LpArgs a) {
     count = kept;
   }
   if (a.segs == 1) {
-    lp_finish<T>(a, t, s, joined, count);
+    lp_finish(a, t, s, target, joined, count);
     return;
   }
   const size_t cell = (size_t)blockIdx.x;
@@ -331,37 +403,46 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(LpArgs a) {
     uint64_t* out = a.seg_keys + cell * a.top;
     for (int i = tid; i < count; i += kLpThreads) {
       const uint64_t key = joined[i];
-      int rank = 0;
-      for (int j = 0; j < count; ++j) rank += joined[j] > key ? 1 : 0;
+      const int rank = lp_rank(joined, count, key);
       if (rank < a.top) out[rank] = key;
     }
     for (int i = count + tid; i < a.top; i += kLpThreads) out[i] = 0;
   }
 }
 
-// Segments of a row joined, one workgroup per row.
+// Segments of a row joined, one workgroup per row: lane i of every wave takes
+// segment i's statistics.
 template <typename T>
 __global__ __launch_bounds__(256) void k_logprobs_join(LpArgs a) {
   __shared__ uint64_t keys[kLpMaxSegs * kLpMaxTop];
+  __shared__ unsigned long long tau;
   __shared__ int kept;
-  const int t = blockIdx.x, tid = threadIdx.x;
-  if (tid == 0) kept = 0;
-  __syncthreads();
-  const LpStats* st = a.seg_stats + (size_t)t * a.segs;
-  LpStats s = st[0];
-  for (int i = 1; i < a.segs; ++i) s = lp_join(s, st[i]);
-  if (a.top > 0) {
-    const uint64_t* k = a.seg_keys + (size_t)t * a.segs * a.top;
-    uint64_t tau = 1;                       // a segment's last key is no larger than the row's
-    for (int i = 0; i < a.segs; ++i) {
-      const uint64_t last = k[(size_t)i * a.top + a.top - 1];
-      tau = last > tau ? last : tau;
-    }
-    for (int i = tid; i < a.segs * a.top; i += 256)
-      if (k[i] >= tau) keys[atomicAdd(&kept, 1)] = k[i];
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1);
+  float target = 0.0f;
+  if (tid == 0) {
+    kept = 0;
+    tau = 1;
+    target = lp_target<T>(a, t);
   }
   __syncthreads();
-  lp_finish<T>(a, t, s, keys, kept);
+  static_assert(kLpMaxSegs == kWave, "a lane a segment");
+  LpStats s{-__builtin_inff(), 0.0f, 0.0f};
+  if (lane < a.segs) s = a.seg_stats[(size_t)t * a.segs + lane];
+  const uint64_t* k = a.seg_keys + (size_t)t * a.segs * a.top;
+  // a segment's last key is no larger than the row's
+  if (a.top > 0 && tid < a.segs) atomicMax(&tau, (unsigned long long)k[(size_t)tid * a.top + a.top - 1]);
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const LpStats o{__shfl_xor(s.m, off), __shfl_xor(s.z, off), __shfl_xor(s.u, off)};
+    s = lp_join(s, o);
+  }
+  __syncthreads();
+  for (int i = tid; i < a.segs * a.top; i += 256) {
+    const uint64_t key = k[i];
+    if (key >= tau) keys[atomicAdd(&kept, 1)] = key;
+  }
+  __syncthreads();
+  lp_finish(a, t, s, target, keys, kept);
 }
 
 template <typename T>
@@ -387,7 +468,7 @@ int logprobs_max_top() { return kLpMaxTop; }
 int logprobs_segments(int64_t tokens, int64_t vocab) {
   if (tokens < 1) return 1;
   const int64_t units = (vocab + 7 + kLpSegUnit - 1) / kLpSegUnit;
-  int64_t want = (512 + tokens - 1) / tokens;
+  int64_t want = (1024 + tokens - 1) / tokens;   // four workgroups a CU
   if (want > units) want = units;
   if (want > kLpMaxSegs) want = kLpMaxSegs;
   if (want <= 1) return 1;
