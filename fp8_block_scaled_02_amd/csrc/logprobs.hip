@@ -13,14 +13,25 @@
 // 64-bit key (the value's ordered bits, then the complement of the place):
 // larger keys are larger values, lower places first among equals, and no
 // two are equal, so any correct selection gives the same answer.  Each wave
-// keeps a list of keys above a threshold that is never above the top-th key
-// of the row: first the top-th largest of its lanes' maxima, then the
-// top-th key of its list whenever that is cut down, shared among the waves.
-// A wave looks at single values only where a lane's maximum reaches the
-// threshold: the values of four such lanes at a time go through LDS to one
-// lane each, so that the wave tests 64 values of interest at once and the
-// step itself pays one comparison a lane.  Rows are cut into segments where there are too few of them to
-// fill the chip, and a second launch joins the segments.
+// lists the keys above a threshold that is never above the top-th key of the
+// row: with w waves, every wave publishes its ceil(top / w)-th largest value
+// so far, and at least `top` values reach the smallest of those.  It follows
+// the row closely (5 of 152 k values: about 20 reach it) and costs a wave a
+// few lane maxima when it finds a larger value.  A wave looks at single
+// values only where a lane's maximum reaches the threshold: the values of
+// four such lanes at a time go through LDS to one lane each, so that the wave
+// tests 64 values of interest at once and a step without any pays one
+// comparison a lane.  A list that fills up all the same (ties, masks) is cut
+// to its largest keys, which gives a second threshold.
+//
+// Rows are cut into segments where there are too few of them to fill the
+// chip, and a second launch joins the segments.
+//
+// Measured, vocabulary 151936, bf16: 2048 rows 108 us without alternatives
+// (5.8 TB/s, which is what one pass of loads reaches), 126 with five (4.9),
+// 143 with twenty; 4 rows 6.8, 11.9 and 20.7 us, of which 6 are the two
+// launches and the chain of one load, one join.  1024 rows of fp32: 103 and
+// 108 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -187,6 +198,60 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
   return ((uint64_t)hi << 32) | lo;
 }
 
+__device__ __forceinline__ uint32_t pick_min(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t pick_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t pick_larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+// Largest value of the wave, in every lane.
+__device__ __forceinline__ uint32_t wave_largest(uint32_t v) {
+  v = pick_max(v, lane_move<0xB1>(v));    // quad_perm [1,0,3,2]
+  v = pick_max(v, lane_move<0x4E>(v));    // quad_perm [2,3,0,1]
+  v = pick_max(v, lane_move<0x141>(v));   // row_half_mirror
+  v = pick_max(v, lane_move<0x140>(v));   // row_mirror
+  const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+  const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+  return pick_max(pick_max(a, b), pick_max(c, d));
+}
+
+// The largest values that a wave has seen, the r-th in lane r.
+struct LpBest {
+  uint32_t mine = 0;
+
+  // Takes in a value a lane (0: none); returns the `want`-th largest (0: not
+  // that many yet).
+  __device__ __forceinline__ uint32_t take(uint32_t v, int want) {
+    const int lane = threadIdx.x & (kWave - 1);
+    uint32_t kept = 0, last = 0;
+    for (int r = 0; r < want; ++r) {
+      last = wave_largest(pick_max(v, mine));
+      if (last == 0) break;
+      const int l = __builtin_ctzll(__ballot(pick_max(v, mine) == last));
+      if (lane == l) {   // one of the lane's two is used up
+        if (v == last)
+          v = 0;
+        else
+          mine = 0;
+      }
+      if (lane == r) kept = last;
+    }
+    mine = kept;
+    return last;
+  }
+};
+
+// The smallest of what the waves have published, as a threshold.
+__device__ __forceinline__ uint64_t least_published(const uint32_t* published) {
+  asm volatile("" ::: "memory");
+  uint32_t least = *(const volatile uint32_t*)&published[threadIdx.x & (kLpWaves - 1)];
+  least = pick_min(least, lane_move<0xB1>(least));
+  least = pick_min(least, lane_move<0x4E>(least));
+  least = pick_min(least, lane_move<0x141>(least));
+  return (uint64_t)__builtin_amdgcn_readfirstlane(least) << 32;
+}
+
 // A wave's list of candidates.
 struct LpList {
   uint64_t* keys;              // LDS, kLpCap words of this wave
@@ -201,17 +266,29 @@ struct LpList {
 #pragma unroll
     for (int r = 0; r < kLpCap / kWave; ++r) k[r] = r * kWave + lane < count ? keys[r * kWave + lane] : 0;
     const uint64_t thr = wave_threshold(k, top, enough);
+    keep(k, thr);
+    raise(thr);
+  }
+  // Drop the keys below the threshold.
+  __device__ __forceinline__ void sweep() {
+    const int lane = threadIdx.x & (kWave - 1);
+    uint64_t k[kLpCap / kWave];
+#pragma unroll
+    for (int r = 0; r < kLpCap / kWave; ++r) k[r] = r * kWave + lane < count ? keys[r * kWave + lane] : 0;
+    keep(k, tau);
+  }
+  __device__ __forceinline__ void keep(const uint64_t (&k)[kLpCap / kWave], uint64_t thr) {
+    const int lane = threadIdx.x & (kWave - 1);
     int kept = 0;
 #pragma unroll
     for (int r = 0; r < kLpCap / kWave; ++r) {
-      const bool keep = k[r] >= thr && k[r] != 0;
-      const uint64_t who = __ballot(keep);
-      if (keep) keys[kept + __builtin_popcountll(who & ((1ull << lane) - 1))] = k[r];
+      const bool stay = k[r] >= thr && k[r] != 0;
+      const uint64_t who = __ballot(stay);
+      if (stay) keys[kept + __builtin_popcountll(who & ((1ull << lane) - 1))] = k[r];
       kept += __builtin_popcountll(who);
     }
     __builtin_amdgcn_wave_barrier();
     count = kept;
-    raise(thr);
   }
   __device__ __forceinline__ void raise(uint64_t t) {
     if (t > tau) {
@@ -222,6 +299,7 @@ struct LpList {
   __device__ __forceinline__ void add(bool want, uint64_t key, int top) {
     const uint64_t who = __ballot(want);
     if (!who) return;
+    if (count > kLpCap - kWave) sweep();
     if (count > kLpCap - kWave) {
       cut(top, kLpCap / 4 > top + 8 ? kLpCap / 4 : top + 8);
       want = want && key >= tau;
@@ -234,26 +312,26 @@ struct LpList {
   }
 };
 
-// One workgroup per row segment.
+// One workgroup per row segment.  With alternatives six waves a SIMD: asked
+// for eight, the lists' state spills to scratch (five of 152 k, 2048 rows:
+// 141 us against 132; fp32, 1024 rows: 168 against 108).
 template <typename T, bool TOP>
-__global__ __launch_bounds__(kLpThreads, 8) void k_logprobs(LpArgs a) {
+__global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) {
   constexpr int kVec = 16 / sizeof(T);       // values of one 16-byte load
   constexpr int kLoads = 16 / kVec;
   __shared__ uint64_t lists[TOP ? kLpWaves * kLpCap : 1];
   __shared__ __attribute__((aligned(16))) float picked[TOP ? kLpWaves : 1][kWave];   // 16 values of four lanes
   __shared__ int picked_lane[TOP ? kLpWaves : 1][4];
   __shared__ uint64_t shared_tau;
+  __shared__ uint32_t published[kLpWaves];
   __shared__ LpStats wave_stats[kLpWaves];
   __shared__ int kept;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs;
-  float target = 0.0f;
   if (tid == 0) {
     shared_tau = kFirstKey;
     kept = 0;
-    target = lp_target<T>(a, t);
   }
-  __syncthreads();
 
   // Places are counted from the 16-byte boundary at or below the row's
   // start, so that every load of whole 16 bytes is aligned; `skew` values
@@ -267,12 +345,26 @@ __global__ __launch_bounds__(kLpThreads, 8) void k_logprobs(LpArgs a) {
 
   LpStats s{-__builtin_inff(), 0.0f, 0.0f};
   LpList list{lists + wave * kLpCap, &shared_tau, kFirstKey, 0};
-  bool first = true;
-  // 1024 values from `at` on, 16 a lane: load v holds those of place (v * 64 + lane) * kVec.
-  const auto consume = [&](const float (&x)[16], int64_t at) __attribute__((always_inline)) {
+  // waves that have values, and of how many each publishes the last
+  const int64_t blocks = (hi - lo + kLpBlock - 1) / kLpBlock;
+  const int active = blocks < kLpWaves ? (int)blocks : kLpWaves;
+  const int want = active > 0 ? (a.top + active - 1) / active : 1;
+  LpBest best;
+  const auto lane_largest = [&](const float (&x)[16], float top) __attribute__((always_inline)) {
+    const uint32_t o = top == top ? ordered(top) : lp_nan_max(x);
+    return o > (uint32_t)((kFirstKey >> 32) - 1) ? o : 0;   // 0: nothing live
+  };
+  const auto largest = [](const float (&x)[16]) __attribute__((always_inline)) {   // NaN if there is one
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = __builtin_elementwise_maximum(top, x[i]);
+    return top;
+  };
+  // 1024 values from `at` on, 16 a lane: load v holds those of place (v * 64 + lane) * kVec.
+  const auto consume = [&](const float (&x)[16], int64_t at) __attribute__((always_inline)) {
+    uint64_t cut = 0;
+    if constexpr (TOP) cut = *(volatile uint64_t*)&shared_tau;   // read ahead of its use
+    const float top = largest(x);
     const float m = __builtin_elementwise_maximum(s.m, top);
     const float down = __builtin_fmaxf((s.m - m) * kLog2E, kMinExp), f = __builtin_amdgcn_exp2f(down);
     float z = 0.0f, u = 0.0f;
@@ -286,15 +378,22 @@ __global__ __launch_bounds__(kLpThreads, 8) void k_logprobs(LpArgs a) {
     s = LpStats{m, __builtin_fmaf(s.z, f, z), __builtin_fmaf(f, __builtin_fmaf(down, s.z, s.u), u)};
 
     if constexpr (TOP) {
-      const uint32_t mine = top == top ? ordered(top) : lp_nan_max(x);
-      if (first) {
-        first = false;
-        const uint32_t k[1] = {mine};
-        list.raise((uint64_t)wave_threshold(k, a.top, a.top + 8) << 32);
+      cut = uniform64(cut);
+      if (cut > list.tau) list.tau = cut;
+      // not below the threshold's value (NaN too: there may be others beside it)
+      uint64_t hit = __ballot(!(top < unordered((uint32_t)(list.tau >> 32))));
+      if (hit) {
+        const uint32_t mine = lane_largest(x, top);
+        hit = __ballot(mine >= (uint32_t)(list.tau >> 32));
+        const uint32_t old = published[wave];
+        if (__ballot(mine > old)) {   // a lane's largest stands for all its values: a bound either way
+          const uint32_t now = best.take(mine, want);
+          if (now > old) {
+            if (lane == 0) published[wave] = now;
+            list.raise(least_published(published));
+          }
+        }
       }
-      const uint64_t seen = uniform64(*(volatile uint64_t*)&shared_tau);
-      if (seen > list.tau) list.tau = seen;
-      uint64_t hit = __ballot(mine >= (uint32_t)(list.tau >> 32));
       while (hit) {
         const int r = __builtin_popcountll(hit & ((1ull << lane) - 1));
         if ((hit >> lane & 1) && r < 4) {
@@ -343,8 +442,33 @@ __global__ __launch_bounds__(kLpThreads, 8) void k_logprobs(LpArgs a) {
       }
     }
   };
+  const auto edge = [&](float (&x)[16], int64_t at) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < kLoads; ++v)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int64_t p = at + (v * kWave + lane) * kVec + i;
+        x[v * kVec + i] = p >= skew && p < hi ? lp_load<T>(base, p) : -__builtin_inff();
+      }
+  };
   const bool has_whole = whole(safe);
   if (has_whole) request(safe);
+  if constexpr (TOP) {
+    // every wave's first values give the first threshold
+    uint32_t now = wave < active ? 0 : 0xFFFFFFFFu;   // a wave without values does not count
+    if (wave < active) {
+      float x[16];
+      if (has_whole)
+        widened(x);
+      else
+        edge(x, mine0);
+      LpBest first;
+      now = first.take(lane_largest(x, largest(x)), want);
+    }
+    if (lane == 0) published[wave] = now;
+    __syncthreads();
+    list.raise(least_published(published));
+  }
 #pragma unroll 1
   for (int64_t at = safe; has_whole && whole(at); at += kStride) {
     float x[16];
@@ -359,27 +483,25 @@ __global__ __launch_bounds__(kLpThreads, 8) void k_logprobs(LpArgs a) {
       continue;
     }
     float x[16];
-#pragma unroll
-    for (int v = 0; v < kLoads; ++v)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const int64_t p = at + (v * kWave + lane) * kVec + i;
-        x[v * kVec + i] = p >= skew && p < hi ? lp_load<T>(base, p) : -__builtin_inff();
-      }
+    edge(x, at);
     consume(x, at);
   }
 
-  // The wave's statistics, then the workgroup's.
+  // The given token's logit is on its way while the statistics are joined:
+  // the wave's, then the workgroup's.
+  const float target = tid == 0 && a.segs == 1 ? lp_target<T>(a, t) : 0.0f;
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
     const LpStats o{__shfl_xor(s.m, off), __shfl_xor(s.z, off), __shfl_xor(s.u, off)};
     s = lp_join(s, o);
   }
   if (lane == 0) wave_stats[wave] = s;
-  if constexpr (TOP) {
-    if (list.count > a.top) list.cut(a.top, a.top < 56 ? a.top + 8 : 64);   // at most 64: one key a lane
-  }
   __syncthreads();
+  if constexpr (TOP) {   // the final threshold, the same in every wave
+    list.tau = pick_larger(shared_tau, least_published(published));
+    list.sweep();
+    if (list.count > kWave) list.cut(a.top, kWave);   // at most 64: one key a lane
+  }
   s = wave_stats[0];
 #pragma unroll
   for (int w = 1; w < kLpWaves; ++w) s = lp_join(s, wave_stats[w]);
@@ -387,8 +509,8 @@ __global__ __launch_bounds__(kLpThreads, 8) void k_logprobs(LpArgs a) {
   uint64_t* joined = lists;
   if constexpr (TOP) {
     const uint64_t key = lane < list.count ? list.keys[lane] : 0;
-    const bool keep = key >= shared_tau;
     __syncthreads();
+    const bool keep = key >= shared_tau && key != 0;
     if (keep) joined[atomicAdd(&kept, 1)] = key;
     __syncthreads();
     count = kept;
@@ -418,28 +540,37 @@ __global__ __launch_bounds__(256) void k_logprobs_join(LpArgs a) {
   __shared__ unsigned long long tau;
   __shared__ int kept;
   const int t = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1);
-  float target = 0.0f;
+  static_assert(kLpMaxSegs == kWave, "a lane a segment");
+  // everything that is read, at once: the first two keys of a thread, each
+  // segment's last (none is larger than the row's last)
+  const int cells = a.segs * a.top;
+  const uint64_t* k = a.seg_keys + (size_t)t * cells;
+  LpStats s{-__builtin_inff(), 0.0f, 0.0f};
+  uint64_t last = 0, key[2] = {0, 0};
+  if (lane < a.segs) s = a.seg_stats[(size_t)t * a.segs + lane];
+  if (tid < a.segs && a.top > 0) last = k[(size_t)tid * a.top + a.top - 1];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (tid + 256 * j < cells) key[j] = k[tid + 256 * j];
+  const float target = tid == 0 ? lp_target<T>(a, t) : 0.0f;
   if (tid == 0) {
     kept = 0;
     tau = 1;
-    target = lp_target<T>(a, t);
   }
   __syncthreads();
-  static_assert(kLpMaxSegs == kWave, "a lane a segment");
-  LpStats s{-__builtin_inff(), 0.0f, 0.0f};
-  if (lane < a.segs) s = a.seg_stats[(size_t)t * a.segs + lane];
-  const uint64_t* k = a.seg_keys + (size_t)t * a.segs * a.top;
-  // a segment's last key is no larger than the row's
-  if (a.top > 0 && tid < a.segs) atomicMax(&tau, (unsigned long long)k[(size_t)tid * a.top + a.top - 1]);
+  if (last != 0) atomicMax(&tau, (unsigned long long)last);
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
     const LpStats o{__shfl_xor(s.m, off), __shfl_xor(s.z, off), __shfl_xor(s.u, off)};
     s = lp_join(s, o);
   }
   __syncthreads();
-  for (int i = tid; i < a.segs * a.top; i += 256) {
-    const uint64_t key = k[i];
-    if (key >= tau) keys[atomicAdd(&kept, 1)] = key;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (key[j] >= tau) keys[atomicAdd(&kept, 1)] = key[j];
+  for (int i = tid + 512; i < cells; i += 256) {
+    const uint64_t more = k[i];
+    if (more >= tau) keys[atomicAdd(&kept, 1)] = more;
   }
   __syncthreads();
   lp_finish(a, t, s, target, keys, kept);
