@@ -159,15 +159,26 @@ def _check(status: int, what: str) -> None:
         raise Fp8wError(status, what)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _current_handle() -> int:
+    """The current stream's handle, without the Stream object (0.3 us, not 2.7)."""
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _stream_handle(stream) -> Optional[int]:
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_handle()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -175,7 +186,7 @@ def _require(t, dtypes, what: str, dims: int):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what}: must be a GPU tensor (libfp8w has no CPU path)")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
@@ -198,8 +209,11 @@ def mx_scale_shape(n: int, k: int):
 
 def scale_shape(fmt: str, n: int, k: int):
     """Shape of the scale buffer of an [n, k] weight in format ``fmt``."""
-    return {"block": block_scale_shape(n, k), "mx": mx_scale_shape(n, k),
-            "block_bf16": block_scale_shape(n, k), "row": (n,), "tensor": (1,)}[fmt]
+    if fmt in ("block", "block_bf16"):
+        return block_scale_shape(n, k)
+    if fmt == "mx":
+        return mx_scale_shape(n, k)
+    return {"row": (n,), "tensor": (1,)}[fmt]
 
 
 def _scale_dtype(torch, fmt: str):
@@ -704,7 +718,7 @@ def _logits(t, what: str):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what}: must be a GPU tensor (libfp8w has no CPU path)")
     if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
         raise TypeError(f"{what}: dtype {t.dtype} is neither bfloat16 nor float32")
@@ -723,7 +737,7 @@ def _buffer(t, shape, dtype, device, what: str):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _require(t, (dtype,), what, len(shape))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
     return t
 
@@ -732,13 +746,13 @@ def _launch_stream(stream, *owned):
     """The stream's handle.  Tensors made for this call belong to the current
     stream: used on another, they are recorded there, so that their memory is
     not handed out again before the kernels have run."""
-    torch = _torch()
+    handle = _current_handle()
     if stream is None:
-        return int(torch.cuda.current_stream().cuda_stream)
-    handle = _stream_handle(stream)
-    if handle != int(torch.cuda.current_stream().cuda_stream):
+        return handle
+    current, handle = handle, _stream_handle(stream)
+    if handle != current:
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(handle)
+            stream = _torch().cuda.ExternalStream(handle)
         for t in owned:
             if t is not None:
                 t.record_stream(stream)
@@ -798,7 +812,7 @@ def fp8w_gemm_experts(x, codes, scales, offsets, rows=None, fmt: str = "block", 
         raise ValueError(f"fp8w_gemm_experts: x has {x.shape[1]} columns, the weights {k}")
     want = (e, *scale_shape(fmt, n, k))
     _require(scales, (_scale_dtype(torch, fmt),), "scales", len(want))
-    if tuple(scales.shape) != want:
+    if scales.shape != want:
         raise ValueError(f"fp8w_gemm_experts: {fmt} scales must be {want}, got {tuple(scales.shape)}")
     if offsets.shape[0] != e + 1:
         raise ValueError(f"offsets: expected shape {(e + 1,)}, got {tuple(offsets.shape)}")
@@ -810,7 +824,7 @@ def fp8w_gemm_experts(x, codes, scales, offsets, rows=None, fmt: str = "block", 
         y = torch.empty((slots, n_out), dtype=torch.bfloat16, device=x.device)
     else:
         _require(y, _bf16_like(torch), "y", 2)
-        if tuple(y.shape) != (slots, n_out):
+        if y.shape != (slots, n_out):
             raise ValueError(f"y: expected shape {(slots, n_out)}, got {tuple(y.shape)}")
     _check(lib().fp8w_gemm_experts(x.data_ptr(), x.shape[0], None if rows is None else rows.data_ptr(),
                                    offsets.data_ptr(), e, slots, codes.data_ptr(), scales.data_ptr(), fid, n, k,
@@ -832,7 +846,7 @@ def fp8w_combine_experts(y, weights, slots, out=None, stream=None):
         out = torch.empty((t, n), dtype=torch.bfloat16, device=y.device)
     else:
         _require(out, _bf16_like(torch), "out", 2)
-        if tuple(out.shape) != (t, n):
+        if out.shape != (t, n):
             raise ValueError(f"out: expected shape {(t, n)}, got {tuple(out.shape)}")
     _check(lib().fp8w_combine_experts(y.data_ptr(), y.shape[0], weights.data_ptr(), slots.data_ptr(), t, k, n,
                                       out.data_ptr(), _launch_stream(stream, out)), "fp8w_combine_experts")
@@ -888,7 +902,7 @@ def fp8w_logprobs(logits, targets=None, top: int = 0, logprob=None, entropy=None
     top_ids = _buffer(top_ids, (t, top), torch.int32, dev, "top_ids")
     top_logprobs = _buffer(top_logprobs, (t, top), f32, dev, "top_logprobs")
     if workspace is None:
-        need = int(lib().fp8w_logprobs_workspace_bytes(t, v, top))
+        need = lib().fp8w_logprobs_workspace_bytes(t, v, top)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _check(lib().fp8w_logprobs(
