@@ -23,8 +23,18 @@
 // below its own, the group's count the number of all.  Above 32 tokens a
 // second launch adds the groups before its own to each expert's offset.
 //
+// A row of 16 lanes takes a token of up to 256 experts and 16 choices, so a
+// wave's step of the choice serves four tokens and needs no lane reads
+// (8192 tokens, 8 of 128 experts: 11.6 us with a wave to a token, 5.5 with a
+// row; then 4.1 for the places, which wait for two rounds of loads out of L2
+// and two scans).  Both calls are bound by their chains of latencies: the
+// 2.2 MB they move take under 1 us.
+//
 // Combination.  out[t][c] = bf16( sum_j w[t][j] * y[slots[t][j]][c] ), fp32,
-// j ascending: one pass over the chosen rows, bound by HBM.
+// j ascending: one pass over the chosen rows, bound by HBM.  8 rows of 2048
+// columns for each of 8192 tokens: 64.7 us with the rows' loads behind a test
+// of each slot, 60.0 with eight of them leaving at once, 51.5 (5.8 TB/s) with
+// non-temporal loads and stores, since no row is read twice.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -62,24 +72,43 @@ __device__ __forceinline__ double lane_value(double v, int l) {
 }
 __device__ __forceinline__ float pick_max(float a, float b) { return __builtin_fmaxf(a, b); }
 __device__ __forceinline__ double pick_max(double a, double b) { return __builtin_fmax(a, b); }
+template <int CTRL>
+__device__ __forceinline__ int dpp_min(int v) {
+  const int o = __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+  return v < o ? v : o;
+}
 
-// Reductions over the wave, the result in every lane: four row steps, then
-// the four rows' values by lane reads.
-template <typename T>
-__device__ __forceinline__ T wave_max(T v) {
+// Reductions over L = 16 or 64 neighbouring lanes, the result in each of
+// them: four steps within rows of 16, then the four rows' values by lane
+// reads.
+template <int L, typename T>
+__device__ __forceinline__ T group_max(T v) {
   v = pick_max(v, dpp_mov<0xB1>(v));    // quad_perm [1,0,3,2]
   v = pick_max(v, dpp_mov<0x4E>(v));    // quad_perm [2,3,0,1]
   v = pick_max(v, dpp_mov<0x141>(v));   // row_half_mirror
   v = pick_max(v, dpp_mov<0x140>(v));   // row_mirror
+  if constexpr (L == 16) return v;
   return pick_max(pick_max(lane_value(v, 0), lane_value(v, 16)), pick_max(lane_value(v, 32), lane_value(v, 48)));
 }
-template <typename T>
-__device__ __forceinline__ T wave_total(T v) {
+template <int L, typename T>
+__device__ __forceinline__ T group_total(T v) {
   v += dpp_mov<0xB1>(v);
   v += dpp_mov<0x4E>(v);
   v += dpp_mov<0x141>(v);
   v += dpp_mov<0x140>(v);
+  if constexpr (L == 16) return v;
   return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+template <int L>
+__device__ __forceinline__ int group_min(int v) {
+  v = dpp_min<0xB1>(v);
+  v = dpp_min<0x4E>(v);
+  v = dpp_min<0x141>(v);
+  v = dpp_min<0x140>(v);
+  if constexpr (L == 16) return v;
+  const int a = min(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16));
+  const int b = min(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48));
+  return min(a, b);
 }
 
 struct RouteArgs {
@@ -102,92 +131,90 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t at) {
   return bf16_lo(ld_global<uint16_t>(p, (size_t)at * 2));
 }
 
-// One token's choice: lane j (< the number chosen, returned) ends with the
-// j-th expert and its weight.
-template <typename T, typename Key, int R>
-__device__ __forceinline__ int route_token(const RouteArgs& a, int t, int& my_id, float& my_w) {
+// A token's choice by L lanes with R experts each (expert r * L + lane of
+// the group): lane j of the group ends with the j-th expert (-1: none) and
+// its weight.  A step takes the largest key left, and among its equals the
+// lowest expert.
+template <typename T, typename Key, int L, int R>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_id, float& my_w) {
   constexpr bool kBias = sizeof(Key) == 8;
-  const int lane = threadIdx.x & (kWave - 1);
+  const int lane = threadIdx.x & (L - 1);
   const float ninf = -__builtin_inff();
   float x[R];
   Key key[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int e = r * kWave + lane;
-    const float v = e < a.experts ? load_logit<T>(a.logits, (int64_t)t * a.stride + e) : ninf;
-    x[r] = v == v ? v : ninf;
+    const int e = r * L + lane;
+    const float v = load_logit<T>(a.logits, (int64_t)t * a.stride + (e < a.experts ? e : 0));
+    x[r] = v == v && e < a.experts ? v : ninf;
   }
   float top = x[0];
 #pragma unroll
   for (int r = 1; r < R; ++r) top = __builtin_fmaxf(top, x[r]);
-  top = wave_max(top);
+  top = group_max<L>(top);
+  float z = 0.0f;   // of all experts' terms
+  if (a.score == 0 && !a.renorm) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) z += x[r] > ninf ? expf(x[r] - top) : 0.0f;
+    z = group_total<L>(z);
+  }
   if constexpr (kBias) {
-    double ex[R], z = 0.0;
+    double zd = 0.0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      ex[r] = a.score == 0 ? exp((double)x[r] - (double)top) : 1.0 / (1.0 + exp(-(double)x[r]));
-      z += x[r] > ninf ? ex[r] : 0.0;
+      key[r] = a.score == 0 ? exp((double)x[r] - (double)top) : 1.0 / (1.0 + exp(-(double)x[r]));
+      zd += x[r] > ninf ? key[r] : 0.0;
     }
-    z = a.score == 0 ? wave_total(z) : 1.0;
+    zd = a.score == 0 ? group_total<L>(zd) : 1.0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int e = r * kWave + lane;
-      const double k = x[r] > ninf ? ex[r] / z + (double)ld_global<float>(a.bias, (size_t)e * 4) : (double)ninf;
-      key[r] = k == k ? k : (double)ninf;
+      const int e = r * L + lane;
+      const double k = key[r] / zd + (double)ld_global<float>(a.bias, (size_t)(e < a.experts ? e : 0) * 4);
+      key[r] = x[r] > ninf && k == k ? k : (double)ninf;
     }
   } else {
 #pragma unroll
     for (int r = 0; r < R; ++r) key[r] = x[r];
   }
 
-  int chosen = 0;
   my_id = -1;
   float my_x = ninf;
   for (int j = 0; j < a.top_k; ++j) {
     Key best = key[0];
 #pragma unroll
     for (int r = 1; r < R; ++r) best = pick_max(best, key[r]);
-    best = wave_max(best);
-    if (!(best > (Key)ninf)) break;
-    bool found = false;
+    best = group_max<L>(best);
+    const bool live = best > (Key)ninf;
+    if (!__ballot(live)) break;   // no token of the wave has an expert left
+    int first = kRouteMaxE;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint64_t hit = __ballot(key[r] == best);
-      if (!found && hit) {
-        found = true;
-        const int l = __builtin_ctzll(hit);
-        const float v = lane_value(x[r], l);
-        if (lane == l) key[r] = (Key)ninf;
-        if (lane == j) {
-          my_id = r * kWave + l;
-          my_x = v;
-        }
-      }
+    for (int r = R - 1; r >= 0; --r) first = key[r] == best ? r * L + lane : first;
+    const int id = group_min<L>(first);
+#pragma unroll
+    for (int r = 0; r < R; ++r) key[r] = r * L + lane == id ? (Key)ninf : key[r];
+    if (live && lane == j) {
+      my_id = id;
+      if constexpr (!kBias) my_x = (float)best;
     }
-    ++chosen;
   }
 
-  const bool live = lane < chosen;
+  const bool live = my_id >= 0;
+  if constexpr (kBias) {
+    if (live) my_x = load_logit<T>(a.logits, (int64_t)t * a.stride + my_id);
+  }
   float w;
   if (a.score == 0) {
     w = live ? expf(my_x - top) : 0.0f;
-    float z = w;
-    if (!a.renorm) {
-      z = 0.0f;
-#pragma unroll
-      for (int r = 0; r < R; ++r) z += x[r] > ninf ? expf(x[r] - top) : 0.0f;
-    }
-    z = wave_total(z);
+    if (a.renorm) z = group_total<L>(w);
     w = live ? w / z : 0.0f;
   } else {
     w = live ? 1.0f / (1.0f + expf(-my_x)) : 0.0f;
     if (a.renorm) {
-      const float z = wave_total(w);
-      w = z > 0.0f ? w / z : 0.0f;   // every chosen score underflowed: no weight
+      const float sum = group_total<L>(w);
+      w = sum > 0.0f ? w / sum : 0.0f;   // every chosen score underflowed: no weight
     }
   }
   my_w = w * a.scale;
-  return chosen;
 }
 
 // Exclusive prefix sums of count[0..E) in place, E <= 1024, by the whole
@@ -218,23 +245,25 @@ __device__ __forceinline__ int scan_experts(int* count, int experts, int* wave_s
 
 // The choice of 32 tokens, and their places among them.  ONE: this group is
 // the whole call, so the map is finished here.
-template <typename T, typename Key, int R, bool ONE>
+template <typename T, typename Key, int L, int R, bool ONE>
 __global__ __launch_bounds__(kRouteThreads) void k_route_choose(RouteArgs a) {
   __shared__ uint32_t mask[kRouteMaxE];
   __shared__ int16_t chosen_id[kRouteTokens * kRouteMaxK];
   __shared__ int count[ONE ? kRouteMaxE : 1];
   __shared__ int wave_sums[kRouteWaves];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid & (L - 1);
   const int t0 = blockIdx.x * kRouteTokens;
   const int nt = min(kRouteTokens, a.tokens - t0);
   for (int e = tid; e < a.experts; e += kRouteThreads) mask[e] = 0;
   __syncthreads();
 #pragma unroll 1
-  for (int i = wave; i < nt; i += kRouteWaves) {
+  for (int first = 0; first < nt; first += kRouteThreads / L) {
+    const int i = first + tid / L;
+    if (L == kWave ? i >= nt : i - i % (kWave / L) >= nt) break;   // a wave's lanes stay together
     int id;
     float w;
-    route_token<T, Key, R>(a, t0 + i, id, w);
-    if (lane < a.top_k) {
+    route_token<T, Key, L, R>(a, t0 + min(i, nt - 1), id, w);
+    if (i < nt && lane < a.top_k) {
       const int64_t at = (int64_t)(t0 + i) * a.top_k + lane;
       a.ids[at] = id;
       a.weights[at] = w;
@@ -329,67 +358,107 @@ __global__ void k_route_empty(int32_t* offsets, int experts) {
   if (e <= experts) offsets[e] = 0;
 }
 
-template <typename T, typename Key, int R>
+template <typename T, typename Key, int L, int R>
 hipError_t route_launch(const RouteArgs& a, hipStream_t stream) {
   const int groups = (a.tokens + kRouteTokens - 1) / kRouteTokens;
   if (groups == 1) {
-    k_route_choose<T, Key, R, true><<<1, kRouteThreads, 0, stream>>>(a);
+    k_route_choose<T, Key, L, R, true><<<1, kRouteThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
-  k_route_choose<T, Key, R, false><<<groups, kRouteThreads, 0, stream>>>(a);
+  k_route_choose<T, Key, L, R, false><<<groups, kRouteThreads, 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   k_route_place<<<groups, kRouteThreads, 0, stream>>>(a, groups);
   return hipGetLastError();
 }
 
+// A row of 16 lanes to a token where a lane can hold its experts and one
+// choice of it: four tokens share a wave's instructions, and no value has to
+// cross rows.
 template <typename T, typename Key>
 hipError_t route_by_experts(const RouteArgs& a, hipStream_t stream) {
-  if (a.experts <= 64) return route_launch<T, Key, 1>(a, stream);
-  if (a.experts <= 128) return route_launch<T, Key, 2>(a, stream);
-  if (a.experts <= 256) return route_launch<T, Key, 4>(a, stream);
-  return route_launch<T, Key, 16>(a, stream);
+  if (a.top_k <= 16) {
+    if (a.experts <= 64) return route_launch<T, Key, 16, 4>(a, stream);
+    if (a.experts <= 128) return route_launch<T, Key, 16, 8>(a, stream);
+    if (a.experts <= 256) return route_launch<T, Key, 16, 16>(a, stream);
+  }
+  if (a.experts <= 256) return route_launch<T, Key, 64, 4>(a, stream);
+  return route_launch<T, Key, 64, 16>(a, stream);
 }
 
-// out = sum of a token's chosen rows, VEC columns per thread.
+// out = sum of a token's chosen rows: a wave takes 64 * VEC columns of one
+// token.  Its lanes hold the token's slots and weights, and the rows' loads
+// leave eight at a time.
 template <int VEC>
-__global__ __launch_bounds__(256) void k_combine(const uint16_t* y, int64_t slot_rows, const float* weights,
-                                                 const int32_t* slots, int64_t tokens, int top_k, int n,
-                                                 uint16_t* out) {
-  const int cols = n / VEC;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t t = at / cols;
-  if (t >= tokens) return;
-  const int c = (int)(at - t * cols) * VEC;
+struct CombineSum {
+  const uint16_t* y;
+  int64_t slot_rows;
+  int n, c, slot;      // this lane's column, and slot `lane`
+  float weight;
   float acc[VEC];
+
+  template <int N>
+  __device__ __forceinline__ void rows(int j) {
+    uint4 v[N];
+    float w[N];
+    bool valid[N];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < top_k; ++j) {
-    const int slot = ld_global<int32_t>(slots, (size_t)(t * top_k + j) * 4);
-    if (slot < 0 || slot >= slot_rows) continue;
-    const float w = ld_global<float>(weights, (size_t)(t * top_k + j) * 4);
-    const size_t from = ((size_t)slot * n + c) * 2;
-    if constexpr (VEC == 8) {
-      const uint4 v = ld_global_u4(y, from);
-      const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < N; ++i) {
+      const int s = __builtin_amdgcn_readlane(slot, j + i);
+      valid[i] = s >= 0 && s < slot_rows;
+      const size_t from = ((size_t)(valid[i] ? s : 0) * n + c) * 2;   // row 0 is there: checked by the caller
+      if constexpr (VEC == 8)
+        v[i] = ld_stream_u4(y, from);
+      else
+        v[i].x = ld_global<uint16_t>(y, from);
+      w[i] = valid[i] ? lane_value(weight, j + i) : 0.0f;
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] = __builtin_fmaf(w, bf16_lo(d[i]), acc[2 * i]);
-        acc[2 * i + 1] = __builtin_fmaf(w, bf16_hi(d[i]), acc[2 * i + 1]);
+    for (int i = 0; i < N; ++i) {
+      const uint32_t d[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int q = 0; q < (VEC + 1) / 2; ++q) {
+        const uint32_t pair = valid[i] ? d[q] : 0;
+        acc[2 * q] = __builtin_fmaf(w[i], bf16_lo(pair), acc[2 * q]);
+        if constexpr (VEC > 1) acc[2 * q + 1] = __builtin_fmaf(w[i], bf16_hi(pair), acc[2 * q + 1]);
       }
-    } else {
-      acc[0] = __builtin_fmaf(w, bf16_lo(ld_global<uint16_t>(y, from)), acc[0]);
     }
   }
+};
+
+template <int VEC>
+__global__ __launch_bounds__(256) void k_combine(const uint16_t* y, int64_t slot_rows, const float* weights,
+                                                 const int32_t* slots, uint32_t pieces, uint32_t per_token, int top_k,
+                                                 int n, uint16_t* out) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const uint32_t piece = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);
+  if (piece >= pieces) return;
+  const uint32_t t = piece / per_token;
+  const uint32_t c = ((piece - t * per_token) * kWave + lane) * VEC;   // may pass n, and 2^31 with it
+  const bool inside = c < (uint32_t)n;
+  CombineSum<VEC> sum{y, slot_rows, n, inside ? (int)c : 0, -1, 0.0f, {}};
+  if (lane < top_k) {
+    sum.slot = ld_global<int32_t>(slots, ((size_t)t * top_k + lane) * 4);
+    sum.weight = ld_global<float>(weights, ((size_t)t * top_k + lane) * 4);
+  }
+  if (slot_rows > 0) {
+    int j = 0;
+    for (; j + 8 <= top_k; j += 8) sum.template rows<8>(j);
+    if (j + 4 <= top_k) {
+      sum.template rows<4>(j);
+      j += 4;
+    }
+    for (; j < top_k; ++j) sum.template rows<1>(j);
+  }
+  if (!inside) return;
   const size_t to = ((size_t)t * n + c) * 2;
   if constexpr (VEC == 8) {
     u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = bf16_pair(acc[2 * i], acc[2 * i + 1]);
-    st_global<u32x4>(out, to, v);
+    for (int i = 0; i < 4; ++i) v[i] = bf16_pair(sum.acc[2 * i], sum.acc[2 * i + 1]);
+    st_stream_u4(out, to, v);
   } else {
-    st_global<uint16_t>(out, to, (uint16_t)f32_to_bf16_rne(acc[0]));
+    st_global<uint16_t>(out, to, (uint16_t)f32_to_bf16_rne(sum.acc[0]));
   }
 }
 
@@ -414,16 +483,23 @@ hipError_t launch_route_experts(const RouteCall& c, hipStream_t stream) {
   return c.bias ? route_by_experts<uint16_t, double>(a, stream) : route_by_experts<uint16_t, float>(a, stream);
 }
 
-int64_t combine_blocks(int64_t tokens, int64_t n, bool vec) { return (tokens * (vec ? n / 8 : n) + 255) / 256; }
+int64_t combine_blocks(int64_t tokens, int64_t n, bool vec) {
+  const int64_t columns = kWave * (vec ? 8 : 1);
+  return (tokens * ((n + columns - 1) / columns) + 3) / 4;
+}
 
 hipError_t launch_combine_experts(const uint16_t* y, int64_t slot_rows, const float* weights, const int32_t* slots,
                                   int64_t tokens, int64_t top_k, int64_t n, uint16_t* out, bool vec,
                                   hipStream_t stream) {
   const unsigned blocks = (unsigned)combine_blocks(tokens, n, vec);
+  const int64_t columns = kWave * (vec ? 8 : 1), per_token = (n + columns - 1) / columns;
+  const uint32_t pieces = (uint32_t)(tokens * per_token);
   if (vec)
-    k_combine<8><<<blocks, 256, 0, stream>>>(y, slot_rows, weights, slots, tokens, (int)top_k, (int)n, out);
+    k_combine<8><<<blocks, 256, 0, stream>>>(y, slot_rows, weights, slots, pieces, (uint32_t)per_token, (int)top_k,
+                                             (int)n, out);
   else
-    k_combine<1><<<blocks, 256, 0, stream>>>(y, slot_rows, weights, slots, tokens, (int)top_k, (int)n, out);
+    k_combine<1><<<blocks, 256, 0, stream>>>(y, slot_rows, weights, slots, pieces, (uint32_t)per_token, (int)top_k,
+                                             (int)n, out);
   return hipGetLastError();
 }
 
