@@ -29,7 +29,7 @@
 //
 // Measured, vocabulary 151936, bf16: 2048 rows 108 us without alternatives
 // (5.8 TB/s, which is what one pass of loads reaches), 126 with five (4.9),
-// 143 with twenty; 4 rows 6.8, 11.9 and 20.7 us, of which 6 are the two
+// 143 with twenty; 4 rows 6.7, 11.0 and 13.5 us, of which 6 are the two
 // launches and the chain of one load, one join.  1024 rows of fp32: 103 and
 // 108 us.
 #include <hip/hip_runtime.h>
@@ -537,18 +537,24 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) 
 template <typename T>
 __global__ __launch_bounds__(256) void k_logprobs_join(LpArgs a) {
   __shared__ uint64_t keys[kLpMaxSegs * kLpMaxTop];
-  __shared__ unsigned long long tau;
+  __shared__ uint64_t marks[kWave];
+  __shared__ uint64_t tau;
   __shared__ int kept;
   const int t = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1);
   static_assert(kLpMaxSegs == kWave, "a lane a segment");
-  // everything that is read, at once: the first two keys of a thread, each
-  // segment's last (none is larger than the row's last)
+  // Everything that is read, at once: the first two keys of a thread, and
+  // each segment's r-th.  The m-th largest of those, m = ceil(top / r), is
+  // reached by m * r keys, `top` at least; r = ceil(top / segments) lets the
+  // fewest keys through (20 of 19 segments: about 32 on average, where the
+  // largest of the segments' last keys lets 230 of 380 through and costs 6 us
+  // in ranks).
+  const int r = max((a.top + a.segs - 1) / a.segs, 1), m = (a.top + r - 1) / r;
   const int cells = a.segs * a.top;
   const uint64_t* k = a.seg_keys + (size_t)t * cells;
   LpStats s{-__builtin_inff(), 0.0f, 0.0f};
-  uint64_t last = 0, key[2] = {0, 0};
+  uint64_t mark = 0, key[2] = {0, 0};
   if (lane < a.segs) s = a.seg_stats[(size_t)t * a.segs + lane];
-  if (tid < a.segs && a.top > 0) last = k[(size_t)tid * a.top + a.top - 1];
+  if (tid < a.segs && a.top > 0) mark = k[(size_t)tid * a.top + r - 1];
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     if (tid + 256 * j < cells) key[j] = k[tid + 256 * j];
@@ -557,13 +563,15 @@ __global__ __launch_bounds__(256) void k_logprobs_join(LpArgs a) {
     kept = 0;
     tau = 1;
   }
-  __syncthreads();
-  if (last != 0) atomicMax(&tau, (unsigned long long)last);
+  if (tid < kWave) marks[tid] = mark;
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
     const LpStats o{__shfl_xor(s.m, off), __shfl_xor(s.z, off), __shfl_xor(s.u, off)};
     s = lp_join(s, o);
   }
+  __syncthreads();
+  // no two live keys are equal; a mark of 0 (fewer live than r) leaves tau at 1
+  if (mark != 0 && lp_rank(marks, a.segs, mark) == m - 1) tau = mark;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 2; ++j)
