@@ -41,7 +41,7 @@ PEAK_BF16 = 2.5e15         # MI355X dense bf16 MFMA, flop/s
 # kernel, launch-plan and helper sources); any change to those reports
 # traffic as null until the counters are retaken.
 COUNTED_TRAFFIC = {
-    "sources_sha256": "da643c86f7ff702dad9247d891e2c9480ebec2cce44877578dd155c9968fdd93",
+    "sources_sha256": "b16d4b96bd20e19a3c605ab0f24384cc18a457befc6262f30508dfb91cbbc20e",
     "bytes_per_launch": 1340.30e6,
 }
 TRAFFIC_SOURCES = ('gemv.hip', 'device.hpp', 'internal.hpp', 'api.cpp')
