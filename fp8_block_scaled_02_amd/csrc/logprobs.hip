@@ -473,7 +473,7 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) 
   for (int64_t at = safe; has_whole && whole(at); at += kStride) {
     float x[16];
     widened(x);
-    request(whole(at + kStride) ? at + kStride : safe);   // the last round reads a block again: no branch
+    request(whole(at + kStride) ? at + kStride : at);   // the last round asks for its block again: no branch
     consume(x, at);
   }
 #pragma unroll 1
