@@ -14,10 +14,13 @@
 // larger keys are larger values, lower places first among equals, and no
 // two are equal, so any correct selection gives the same answer.  Each wave
 // lists the keys above a threshold that is never above the top-th key of the
-// row: with w waves, every wave publishes its ceil(top / w)-th largest value
-// so far, and at least `top` values reach the smallest of those.  It follows
-// the row closely (5 of 152 k values: about 20 reach it) and costs a wave a
-// few lane maxima when it finds a larger value.  A wave looks at single
+// row: with w waves, every wave publishes its r-th largest value so far, r =
+// ceil(top / w), and at least `top` values reach the ceil(top / r)-th largest
+// of those.  It follows the row closely (5 of 152 k values: 7 to 20 reach it)
+// and costs a wave a few lane maxima when it finds a larger value.  (Larger r
+// bounds more tightly but takes longer to find: r = ceil(top / 5), twenty of
+// 152 k, 2048 rows, 149 us against 142; the smallest of the published values,
+// five, 125 us against 123, one, 127 against 118.)  A wave looks at single
 // values only where a lane's maximum reaches the threshold: the values of
 // four such lanes at a time go through LDS to one lane each, so that the wave
 // tests 64 values of interest at once and a step without any pays one
@@ -27,11 +30,12 @@
 // Rows are cut into segments where there are too few of them to fill the
 // chip, and a second launch joins the segments.
 //
-// Measured, vocabulary 151936, bf16: 2048 rows 108 us without alternatives
-// (5.8 TB/s, which is what one pass of loads reaches), 126 with five (4.9),
-// 143 with twenty; 4 rows 6.7, 11.0 and 13.5 us, of which 6 are the two
-// launches and the chain of one load, one join.  1024 rows of fp32: 103 and
-// 108 us.
+// Measured, vocabulary 151936, bf16: 2048 rows 106 us without alternatives
+// (5.9 TB/s, which is what one pass of loads reaches), 118 with one, 123 with
+// five (5.1), 142 with twenty; 4 rows 6.8, 10.4, 11.3 and 13.7 us, of which 6
+// are the two launches and the chain of one load, one join.  1024 rows of
+// fp32: 100 us, and 106 with five.  Without alternatives bound by HBM, with
+// them by the VALU: 12 instructions a value, 8 of them for the statistics.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -198,7 +202,6 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
   return ((uint64_t)hi << 32) | lo;
 }
 
-__device__ __forceinline__ uint32_t pick_min(uint32_t a, uint32_t b) { return a < b ? a : b; }
 __device__ __forceinline__ uint32_t pick_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint64_t pick_larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 template <int CTRL>
@@ -242,14 +245,20 @@ struct LpBest {
   }
 };
 
-// The smallest of what the waves have published, as a threshold.
-__device__ __forceinline__ uint64_t least_published(const uint32_t* published) {
-  asm volatile("" ::: "memory");
-  uint32_t least = *(const volatile uint32_t*)&published[threadIdx.x & (kLpWaves - 1)];
-  least = pick_min(least, lane_move<0xB1>(least));
-  least = pick_min(least, lane_move<0x4E>(least));
-  least = pick_min(least, lane_move<0x141>(least));
-  return (uint64_t)__builtin_amdgcn_readfirstlane(least) << 32;
+// The m-th largest of what the waves have published, as a threshold: lane l
+// compares wave l % 8's value with wave l / 8's.
+__device__ __forceinline__ uint64_t published_bound(const uint32_t* published, int m) {
+  static_assert(kLpWaves == 8, "a pair of waves a lane");
+  int lane = threadIdx.x & (kWave - 1);
+  asm volatile("" : "+v"(lane)::"memory");   // what depends on it is not kept in registers from call to call
+  const volatile uint32_t* p = published;
+  const uint32_t mine = p[lane & 7], other = p[lane >> 3];
+  const uint64_t reach = __ballot(other >= mine) & 0x0101010101010101ull << (lane & 7);
+  uint32_t v = __builtin_popcountll(reach) >= m ? mine : 0;
+  v = pick_max(v, lane_move<0xB1>(v));
+  v = pick_max(v, lane_move<0x4E>(v));
+  v = pick_max(v, lane_move<0x141>(v));
+  return (uint64_t)__builtin_amdgcn_readfirstlane(v) << 32;
 }
 
 // A wave's list of candidates.
@@ -345,10 +354,11 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) 
 
   LpStats s{-__builtin_inff(), 0.0f, 0.0f};
   LpList list{lists + wave * kLpCap, &shared_tau, kFirstKey, 0};
-  // waves that have values, and of how many each publishes the last
+  // each wave that has values publishes its `want`-th largest, and m of them
+  // bound the answer
   const int64_t blocks = (hi - lo + kLpBlock - 1) / kLpBlock;
   const int active = blocks < kLpWaves ? (int)blocks : kLpWaves;
-  const int want = active > 0 ? (a.top + active - 1) / active : 1;
+  const int want = TOP ? (a.top + active - 1) / active : 1, m = (a.top + want - 1) / want;
   LpBest best;
   const auto lane_largest = [&](const float (&x)[16], float top) __attribute__((always_inline)) {
     const uint32_t o = top == top ? ordered(top) : lp_nan_max(x);
@@ -365,17 +375,17 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) 
     uint64_t cut = 0;
     if constexpr (TOP) cut = *(volatile uint64_t*)&shared_tau;   // read ahead of its use
     const float top = largest(x);
-    const float m = __builtin_elementwise_maximum(s.m, top);
-    const float down = __builtin_fmaxf((s.m - m) * kLog2E, kMinExp), f = __builtin_amdgcn_exp2f(down);
+    const float mx = __builtin_elementwise_maximum(s.m, top);
+    const float down = __builtin_fmaxf((s.m - mx) * kLog2E, kMinExp), f = __builtin_amdgcn_exp2f(down);
     float z = 0.0f, u = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float e = __builtin_fmaxf((x[i] - m) * kLog2E, kMinExp);   // the difference first: m log2 e can overflow
+      const float e = __builtin_fmaxf((x[i] - mx) * kLog2E, kMinExp);   // the difference first: m log2 e can overflow
       const float p = __builtin_amdgcn_exp2f(e);
       z += p;
       u = __builtin_fmaf(e, p, u);
     }
-    s = LpStats{m, __builtin_fmaf(s.z, f, z), __builtin_fmaf(f, __builtin_fmaf(down, s.z, s.u), u)};
+    s = LpStats{mx, __builtin_fmaf(s.z, f, z), __builtin_fmaf(f, __builtin_fmaf(down, s.z, s.u), u)};
 
     if constexpr (TOP) {
       cut = uniform64(cut);
@@ -390,7 +400,7 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) 
           const uint32_t now = best.take(mine, want);
           if (now > old) {
             if (lane == 0) published[wave] = now;
-            list.raise(least_published(published));
+            list.raise(published_bound(published, m));
           }
         }
       }
@@ -455,8 +465,8 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) 
   if (has_whole) request(safe);
   if constexpr (TOP) {
     // every wave's first values give the first threshold
-    uint32_t now = wave < active ? 0 : 0xFFFFFFFFu;   // a wave without values does not count
-    if (wave < active) {
+    uint32_t now = 0;   // reaches no bound
+    if (wave < blocks) {
       float x[16];
       if (has_whole)
         widened(x);
@@ -467,7 +477,7 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) 
     }
     if (lane == 0) published[wave] = now;
     __syncthreads();
-    list.raise(least_published(published));
+    list.raise(published_bound(published, m));
   }
 #pragma unroll 1
   for (int64_t at = safe; has_whole && whole(at); at += kStride) {
@@ -498,7 +508,7 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void k_logprobs(LpArgs a) 
   if (lane == 0) wave_stats[wave] = s;
   __syncthreads();
   if constexpr (TOP) {   // the final threshold, the same in every wave
-    list.tau = pick_larger(shared_tau, least_published(published));
+    list.tau = pick_larger(shared_tau, published_bound(published, m));
     list.sweep();
     if (list.count > kWave) list.cut(a.top, kWave);   // at most 64: one key a lane
   }
