@@ -736,10 +736,17 @@ def _buffer(t, shape, dtype, device, what: str):
     torch = _torch()
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _require(t, (dtype,), what, len(shape))
-    if t.shape != shape:
-        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    return t
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
+    _require(t, (dtype,), what, len(shape))   # says what is wrong
+    raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _workspace_bytes(t) -> int:
+    """The size of a caller's workspace, any GPU tensor without gaps."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace: expected a contiguous GPU tensor")
+    return t.numel() * t.element_size()
 
 
 def _launch_stream(stream, *owned):
@@ -782,13 +789,16 @@ def fp8w_route_experts(logits, top_k: int, score: str = "softmax", bias=None, re
     slots = _buffer(slots, (t, k), i32, dev, "slots")
     rows = _buffer(rows, (t * k,), i32, dev, "rows")
     offsets = _buffer(offsets, (e + 1,), i32, dev, "offsets")
-    if workspace is None and t > 32:
-        workspace = torch.empty(int(lib().fp8w_route_experts_workspace_bytes(t, e)), dtype=torch.uint8, device=dev)
+    need = 0
+    if workspace is not None:
+        need = _workspace_bytes(workspace)
+    elif t > 32:
+        need = lib().fp8w_route_experts_workspace_bytes(t, e)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _check(lib().fp8w_route_experts(
         logits.data_ptr(), dtype, stride, t, e, k, SCORE_IDS[score], None if bias is None else bias.data_ptr(),
         1 if renorm else 0, scale, ids.data_ptr(), weights.data_ptr(), slots.data_ptr(), rows.data_ptr(),
-        offsets.data_ptr(), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        offsets.data_ptr(), None if workspace is None else workspace.data_ptr(), need,
         _launch_stream(stream, ids, weights, slots, rows, offsets, workspace)), "fp8w_route_experts")
     return ExpertRouting(ids, weights, slots, rows, offsets)
 
@@ -901,15 +911,16 @@ def fp8w_logprobs(logits, targets=None, top: int = 0, logprob=None, entropy=None
     entropy = _buffer(entropy, (t,), f32, dev, "entropy")
     top_ids = _buffer(top_ids, (t, top), torch.int32, dev, "top_ids")
     top_logprobs = _buffer(top_logprobs, (t, top), f32, dev, "top_logprobs")
-    if workspace is None:
+    if workspace is not None:
+        need = _workspace_bytes(workspace)
+    else:
         need = lib().fp8w_logprobs_workspace_bytes(t, v, top)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _check(lib().fp8w_logprobs(
         logits.data_ptr(), dtype, stride, t, v, None if targets is None else targets.data_ptr(), top,
         None if logprob is None else logprob.data_ptr(), entropy.data_ptr(), top_ids.data_ptr() if top else None,
-        top_logprobs.data_ptr() if top else None, None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        top_logprobs.data_ptr() if top else None, None if workspace is None else workspace.data_ptr(), need,
         _launch_stream(stream, logprob, entropy, top_ids, top_logprobs, workspace)), "fp8w_logprobs")
     return Logprobs(logprob, entropy, top_ids, top_logprobs)
 

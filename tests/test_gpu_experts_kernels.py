@@ -142,3 +142,25 @@ def test_combine_reads_nothing_for_no_slot(F):
     assert out[:, 0].tolist() == [1.0, 0.0, 2.0] and (out == out[:, :1]).all()
     none = F.fp8w_combine_experts(y[:0], w, slots)
     assert none.shape == (3, 24) and (none == 0).all()
+
+
+# --------------------------------------------------------------- refusals --
+
+def test_refused_buffers_and_workspaces(F):
+    """Nothing is launched with a buffer of another shape, type, place or
+    layout, or with a workspace that the GPU cannot write."""
+    x = torch.randn(40, 64, device=dev())
+    i32 = dict(dtype=torch.int32, device=dev())
+    for bad, error in ((torch.empty(40, 3, **i32), ValueError), (torch.empty(40, 4, device=dev()), TypeError),
+                       (torch.empty(40, 4, dtype=torch.int32), ValueError), (torch.empty(4, 40, **i32).T, ValueError)):
+        with pytest.raises(error, match="ids"):
+            F.fp8w_route_experts(x, 4, ids=bad)
+        with pytest.raises(error, match="top_ids"):
+            F.fp8w_logprobs(x, top=4, top_ids=bad)
+    for bad in (torch.empty(1 << 16, dtype=torch.uint8), torch.empty(1 << 9, 1 << 9, device=dev())[:, ::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            F.fp8w_route_experts(x, 4, workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            F.fp8w_logprobs(x, top=4, workspace=bad)
+    with pytest.raises(F.Fp8wError):
+        F.fp8w_route_experts(x, 4, workspace=torch.empty(3, dtype=torch.uint8, device=dev()))
