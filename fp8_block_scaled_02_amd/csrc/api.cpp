@@ -564,6 +564,10 @@ namespace {
 constexpr int64_t kMaxBlocks256 = 0xFFFFFFFF / 256;
 constexpr int64_t kMaxBlocks512 = 0xFFFFFFFF / 512;
 
+// The grouped products step past the end of rows, columns and slots in 32
+// bits (whole tiles; eight rows of codes from one) before they compare.
+constexpr int64_t kMaxExpertsNK = 1 << 28, kMaxExpertsSlots = 1 << 30;
+
 bool dtype_ok(int d) { return d == FP8W_DTYPE_BF16 || d == FP8W_DTYPE_F32; }
 uint64_t dtype_bytes(int d) { return d == FP8W_DTYPE_F32 ? 4 : 2; }
 
@@ -617,8 +621,8 @@ FP8W_API fp8w_status fp8w_gemm_experts(const uint16_t* x, int64_t x_rows, const 
   if (!offsets || !codes || !scales || (slots != 0 && (!x || !y))) return FP8W_ERR_NULL;
   if (!format_ok(format) || (act != FP8W_ACT_NONE && act != FP8W_ACT_SWIGLU)) return FP8W_ERR_UNSUPPORTED;
   const bool swiglu = act == FP8W_ACT_SWIGLU;
-  if (!dims_ok(n, k) || k < 16 || experts < 1 || experts > kMaxDim || slots < 0 || slots > kMaxDim ||
-      x_rows < (slots != 0) || x_rows > kMaxDim || (!rows && x_rows < slots) || (swiglu && n % 2 != 0))
+  if (n < 1 || n > kMaxExpertsNK || k < 16 || k > kMaxExpertsNK || experts < 1 || experts > kMaxExpertsNK ||
+      slots < 0 || slots > kMaxExpertsSlots || x_rows < (slots != 0) || x_rows > kMaxDim || (!rows && x_rows < slots) || (swiglu && n % 2 != 0))
     return FP8W_ERR_SHAPE;
   if (k % 16 != 0 || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, scale_align(format)) ||
       !aligned(y, 8) || !aligned(rows, 4) || !aligned(offsets, 4))

@@ -561,8 +561,9 @@ fp8w_status fp8w_route_experts(const void* logits, fp8w_dtype dtype, int64_t str
  * row of zeros, offsets are cut to [0, slots].
  * Each product meets the bound of fp8w_gemv (|y - y_ref| <= 2^-7 * sum |x|
  * |deq| + 1e-6).
- * Requires k >= 16, k % 16 == 0, n >= 1 (SWIGLU: n even), slots >= 0 (0: no
- * launch), experts >= 1, x_rows >= 1 (x_rows >= slots without rows).
+ * Requires 16 <= k <= 2^28, k % 16 == 0, 1 <= n <= 2^28 (SWIGLU: n even),
+ * 0 <= slots <= 2^30 (0: no launch), 1 <= experts <= 2^28, x_rows >= 1
+ * (x_rows >= slots without rows).
  * Errors: NULL, SHAPE, UNSUPPORTED (format, act), ALIGN, OVERLAP, HIP. */
 fp8w_status fp8w_gemm_experts(const uint16_t* x, int64_t x_rows, const int32_t* rows,
                               const int32_t* offsets, int64_t experts, int64_t slots,

@@ -190,6 +190,16 @@ def test_gemm_experts_refusals(L):
     assert call(slots=0, x=None, y=None, x_rows=0) == F.OK                     # nothing to do, nothing launched
 
 
+def test_gemm_experts_limits(L):
+    """Sizes whose tiles would step past 32 bits."""
+    import fp8_block_scaled_02_amd as F
+
+    def call(e=1, slots=16, n=32, k=64, x_rows=8):
+        return L.fp8w_gemm_experts(A, x_rows, B, C, e, slots, D, E, 0, n, k, 0, G, None)
+    for bad in (dict(n=(1 << 28) + 1), dict(k=(1 << 28) + 16), dict(e=(1 << 28) + 1), dict(slots=(1 << 30) + 1)):
+        assert call(**bad) == F.ERR_SHAPE, bad
+
+
 def test_combine_refusals(L):
     import fp8_block_scaled_02_amd as F
 
