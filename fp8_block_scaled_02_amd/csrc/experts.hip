@@ -255,6 +255,14 @@ typedef uint32_t u32_unaligned __attribute__((aligned(1)));
 // The waits name how many younger loads may still be on their way; a wait
 // for everything would put the memory's latency into every step.
 //
+// A CU takes about 58 bytes a clock of such loads, and a wave that issues one
+// while the queue is full stands still.  With TW = 2 they are therefore spread
+// over the products of a step (12 and 4 of them between 32 products), instead
+// of all at its start: 4096 tokens, 8 of 64 experts, gate and up 2048 x 2048,
+// block scales 317 -> 298 us, down 2048 x 1024, row scales 156 -> 145 us.  (Of
+// 534 us at k = 4096, row scales, 192 went when nothing was loaded, 7 when
+// nothing was converted, 46 when all came out of L2.)
+//
 // A lane's 16 bytes of codes are two MFMA steps of 8 columns each, so step
 // (p, s) takes columns 32p + 16(l/32) + 8s of the step, for weights and x
 // alike.  LDS rows are 128 bytes, their 16-byte units XOR-swizzled by row / 2,
@@ -296,17 +304,17 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
   const int wu = (lane & 7) ^ (lane >> 4);
   uint32_t wrow = (uint32_t)(lane >> 3) * (uint32_t)k;
   int wcol = 16 * wu;
-  const auto request_w = [&](int kb) __attribute__((always_inline)) {
+  const auto load_w = [&](int kb, int j) __attribute__((always_inline)) {
     asm volatile("" : "+v"(wrow), "+v"(wcol)::"memory");
-    const int c0 = kb * 128 + wcol, c1 = kb * 128 + (wcol ^ 64);
-    const uint32_t col[2] = {(uint32_t)(c0 < k ? c0 : 0), (uint32_t)(c1 < k ? c1 : 0)};
-#pragma unroll
-    for (int j = 0; j < kWLoads; ++j) {
-      const int row = min(out_row(8 * j), n_out - 1);
-      const uint32_t within = (uint32_t)min(n_out - 1 - row, 7) * (uint32_t)k;
-      stage16(codes + (size_t)(row + half(8 * j)) * k + (min(wrow, within) + col[j & 1]), wl + j * 1024);
-    }
+    const int c0 = kb * 128 + (wcol ^ (j & 1) * 64);
+    const int row = min(out_row(8 * j), n_out - 1);
+    const uint32_t within = (uint32_t)min(n_out - 1 - row, 7) * (uint32_t)k;
+    stage16(codes + (size_t)(row + half(8 * j)) * k + (min(wrow, within) + (uint32_t)(c0 < k ? c0 : 0)), wl + j * 1024);
     asm volatile("" ::: "memory");
+  };
+  const auto request_w = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kWLoads; ++j) load_w(kb, j);
   };
   // x rows a wave stages: 8 (MT * wave + j) + l/8, the same places (row / 2 % 8
   // = 4 (row / 8 % 2) + l/16)
@@ -318,16 +326,16 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
     xrow[j] = row >= 0 && row < c.x_rows ? row : 0;
   }
   int xcol = 8 * (wu ^ (kXLoads * wave & 1) * 4);
-  const auto request_x = [&](int step, unsigned char* to) __attribute__((always_inline)) {
-    asm volatile("" : "+v"(xcol)::"memory");
-    const int c0 = step * 64 + xcol, c1 = step * 64 + (xcol ^ 32);
-    const uint32_t col[2] = {(uint32_t)(c0 < k ? 2 * c0 : 0), (uint32_t)(c1 < k ? 2 * c1 : 0)};
-#pragma unroll
-    for (int j = 0; j < kXLoads; ++j) {
-      asm volatile("" : "+v"(xrow[j]));
-      stage16(reinterpret_cast<const char*>(c.x) + ((uint64_t)xrow[j] * (uint32_t)(2 * k) + col[j & 1]), to + (kXLoads * wave + j) * 1024);
-    }
+  const auto load_x = [&](int step, int j, unsigned char* to) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(xcol), "+v"(xrow[j])::"memory");
+    const int c0 = step * 64 + (xcol ^ (j & 1) * 32);
+    stage16(reinterpret_cast<const char*>(c.x) + ((uint64_t)xrow[j] * (uint32_t)(2 * k) + (uint32_t)(c0 < k ? 2 * c0 : 0)),
+            to + (kXLoads * wave + j) * 1024);
     asm volatile("" ::: "memory");
+  };
+  const auto request_x = [&](int step, unsigned char* to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j) load_x(step, j, to);
   };
   // whether the slots a lane will store, 32q + i, have a row of x
   uint32_t live = 0;
@@ -397,15 +405,13 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0): the codes are in registers
-    const int next = kb + 1 < nkb ? kb + 1 : 0;   // the last block asks for one nobody takes
-    request_s(next);
-    request_w(next);
+    request_s(kb + 1 < nkb ? kb + 1 : 0);         // the last block asks for one nobody takes
     __builtin_amdgcn_sched_barrier(0);
   };
   // 64 columns.  Scaled sums are settled after every 32 slots: left alone
   // the compiler starts all products first, each with sums of its own, and
   // spills.
-  const auto step = [&](int h, const unsigned char* xb) __attribute__((always_inline)) {
+  const auto step = [&](int h, const unsigned char* xb, const auto& load) __attribute__((always_inline)) {
     const auto read_b = [&](int q, int u) __attribute__((always_inline)) {
       return *reinterpret_cast<const bf16x8*>(&xb[(32 * q + i) * 128 + 16 * ((4 * (u >> 1) + 2 * hh + (u & 1)) ^ (i >> 1 & 7))]);
     };
@@ -421,7 +427,7 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
     for (int q = 0; q < MT; ++q) {
       // No slots left, in the last run of an expert.  (With block scales the
       // branches cost registers that are not there.)
-      if (!kBlock && q > 0 && 32 * q >= at.count) break;
+      if (!kBlock && TW == 1 && q > 0 && 32 * q >= at.count) break;
       f32x16 part[TW];
 #pragma unroll
       for (int t = 0; t < TW; ++t) {
@@ -439,6 +445,7 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
         // the operand's register is free: the next 32 slots' into it, three
         // products ahead of their use
         if (q + 1 < MT) b[u] = read_b(q + 1, u);
+        if (TW == 2) load(4 * q + u);
         if (q + 1 < MT || u < 3) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -457,11 +464,29 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
   // the two after them go to x2 and x0.
   const auto block = [&](int kb, unsigned char* x0, unsigned char* x1, unsigned char* x2) __attribute__((always_inline)) {
     take_w(kb);
-    request_x(2 * kb + 2 < 2 * nkb ? 2 * kb + 2 : 0, x2);
-    step(0, x0);
+    const int next = kb + 1 < nkb ? kb + 1 : 0;
+    const auto first = [&](int n) __attribute__((always_inline)) {   // 4 MT places for 8 + MT loads
+      const int to = (n + 1) * (kWLoads + kXLoads) / (4 * MT);
+#pragma unroll
+      for (int j = n * (kWLoads + kXLoads) / (4 * MT); j < to; ++j) {
+        if (j < kWLoads)
+          load_w(next, j);
+        else
+          load_x(2 * next, j - kWLoads, x2);
+      }
+    };
+    const auto second = [&](int n) __attribute__((always_inline)) {
+      if (n % 4 == 0) load_x(2 * next + 1, n / 4, x0);
+    };
+    if (TW == 1) {
+      request_w(next);
+      request_x(2 * next, x2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    step(0, x0, first);
     land_and_meet<kWLoads + kXLoads>();           // younger than x1's: weights and x2's
-    request_x(2 * kb + 3 < 2 * nkb ? 2 * kb + 3 : 0, x0);
-    step(1, x1);
+    if (TW == 1) request_x(2 * next + 1, x0);
+    step(1, x1, second);
     land_and_meet<kXLoads>();                     // the weights and x2's have landed
   };
 
@@ -543,11 +568,11 @@ __global__ __launch_bounds__(256, TW == 2 ? 2 : 4) void k_experts_wide(ExpertsCa
   __shared__ __attribute__((aligned(16))) unsigned char xs2[32 * MT * 128];
   const TileAt at = tile_at(c.offsets, c.experts, c.slots, 32 * MT, n_groups);
   if (at.expert < 0) return;
-  // Block scales, whose steps do not skip empty slots: an expert's last run
-  // as one of half the height, where that holds it (32768 slots over 64
-  // experts, gate and up 2048 x 2048: 332 us without, 320 with; for the
-  // narrow tiles the difference is within the noise).
-  if constexpr ((FMT == kFmtBlock || FMT == kFmtBlockBf16) && TW == 2) {
+  // These steps do not skip empty slots: an expert's last run as one of half
+  // the height, where that holds it (32768 slots over 64 experts, gate and up
+  // 2048 x 2048, block scales: 332 us without, 320 with; for the narrow tiles
+  // the difference is within the noise).
+  if constexpr (TW == 2) {
     if (at.count <= 16 * MT) {
       experts_run<FMT, SWIGLU, MT / 2, TW>(c, at, ws, xs0, xs1, xs2);
       return;
