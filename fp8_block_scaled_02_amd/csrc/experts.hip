@@ -426,7 +426,8 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
 #pragma unroll
     for (int q = 0; q < MT; ++q) {
       // No slots left, in the last run of an expert.  (With block scales the
-      // branches cost registers that are not there.)
+      // branches cost registers that are not there; the wide tile's loads
+      // stand between its products.)
       if (!kBlock && TW == 1 && q > 0 && 32 * q >= at.count) break;
       f32x16 part[TW];
 #pragma unroll
