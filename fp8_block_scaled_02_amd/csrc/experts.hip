@@ -752,14 +752,15 @@ struct ExpertsPlan {
   int width;    // outputs of a group
 };
 
-// By the slots an expert has on average, from sweeps on MI355X (E = 64, 4
-// choices, gate and up 2048 x 2048, block scales; us at 2 / 4 / 8 / 12 slots
-// an expert, and down 2048 x 2048, row scales, at 24 / 48 / 96 / 160 / 256):
-//   streaming          36  44  54  65     88 141 250 395 615
-//   128 x 64 tiles     43  51  55  56     62  69  98 134 190
-//   256 x 128 tiles    68  74  78  78     59  78  97 121 163
-// With 8 experts of 4096 x 2048 the narrow tiles' lead lasts (24 .. 256
-// slots: 17 / 21 / 25 / 35 / 54 us against 25 / 32 / 34 / 35 / 54 us).
+// By the slots an expert has on average, from sweeps on MI355X (us).
+//   E = 64, 4 choices, gate and up 2048 x 2048, block scales, at 2 / 4 / 8 / 12
+//   slots an expert; the same at 24 / 48 / 64 / 96 / 128 / 160 / 256; down
+//   2048 x 2048, row scales, at those:
+//   streaming        36 44 54 65
+//   128 x 64 tiles   43 51 55 55     62 73 85 103 122 143 198    62 69 81 97 114 134 186
+//   256 x 128 tiles   .  .  . 53     65 84 91 106 116 131 178    59 73 85 92 101 116 156
+// With 8 experts of 4096 x 2048 the narrow tiles' lead lasts (24 / 48 / 96 /
+// 160 / 256 slots: 18 / 21 / 23 / 34 / 51 us against 21 / 27 / 28 / 31 / 48).
 //
 // Halves that do not start on a multiple of 32 rows would put a tile's rows
 // in two scale blocks (the streaming kernel asks for 4), and rows of fewer
@@ -771,7 +772,7 @@ ExpertsPlan experts_plan(int64_t experts, int64_t slots, int64_t n, int64_t k, b
   const int outputs = swiglu ? 1 : 2;   // of two weight rows
   if (split % 4 != 0 || (format == kFmtMx && k <= 96)) return {ExpertsPlan::kSimple, 16, 64};
   if (average <= 8 || split % 32 != 0) return {ExpertsPlan::kStream, 16, 8 * kStreamTiles * outputs};
-  if (average <= 128) return {ExpertsPlan::kNarrow, 64, 64 * outputs};
+  if (average <= 112) return {ExpertsPlan::kNarrow, 64, 64 * outputs};
   return {ExpertsPlan::kWide, 128, 128 * outputs};
 }
 

@@ -1,5 +1,5 @@
 """GPU parity of the products grouped by expert around the average group size
-at which the kernel changes (8 / 9 and 128 / 129 slots an expert), for every
+at which the kernel changes (8 / 9 and 112 / 113 slots an expert), for every
 scale format and activation, halves that only the streaming kernel takes,
 every e4m3 code, and drawn shapes; routing at the edges of its lane groups;
 the weighted sum at every length of its row batches."""
@@ -31,6 +31,13 @@ def F():
 @pytest.mark.parametrize("sizes", [[17, 0, 7], [9, 1, 17], [200, 3, 181], [258, 0, 129]])
 def test_formats_where_the_kernel_changes(F, sizes, act, fmt):
     check_experts(F, sizes, 320, 400, fmt, act)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("sizes", [[9, 8, 8], [9, 8, 10], [224, 112, 0], [226, 113, 0], [0, 0, 337]])
+def test_sizes_next_to_the_changes(F, sizes, act, fmt):
+    check_experts(F, sizes, 192, 272, fmt, act)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
