@@ -204,6 +204,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_i
   }
   float w;
   if (a.score == 0) {
+    // Of the chosen alone, their own largest: under a bias the row's may not
+    // be among them, and terms taken from it could all be zero.
+    if constexpr (kBias) {
+      if (a.renorm) top = group_max<L>(my_x);
+    }
     w = live ? expf(my_x - top) : 0.0f;
     if (a.renorm) z = group_total<L>(w);
     w = live ? w / z : 0.0f;

@@ -1,0 +1,70 @@
+"""GPU routing weights where the chosen experts lie far below the row's best
+(a selection bias chooses) or far below zero (sigmoid scores near and below
+fp32's smallest number): the weights are ratios of the chosen scores, however
+small those are."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import dev
+
+pytestmark = pytest.mark.gpu
+
+# An exponential's argument is one fp32 difference d (rounded by 2^-24 |d|),
+# the exponential and the divisions are good to 2 units of 2^-23 each, the sum
+# of up to 16 terms adds a rounding for each.
+EPS32 = 2.0 ** -23
+
+
+def tolerance(x, k):
+    return (np.ptp(x) + k + 8) * EPS32
+
+
+@pytest.fixture(scope="module")
+def F():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm GPU"
+    import fp8_block_scaled_02_amd as fp8w
+    fp8w.lib()
+    return fp8w
+
+
+def _route(F, x, bias, k, **kw):
+    r = F.fp8w_route_experts(x, k, bias=bias, **kw)
+    torch.cuda.synchronize()
+    return r.ids.cpu().numpy(), r.weights.cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("gap", [5, 60, 88, 90, 96, 103, 104, 120, 200, 1000, 3e38])
+@pytest.mark.parametrize("e,k", [(3, 2), (60, 6), (128, 16), (200, 17), (256, 8), (300, 8), (1024, 64)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("t", [3, 40])
+def test_softmax_of_the_chosen_below_the_best(F, gap, e, k, dtype, t):
+    """The best logit is barred by its bias, and the others lie `gap` below."""
+    g = torch.Generator(device="cuda").manual_seed(e + k)
+    x = (torch.randn(t, e, generator=g, device=dev()) - gap).to(dtype)
+    x[:, e // 2] = 0.5
+    bias = torch.zeros(e, device=dev())
+    bias[e // 2] = -5.0
+    bias[torch.randperm(e, generator=g, device=dev())[:k]] += torch.arange(1, k + 1, device=dev()).float()
+    bias[e // 2] = -5.0
+    ids, w = _route(F, x, bias, k)
+    named = np.flatnonzero(bias.cpu().numpy() > 0)             # their biases decide: a score is at most 1
+    xs = x.float().cpu().numpy().astype(np.float64)
+    for r in range(t):
+        assert (ids[r] >= 0).all()
+        if gap >= 60:                                         # and nothing, beside the barred one's
+            assert np.isin(named, ids[r]).all()
+        c = xs[r, ids[r]]
+        p = np.exp(c - c.max())
+        p /= p.sum()
+        assert (np.abs(w[r] - p) <= tolerance(c, k) * p + 1e-37).all(), (r, w[r], p)
+
+
+def test_softmax_with_a_bias_as_in_the_definition(F):
+    x = torch.tensor([[200.0, 0.0, -1.0, -2.0], [0.0, -120.0, -119.0, -400.0]], device=dev())
+    ids, w = _route(F, x, torch.tensor([-5.0, 0.0, 0.0, 0.0], device=dev()), 2)
+    assert ids.tolist() == [[1, 2], [2, 1]]
+    assert np.abs(w - [[0.7310585786, 0.2689414214]] * 2).max() < 1e-6
+    # without renorm they are parts of the whole row's sum: nothing, in fp32
+    _, w = _route(F, x, torch.tensor([-5.0, 0.0, 0.0, 0.0], device=dev()), 2, renorm=False)
+    assert (w == 0).all()
