@@ -12,6 +12,7 @@
 // with fewer than top_k live experts gets id -1, weight 0, slot -1 there.
 //   softmax  w = exp(l - max) / sum      over the chosen (renorm) or all experts
 //   sigmoid  w = 1 / (1 + exp(-l)),      over the sum of the chosen if renorm
+//                                        (0 if all of them are 0 in fp32)
 // times `scale`.  The pairs (t, j) sorted by expert, then token, are the
 // slots of the grouped products: offsets[e] .. offsets[e + 1) are expert e's
 // and rows[slot] = t.
@@ -49,6 +50,7 @@ constexpr int kRouteThreads = 512;   // 8 waves, 4 tokens each
 constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr int kRouteMaxE = 1024;
 constexpr int kRouteMaxK = 64;       // a lane holds one choice
+constexpr float kLeastScore = -103.972077f;   // -150 ln 2: e^x rounds to zero in fp32 from here down
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_mov(float v) {
@@ -213,10 +215,16 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_i
     if (a.renorm) z = group_total<L>(w);
     w = live ? w / z : 0.0f;
   } else {
-    w = live ? 1.0f / (1.0f + expf(-my_x)) : 0.0f;
+    // e^x / (1 + e^x) below zero: 1 + e^-x overflows where the score is still
+    // a number.  To be divided by their sum the chosen scores are taken times
+    // e^-best, since most of an fp32's bits are gone before the ratio is.
+    const float best = a.renorm ? group_max<L>(my_x) : 0.0f;
+    const float t = expf(-__builtin_fabsf(my_x));
+    const float up = a.renorm && best < 0.0f ? expf(my_x - best) : my_x < 0.0f ? t : 1.0f;
+    w = live ? up / (1.0f + t) : 0.0f;
     if (a.renorm) {
       const float sum = group_total<L>(w);
-      w = sum > 0.0f ? w / sum : 0.0f;   // every chosen score underflowed: no weight
+      w = live && best > kLeastScore ? w / sum : 0.0f;   // every chosen score is zero in fp32: no weight
     }
   }
   my_w = w * a.scale;

@@ -68,3 +68,32 @@ def test_softmax_with_a_bias_as_in_the_definition(F):
     # without renorm they are parts of the whole row's sum: nothing, in fp32
     _, w = _route(F, x, torch.tensor([-5.0, 0.0, 0.0, 0.0], device=dev()), 2, renorm=False)
     assert (w == 0).all()
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("e,k", [(4, 2), (40, 16), (200, 20), (300, 4)])
+def test_sigmoid_scores_next_to_the_smallest_number(F, e, k, bias):
+    """Ratios of scores from e^-80 down to where fp32 has none left."""
+    g = torch.Generator(device="cuda").manual_seed(e)
+    far = torch.tensor([0.0, -30.0, -80.0, -86.0, -88.0, -89.0, -91.0, -95.0, -98.0, -101.0], device=dev())
+    x = far[:, None] - torch.rand(10, e, generator=g, device=dev()) * 2
+    x[0, 0] = x[5, 1] = 3.0                                  # one score of ordinary size among small ones
+    b = torch.rand(e, generator=g, device=dev()) if bias else None
+    ids, w = _route(F, x, b, k, score="sigmoid")
+    xs = x.cpu().numpy().astype(np.float64)
+    for r in range(len(xs)):
+        c = xs[r, ids[r]]
+        p = 1 / (1 + np.exp(-c))
+        p /= p.sum()
+        assert (np.abs(w[r] - p) <= tolerance(c, k) * p + 1e-37).all(), (r, w[r], p)
+
+
+def test_sigmoid_scores_below_the_smallest_number(F):
+    """A score below fp32's smallest number is zero, and zeros have no ratio;
+    beside a larger one it counts by its definition."""
+    x = torch.tensor([[-104.5, -105.0, -300.0], [-103.0, -104.5, -300.0], [-np.inf, -200.0, -201.0]], device=dev())
+    _, w = _route(F, x, None, 2, score="sigmoid")
+    assert (w[[0, 2]] == 0).all()
+    assert np.abs(w[1] - [0.8175744762, 0.1824255238]).max() < 1e-6
+    _, w = _route(F, x, None, 2, score="sigmoid", renorm=False)
+    assert (w <= 1e-44).all() and (w >= 0).all()
