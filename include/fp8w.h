@@ -525,8 +525,8 @@ typedef enum fp8w_act {
  * `renorm`, times `scale`, in fp32.  Sigmoid scores that are all below the
  * smallest fp32 number (logits below about -104) have no ratio: with `renorm`
  * the token's weights are 0.  Slots are sorted by expert, then by token.
- * An expert whose logit is -inf or NaN is never chosen: a token with fewer
- * than top_k others has id -1, weight 0 and slot -1 for what is missing, and
+ * An expert whose logit or bias is -inf or NaN is never chosen: a token with
+ * fewer than top_k others has id -1, weight 0 and slot -1 for what is missing, and
  * rows past offsets[experts] are -1.  Logits of +inf give unspecified weights.
  * workspace: fp8w_route_experts_workspace_bytes(tokens, experts) bytes
  * (0 up to 32 tokens), 4-byte aligned.  tokens may be 0 (offsets are then

@@ -33,7 +33,7 @@ def route(logits: np.ndarray, top_k: int, score: str = "softmax", bias=None, ren
             else:
                 p = np.where(live, 1.0 / (1.0 + np.exp(np.where(live, -x[r], 0.0))), 0.0)
         key = x[r] if bias is None else p + np.asarray(bias, np.float64)
-        order = sorted(np.flatnonzero(live), key=lambda i: (-key[i], i))[:top_k]
+        order = sorted(np.flatnonzero(live & (key > -np.inf)), key=lambda i: (-key[i], i))[:top_k]
         ids[r, :len(order)] = order
         w[r, :len(order)] = p[order]
         if renorm and p[order].sum() > 0:

@@ -97,3 +97,24 @@ def test_sigmoid_scores_below_the_smallest_number(F):
     assert np.abs(w[1] - [0.8175744762, 0.1824255238]).max() < 1e-6
     _, w = _route(F, x, None, 2, score="sigmoid", renorm=False)
     assert (w <= 1e-44).all() and (w >= 0).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,k", [(9, 6), (70, 20), (300, 5)])
+def test_barred_experts(F, score, e, k):
+    """A bias of -inf or NaN bars an expert; its score stays in softmax's sum."""
+    from oracle import serving as S
+    g = torch.Generator(device="cuda").manual_seed(e)
+    x = torch.randn(35, e, generator=g, device=dev())
+    bias = torch.randn(e, generator=g, device=dev())
+    bias[torch.randperm(e, generator=g, device=dev())[:e // 2]] = -np.inf
+    bias[e - 1], bias[3] = float("nan"), float("inf")
+    for renorm in (True, False):
+        r = F.fp8w_route_experts(x, k, score=score, bias=bias, renorm=renorm)
+        torch.cuda.synchronize()
+        want = S.route(x.cpu().numpy(), k, score, bias.cpu().numpy(), renorm)
+        for got, w in zip((r.ids, r.slots, r.rows, r.offsets), (want[0], *want[2:])):
+            assert np.array_equal(got.cpu().numpy(), w)
+        assert (np.abs(r.weights.cpu().numpy() - want[1]) <= (8 + e + k + 8) * EPS32 * want[1] + 1e-37).all()
+    left = int((bias > -np.inf).sum())
+    assert (r.ids[:, :left] >= 0).all() and (r.ids[:, left:] == -1).all()
