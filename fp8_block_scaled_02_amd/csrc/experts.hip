@@ -220,6 +220,9 @@ __device__ __forceinline__ void stage16(const void* from, unsigned char* to) {
                                    (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
+// What x holds past its columns.
+__device__ const uint4 kNoColumns = {0, 0, 0, 0};
+
 // s_waitcnt vmcnt(n) lgkmcnt(0), n < 64, then the workgroup's barrier.  The
 // LDS reads before it have returned, so that what they read may be
 // overwritten after it; and all but the wave's last n loads have landed.
@@ -296,8 +299,9 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
 
   // Load j of a wave's weights brings rows 8j + l/8; LDS place l%8 of a row
   // holds its unit (l%8) ^ (row / 2 % 8), so j odd the unit of j even ^ 4.
-  // Rows past the end are the last one, columns past it column 0 (whose
-  // products the zeroed weights of take_w drop).  No branches: a load that
+  // Rows past the end are the last one, columns past it the first ones (zeroed
+  // by take_w; x has zeros there, so that no infinity of a column that is read
+  // in their place meets them).  No branches: a load that
   // two paths share is one the compiler takes to write any of the arrays.
   // Offsets pass through an empty asm statement where they are used: the
   // addresses of all loads would otherwise be kept in registers throughout.
@@ -329,8 +333,8 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
   const auto load_x = [&](int step, int j, unsigned char* to) __attribute__((always_inline)) {
     asm volatile("" : "+v"(xcol), "+v"(xrow[j])::"memory");
     const int c0 = step * 64 + (xcol ^ (j & 1) * 32);
-    stage16(reinterpret_cast<const char*>(c.x) + ((uint64_t)xrow[j] * (uint32_t)(2 * k) + (uint32_t)(c0 < k ? 2 * c0 : 0)),
-            to + (kXLoads * wave + j) * 1024);
+    const char* from = reinterpret_cast<const char*>(c.x) + ((uint64_t)xrow[j] * (uint32_t)(2 * k) + (uint32_t)(2 * c0));
+    stage16(c0 < k ? from : reinterpret_cast<const char*>(&kNoColumns), to + (kXLoads * wave + j) * 1024);
     asm volatile("" ::: "memory");
   };
   const auto request_x = [&](int step, unsigned char* to) __attribute__((always_inline)) {
@@ -617,7 +621,7 @@ __global__ __launch_bounds__(256, 16 / NT) void k_experts_stream(ExpertsCall c, 
 
   // Load j of a block brings rows 8j + l/8 (tile j / 2); LDS place l%8 of a
   // row holds its unit (l%8) ^ (row / 2 % 8).  Rows past the end are the
-  // last one, columns past it column 0, and zero weights.
+  // last one, columns past it the first ones, taken as zeros.
   const uint8_t* wp[2 * NT];
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j)
@@ -668,6 +672,11 @@ __global__ __launch_bounds__(256, 16 / NT) void k_experts_stream(ExpertsCall c, 
     }
     vm_wait_all();
     asm volatile("" ::: "memory");
+    if (kb * 128 + 128 > k) {   // zeros past k, where a column's infinity would meet the zero weights
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (kb * 128 + 64 * (u >> 1) + 16 * g >= k) x[u] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       f32x4 part = {};

@@ -1,0 +1,57 @@
+"""The products grouped by expert with infinite inputs, on every kernel: an
+infinity in any column of x shows where and as the definition says."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from fp8_block_scaled_02_amd import workloads as W
+from gpu_util import bf16_to_f64, dev, to_dev_bf16
+from test_gpu_experts import _experts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def F():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm GPU"
+    import fp8_block_scaled_02_amd as fp8w
+    fp8w.lib()
+    return fp8w
+
+
+# streaming, 128 x 64 tiles, 256 x 128 tiles, these with last runs of half a tile
+@pytest.mark.parametrize("slots", [3, 40, 300, 420])
+@pytest.mark.parametrize("act", ["none"])
+@pytest.mark.parametrize("fmt,n,k", [("block", 64, 400), ("block", 6, 144), ("row", 64, 16), ("mx", 64, 48),
+                                     ("mx", 96, 112), ("mx", 64, 208), ("block_bf16", 130, 272), ("tensor", 32, 240),
+                                     ("row", 300, 384)])
+def test_infinities_of_x(F, fmt, n, k, act, slots):
+    """One infinite column in each row of x, every column among them: the
+    products are infinite with the weight's sign, NaN where it is zero, and no
+    column is met by anything else (k that is no multiple of 128 ends in
+    places that read other columns)."""
+    codes, scales, cd, sd = _experts(2, n, k, fmt)
+    x = W.activation(90, slots, k)
+    at = (np.arange(slots) * 5) % k                          # columns 0, 5, 10, ...
+    x[np.arange(slots), at] = np.where(np.arange(slots) % 3 == 0, 0xFF80, 0x7F80)
+    x[np.arange(slots) % 7 == 6] = W.activation(91, slots, k)[np.arange(slots) % 7 == 6]   # some rows are finite
+    split = slots // 4
+    off = torch.tensor([0, split, slots], dtype=torch.int32, device=dev())
+    y = F.fp8w_gemm_experts(to_dev_bf16(x), cd, sd, off, fmt=fmt, act=act)
+    torch.cuda.synchronize()
+    got = bf16_to_f64(y)
+    inf = np.flatnonzero(np.arange(slots) % 7 != 6)
+    expert = (inf >= split).astype(int)
+    with np.errstate(all="ignore"):
+        w = oracle.e4m3_decode(codes[expert, :, at[inf]]).astype(np.float64)          # its weights, [inf, n], but for scales
+        p = w * np.where(inf % 3 == 0, -np.inf, np.inf)[:, None]
+        if act == "swiglu":
+            h = n // 2
+            g, u = p[:, :h], p[:, h:]
+            p = np.where(g == -np.inf, np.nan, g) * u          # -inf * 0, as the formula has it
+    assert np.array_equal(got[inf], p, equal_nan=True)
+    clean = F.fp8w_gemm_experts(to_dev_bf16(np.where(np.isin(np.arange(slots), inf)[:, None], 0, x).astype(np.uint16)), cd,
+                                sd, off, fmt=fmt, act=act)
+    rest = np.setdiff1d(np.arange(slots), inf)
+    assert np.isfinite(got[rest]).all() and np.array_equal(got[rest], bf16_to_f64(clean)[rest])
