@@ -128,7 +128,9 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* offsets, int experts, i
 // instructions as a third of the products at k = 2048).
 __device__ __forceinline__ float silu_times(float g, float u) {
   constexpr float kLog2E = 0x1.715476p+0f, kLog2ELow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  const float a = -__builtin_fmaxf(g, -200.0f);   // beyond, 2^t is infinite and the result zero
+  // Beyond 200 either way 2^t is infinite and the result zero, or it is zero
+  // and silu(g) is g, up to infinity.
+  const float a = -__builtin_amdgcn_fmed3f(g, -200.0f, 200.0f);
   const float t = a * kLog2E;
   const float lost = __builtin_fmaf(a, kLog2ELow, __builtin_fmaf(a, kLog2E, -t));
   const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(lost, kLn2, 1.0f);
