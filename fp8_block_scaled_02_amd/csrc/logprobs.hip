@@ -610,13 +610,18 @@ hipError_t lp_launch(const LpArgs& a, hipStream_t stream) {
 // Values of a segment: whole steps of all the workgroup's waves.
 constexpr int64_t kLpSegUnit = kLpBlock * kLpWaves;
 
+// Counted from the row's values alone: the last segment, which always has
+// some, also takes what a row that is not aligned moves up by (7 places at
+// most).
+int64_t lp_units(int64_t vocab) { return (vocab + kLpSegUnit - 1) / kLpSegUnit; }
+
 }  // namespace
 
 int logprobs_max_top() { return kLpMaxTop; }
 
 int logprobs_segments(int64_t tokens, int64_t vocab) {
   if (tokens < 1) return 1;
-  const int64_t units = (vocab + 7 + kLpSegUnit - 1) / kLpSegUnit;
+  const int64_t units = lp_units(vocab);
   int64_t want = (1024 + tokens - 1) / tokens;   // four workgroups a CU
   if (want > units) want = units;
   if (want > kLpMaxSegs) want = kLpMaxSegs;
@@ -632,8 +637,7 @@ int64_t logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t top) {
 
 hipError_t launch_logprobs(const LogprobsCall& c, hipStream_t stream) {
   const int segs = logprobs_segments(c.tokens, c.vocab);
-  const int64_t units = (c.vocab + 7 + kLpSegUnit - 1) / kLpSegUnit;
-  const int64_t per = (units + segs - 1) / segs * kLpSegUnit;
+  const int64_t per = (lp_units(c.vocab) + segs - 1) / segs * kLpSegUnit;
   LpArgs a{c.logits, c.targets, c.logprob, c.entropy, c.top_ids, c.top_logprobs, nullptr, nullptr, c.stride,
            c.tokens, c.vocab, c.top, segs, segs == 1 ? 0 : (int32_t)per};
   if (segs > 1) {   // the keys first: 8-byte words
