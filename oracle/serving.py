@@ -121,12 +121,35 @@ def logprobs(logits, targets, top: int):
     return lp, ent, ids, best
 
 
-def logprobs_tolerance(logits, entropy):
-    """What fp32 rounding can add to a row's log probabilities and entropy
-    (relative to 1 + their magnitude): the product with log2 e is rounded at
-    the size of the largest logit, exponents down to -100 carry an error of
-    2^-23 of themselves into terms that still count, and the sums run through
-    16 values a step, a step for every 8192 values, and the joins."""
+def logprobs_errors(logits):
+    """What fp32 can add to each row's ln z (what its log probabilities share)
+    and to its entropy; a log probability has one more rounding of itself.
+
+    With d = max - x, a term is 2^(-d log2 e): the difference, the product and
+    the constant are off by at most 2.5 * 2^-24 of d together, so a term by 2.5
+    * 2^-24 * d of itself, however the running maximum got there and whatever
+    the logits' own size.  Besides, the exponentials (one of its own, one for
+    each new maximum) are good to a unit of 2^-23 each, and the sums round:
+    16 values and two more operations a step of 8192 values, up to 19 joins.
+    The entropy weighs its terms by d once more."""
     x = np.asarray(logits, np.float64)
-    m = np.where(np.isfinite(x), np.abs(x), 0).max(axis=1)
-    return EPS32 * (2 * m + 128 + x.shape[1] / 512.0) * (1 + np.nan_to_num(entropy))
+    top = x.max(axis=1, keepdims=True)
+    usable = np.isfinite(top)
+    with np.errstate(invalid="ignore"):
+        d = np.where(usable & (x > -np.inf), top - x, np.inf)
+        p = np.exp(-d)
+        z = p.sum(axis=1)
+        z[z == 0] = 1.0
+        far = np.where(p > 0, d, 0.0)
+        mean, square = (p * far).sum(axis=1) / z, (p * far * far).sum(axis=1) / z
+    n = 2.0 * -(-x.shape[1] // 8192) + 50
+    err_z = EPS32 * (1.25 * mean + n)                      # relative
+    err_ln = err_z + 2 * EPS32 * np.log(np.maximum(z, 1.0))
+    return err_ln, err_ln + EPS32 * (1.25 * square + mean * (n + 2)) + mean * err_z
+
+
+def logprobs_tolerance(logits, entropy):
+    """The errors of a row's log probabilities and entropy, relative to 1 +
+    their magnitude."""
+    err_ln, err_h = logprobs_errors(logits)
+    return np.maximum(err_ln + EPS32, err_h / (1 + np.nan_to_num(entropy)))
