@@ -30,9 +30,9 @@ Functions carry the names of the C entry points:
 * ``fp8w_logprobs(logits, targets, top) -> Logprobs``: log probabilities of
   given tokens, entropy and top alternatives
 
-plus ``Fp8Experts``, the fp8 weights of a layer's experts, and ``Fp8Weight``, a format-tagged weight whose GEMV asserts the format
-before dispatch (a scale buffer of the wrong format cannot be detected by a
-kernel: "quantize_fp8_bs.rs", Atlas weight_map, module notes).
+plus ``Fp8Experts``, the fp8 weights of a layer's experts, and ``Fp8Weight``,
+a format-tagged weight whose GEMV asserts the format before dispatch (a scale
+buffer of the wrong format cannot be detected by a kernel: "quantize_fp8_bs.rs", Atlas weight_map, module notes).
 """
 from __future__ import annotations
 
@@ -182,6 +182,25 @@ def _stream_handle(stream) -> Optional[int]:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _launch_stream(stream, *used):
+    """The handle of the stream a call goes to.  The call's outputs and
+    workspaces belong to the stream they were made on, the current one as a
+    rule: used on another, they are recorded there, so that their memory is
+    not handed out again before the kernels have run."""
+    handle = _current_handle()
+    if stream is None:
+        return handle
+    current, handle = handle, _stream_handle(stream)
+    if handle != current:
+        cuda = _torch().cuda
+        if not isinstance(stream, cuda.Stream):   # 0 would make an ExternalStream one of the pool's
+            stream = cuda.ExternalStream(handle) if handle else cuda.default_stream()
+        for t in used:
+            if t is not None:
+                t.record_stream(stream)
+    return handle
+
+
 def _require(t, dtypes, what: str, dims: int):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
@@ -252,7 +271,7 @@ def fp8w_quantize(w, fmt: str = "block", codes=None, scales=None, workspace=None
     _check_scales(torch, fmt, scales, n, k, "fp8w_quantize")
     ws_ptr, ws_n = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
     _check(lib().fp8w_quantize(w.data_ptr(), n, k, fid, codes.data_ptr(), scales.data_ptr(), ws_ptr,
-                               ws_n, _stream_handle(stream)), "fp8w_quantize")
+                               ws_n, _launch_stream(stream, codes, scales, workspace)), "fp8w_quantize")
     return codes, scales
 
 
@@ -265,7 +284,7 @@ def fp8w_dequantize(codes, scales, fmt: str = "block", w=None, stream=None):
         w = torch.empty((n, k), dtype=torch.bfloat16, device=codes.device)
     _require(w, _bf16_like(torch), "w", 2)
     _check(lib().fp8w_dequantize(codes.data_ptr(), scales.data_ptr(), _format_id(fmt), n, k,
-                                 w.data_ptr(), _stream_handle(stream)), "fp8w_dequantize")
+                                 w.data_ptr(), _launch_stream(stream, w)), "fp8w_dequantize")
     return w
 
 
@@ -280,7 +299,7 @@ def fp8w_gemv(x, codes, scales, fmt: str = "block", y=None, route=0, stream=None
         y = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
     _require(y, _bf16_like(torch), "y", 2)
     _check(lib().fp8w_gemv(x.data_ptr(), m, codes.data_ptr(), scales.data_ptr(), _format_id(fmt), n,
-                           k, y.data_ptr(), int(route), _stream_handle(stream)), "fp8w_gemv")
+                           k, y.data_ptr(), int(route), _launch_stream(stream, y)), "fp8w_gemv")
     return y
 
 
@@ -305,7 +324,7 @@ def fp8w_gemm(x, codes, scales, fmt: str = "block", y=None, workspace=None, stre
                                 device=x.device)
     _require(y, _bf16_like(torch), "y", 2)
     _check(lib().fp8w_gemm(x.data_ptr(), m, codes.data_ptr(), scales.data_ptr(), _format_id(fmt), n, k,
-                           y.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_handle(stream)),
+                           y.data_ptr(), workspace.data_ptr(), workspace.numel(), _launch_stream(stream, y, workspace)),
            "fp8w_gemm")
     return y
 
@@ -323,7 +342,7 @@ def fp8w_gemv_w8a8(x_codes, x_scale, codes, scales, fmt: str = "block", y=None, 
     _require(y, _bf16_like(torch), "y", 2)
     _check(lib().fp8w_gemv_w8a8(x_codes.data_ptr(), x_scale.data_ptr(), m, codes.data_ptr(),
                                 scales.data_ptr(), _format_id(fmt), n, k, y.data_ptr(),
-                                _stream_handle(stream)), "fp8w_gemv_w8a8")
+                                _launch_stream(stream, y)), "fp8w_gemv_w8a8")
     return y
 
 
@@ -342,7 +361,7 @@ def fp8w_quantize_block(w, codes=None, scales=None, stream=None):
     if tuple(codes.shape) != (n, k) or tuple(scales.shape) != block_scale_shape(n, k):
         raise ValueError("fp8w_quantize_block: output shapes do not match w")
     _check(lib().fp8w_quantize_block(w.data_ptr(), n, k, codes.data_ptr(), scales.data_ptr(),
-                                     _stream_handle(stream)), "fp8w_quantize_block")
+                                     _launch_stream(stream, codes, scales)), "fp8w_quantize_block")
     return codes, scales
 
 
@@ -360,7 +379,7 @@ def fp8w_quantize_mx(w, codes=None, e8m0=None, stream=None):
     if tuple(codes.shape) != (n, k) or tuple(e8m0.shape) != mx_scale_shape(n, k):
         raise ValueError("fp8w_quantize_mx: output shapes do not match w")
     _check(lib().fp8w_quantize_mx(w.data_ptr(), n, k, codes.data_ptr(), e8m0.data_ptr(),
-                                  _stream_handle(stream)), "fp8w_quantize_mx")
+                                  _launch_stream(stream, codes, e8m0)), "fp8w_quantize_mx")
     return codes, e8m0
 
 
@@ -384,7 +403,7 @@ def _gemv(fn_name, x, codes, scale_t, scale_shape, scale_dtype, y, route, stream
         raise ValueError(f"{fn_name}: y must be [{m}, {n}]")
     fn = getattr(lib(), fn_name + "_route")
     _check(fn(x.data_ptr(), m, codes.data_ptr(), scale_t.data_ptr(), n, k, y.data_ptr(),
-              int(route), _stream_handle(stream)), fn_name)
+              int(route), _launch_stream(stream, y)), fn_name)
     return y
 
 
@@ -416,7 +435,7 @@ def _dequantize(fn_name, codes, scale_t, scale_shape, scale_dtype, w, stream):
     if tuple(w.shape) != (n, k):
         raise ValueError(f"{fn_name}: w must be [{n}, {k}]")
     _check(getattr(lib(), fn_name)(codes.data_ptr(), scale_t.data_ptr(), n, k, w.data_ptr(),
-                                   _stream_handle(stream)), fn_name)
+                                   _launch_stream(stream, w)), fn_name)
     return w
 
 
@@ -456,7 +475,7 @@ def _gemm(fn_name, x, codes, scale_t, scale_shape, scale_dtype, y, workspace, st
     _require(workspace, (torch.uint8,), "workspace", 1)
     _check(getattr(lib(), fn_name)(x.data_ptr(), m, codes.data_ptr(), scale_t.data_ptr(), n, k,
                                    y.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   _stream_handle(stream)), fn_name)
+                                   _launch_stream(stream, y, workspace)), fn_name)
     return y
 
 
@@ -493,7 +512,7 @@ def fp8w_read_ceiling(buf, out=None, stream=None):
         out = torch.empty(2048, dtype=torch.int32, device=buf.device)
     _require(out, (torch.int32,), "out", 1)
     _check(lib().fp8w_read_ceiling(buf.data_ptr(), buf.numel() * buf.element_size(), out.data_ptr(),
-                                   out.numel(), _stream_handle(stream)), "fp8w_read_ceiling")
+                                   out.numel(), _launch_stream(stream, out)), "fp8w_read_ceiling")
     return out
 
 
@@ -516,8 +535,8 @@ def fp8w_quantize_act(x, codes=None, scale=None, workspace=None, stream=None):
     if tuple(codes.shape) != (m, k) or scale.numel() != 1:
         raise ValueError("fp8w_quantize_act: codes must be [m, k] and scale one element")
     _check(lib().fp8w_quantize_act(x.data_ptr(), m, k, codes.data_ptr(), scale.data_ptr(),
-                                   workspace.data_ptr(), workspace.numel(), _stream_handle(stream)),
-           "fp8w_quantize_act")
+                                   workspace.data_ptr(), workspace.numel(),
+                                   _launch_stream(stream, codes, scale, workspace)), "fp8w_quantize_act")
     return codes, scale
 
 
@@ -553,7 +572,7 @@ def _gemv_w8a8(fn_name, x_codes, x_scale, codes, scale_t, scale_shape, scale_dty
         y = torch.empty((m, n), dtype=torch.bfloat16, device=codes.device)
     _require(y, _bf16_like(torch), "y", 2)
     _check(getattr(lib(), fn_name)(x_codes.data_ptr(), x_scale.data_ptr(), m, codes.data_ptr(),
-                                   scale_t.data_ptr(), n, k, y.data_ptr(), _stream_handle(stream)),
+                                   scale_t.data_ptr(), n, k, y.data_ptr(), _launch_stream(stream, y)),
            fn_name)
     return y
 
@@ -747,23 +766,6 @@ def _workspace_bytes(t) -> int:
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("workspace: expected a contiguous GPU tensor")
     return t.numel() * t.element_size()
-
-
-def _launch_stream(stream, *owned):
-    """The stream's handle.  Tensors made for this call belong to the current
-    stream: used on another, they are recorded there, so that their memory is
-    not handed out again before the kernels have run."""
-    handle = _current_handle()
-    if stream is None:
-        return handle
-    current, handle = handle, _stream_handle(stream)
-    if handle != current:
-        if not hasattr(stream, "cuda_stream"):
-            stream = _torch().cuda.ExternalStream(handle)
-        for t in owned:
-            if t is not None:
-                t.record_stream(stream)
-    return handle
 
 
 def fp8w_route_experts(logits, top_k: int, score: str = "softmax", bias=None, renorm: bool = True,
