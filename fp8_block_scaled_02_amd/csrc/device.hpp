@@ -128,6 +128,15 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
   return v;
 }
 
+// The lane index, recomputed at every call (an opaque v_mbcnt pair): kernels
+// at the register limit otherwise keep lane-derived row indices live from the
+// start, and spill them.
+__device__ __forceinline__ int lane_fresh() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
+}
+
 // 2^(e - 127) as an exact fp32: a normal number for e >= 1, the subnormal
 // 2^-127 for e == 0.
 __device__ __forceinline__ float mx_scale(uint8_t e) {

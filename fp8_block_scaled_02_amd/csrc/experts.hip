@@ -138,7 +138,10 @@ __device__ __forceinline__ float silu_times(float g, float u) {
 }
 
 // The simple kernel: one wave takes 16 weight rows (with SWIGLU 16 of each
-// half) against 16 slots, operands straight from memory.
+// half) against 16 slots, operands straight from memory.  It takes what the
+// others do not (experts_plan): block scales of two halves that a row quad
+// would cross, and rows of at most three MX exponents; row and tensor scales
+// never come here.
 template <bool SWIGLU>
 __global__ __launch_bounds__(256) void k_experts_simple(ExpertsCall c, int n_groups) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -197,23 +200,9 @@ __global__ __launch_bounds__(256) void k_experts_simple(ExpertsCall c, int n_gro
   for (int v = 0; v < 4; ++v) {
     const int n = n0 + 4 * g + v;
     if (n >= n_out) continue;
-    float out[2] = {acc[0][v], acc[1][v]};
-#pragma unroll
-    for (int q = 0; q < (SWIGLU ? 2 : 1); ++q) {
-      if (c.format == kFmtRow) out[q] *= ld_global<float>(sc, (size_t)(n + q * n_out) * 4);
-      if (c.format == kFmtTensor) out[q] *= ld_global<float>(sc, 0);
-    }
-    const float r = SWIGLU ? silu_times(out[0], out[1]) : out[0];
+    const float r = SWIGLU ? silu_times(acc[0][v], acc[1][v]) : acc[0][v];
     st_global<uint16_t>(c.y, ((size_t)slot * n_out + n) * 2, (uint16_t)f32_to_bf16_rne(r));
   }
-}
-
-// The lane index, recomputed at every call (an opaque v_mbcnt pair), so that
-// nothing derived from it is kept in registers from one use to the next.
-__device__ __forceinline__ int lane_fresh() {
-  int l;
-  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
-  return l;
 }
 
 // 16 bytes a lane from memory to LDS at `to` + 16 * lane (`to` uniform).

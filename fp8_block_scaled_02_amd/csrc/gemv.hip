@@ -74,15 +74,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 
-// The lane index, recomputed at every call (an opaque v_mbcnt pair): kernels
-// at the register limit otherwise keep lane-derived row indices live from the
-// start, and spill them.
-__device__ __forceinline__ int lane_fresh() {
-  int l;
-  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
-  return l;
-}
-
 __device__ __forceinline__ bf16x2 as_bf16x2(uint32_t d) { return __builtin_bit_cast(bf16x2, d); }
 
 // Non-MX scale formats.  The scale of 128-column block kb for the 128-row

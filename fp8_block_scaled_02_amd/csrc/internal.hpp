@@ -150,8 +150,6 @@ struct RouteCall {
   float scale;
   int32_t tokens, experts, top_k, score, renorm, f32;
 };
-int route_max_experts();
-int route_max_top_k();
 int64_t route_workspace_bytes(int64_t tokens, int64_t experts);
 hipError_t launch_route_experts(const RouteCall& c, hipStream_t stream);
 
@@ -188,7 +186,6 @@ struct LogprobsCall {
   int64_t stride;
   int32_t tokens, vocab, top, f32;
 };
-int logprobs_max_top();
 int logprobs_segments(int64_t tokens, int64_t vocab);
 int64_t logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t top);
 hipError_t launch_logprobs(const LogprobsCall& c, hipStream_t stream);

@@ -40,6 +40,7 @@
 #include <stdint.h>
 
 #include "device.hpp"
+#include "fp8w.h"
 #include "internal.hpp"
 
 namespace fp8w {
@@ -49,6 +50,7 @@ constexpr int kLpThreads = 512;
 constexpr int kLpWaves = kLpThreads / kWave;
 constexpr int kLpBlock = 1024;        // values of one wave step: 16 per lane
 constexpr int kLpMaxTop = 64;
+static_assert(kLpMaxTop == FP8W_MAX_TOP, "what the entry points check");
 constexpr int kLpCap = 256;           // keys a wave's list holds (4 per lane)
 constexpr int kLpMaxSegs = 64;
 constexpr float kLog2E = 1.44269504088896340736f;
@@ -616,8 +618,6 @@ constexpr int64_t kLpSegUnit = kLpBlock * kLpWaves;
 int64_t lp_units(int64_t vocab) { return (vocab + kLpSegUnit - 1) / kLpSegUnit; }
 
 }  // namespace
-
-int logprobs_max_top() { return kLpMaxTop; }
 
 int logprobs_segments(int64_t tokens, int64_t vocab) {
   if (tokens < 1) return 1;

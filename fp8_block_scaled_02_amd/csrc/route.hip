@@ -40,6 +40,7 @@
 #include <stdint.h>
 
 #include "device.hpp"
+#include "fp8w.h"
 #include "internal.hpp"
 
 namespace fp8w {
@@ -51,6 +52,7 @@ constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr int kRouteMaxE = 1024;
 constexpr int kRouteMaxK = 64;       // a lane holds one choice
 constexpr float kLeastScore = -103.972077f;   // -150 ln 2: e^x rounds to zero in fp32 from here down
+static_assert(kRouteMaxE == FP8W_MAX_EXPERTS && kRouteMaxK == FP8W_MAX_TOP_K, "what the entry points check");
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_mov(float v) {
@@ -476,9 +478,6 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* y, int64_t slot
 }
 
 }  // namespace
-
-int route_max_experts() { return kRouteMaxE; }
-int route_max_top_k() { return kRouteMaxK; }
 
 int64_t route_workspace_bytes(int64_t tokens, int64_t experts) {
   if (tokens <= kRouteTokens) return 0;
