@@ -36,8 +36,14 @@ def route(logits: np.ndarray, top_k: int, score: str = "softmax", bias=None, ren
         order = sorted(np.flatnonzero(live & (key > -np.inf)), key=lambda i: (-key[i], i))[:top_k]
         ids[r, :len(order)] = order
         w[r, :len(order)] = p[order]
-        if renorm and p[order].sum() > 0:
-            w[r] /= p[order].sum()
+        if renorm and len(order):
+            if score == "softmax":                 # of the chosen alone, however far below the best
+                c = np.exp(x[r, order] - x[r, order].max())
+                w[r, :len(order)] = c / c.sum()
+            elif p[order].max() < 2.0 ** -150:     # zero in fp32: no ratio
+                w[r] = 0.0
+            else:
+                w[r] /= p[order].sum()
     w *= np.float64(np.float32(scale))
     pairs = sorted((ids[r, j], r, j) for r in range(t) for j in range(top_k) if ids[r, j] >= 0)
     slots = np.full((t, top_k), -1, np.int64)
