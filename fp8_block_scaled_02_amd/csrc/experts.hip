@@ -263,8 +263,11 @@ typedef uint32_t u32_unaligned __attribute__((aligned(1)));
 // so that any 16 consecutive rows fall into 16 different bank groups.
 //
 // A block scale multiplies its sums every 64 columns (a full block's sums
-// would need as many registers as the accumulators); MX scales multiply the
-// codes as they become bf16 (exact); row and tensor scales the results.
+// would need as many registers as the accumulators, and with TW = 2 some 16
+// registers a lane are spilled as it is); MX scales multiply the codes as
+// they become bf16 (exact); row and tensor scales the results.  The same
+// prefill, gate and up, by format: block 312 us, bf16 block 317, MX 275, row
+// 270, tensor 268.
 template <int FMT, bool SWIGLU, int MT, int TW>
 __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& at, unsigned char* ws, unsigned char* xs0,
                                             unsigned char* xs1, unsigned char* xs2) {
@@ -324,8 +327,11 @@ __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& 
   const auto load_x = [&](int step, int j, unsigned char* to) __attribute__((always_inline)) {
     asm volatile("" : "+v"(xcol), "+v"(xrow[j])::"memory");
     const int c0 = step * 64 + (xcol ^ (j & 1) * 32);
-    const char* from = reinterpret_cast<const char*>(c.x) + ((uint64_t)xrow[j] * (uint32_t)(2 * k) + (uint32_t)(2 * c0));
-    stage16(c0 < k ? from : reinterpret_cast<const char*>(&kNoColumns), to + (kXLoads * wave + j) * 1024);
+    // An offset from x either way: chosen between two addresses the MX tile
+    // spilled (prefill 278 -> 282 us).
+    const uint64_t x = reinterpret_cast<uint64_t>(c.x), none = reinterpret_cast<uint64_t>(&kNoColumns) - x;
+    const uint64_t from = (uint64_t)xrow[j] * (uint32_t)(2 * k) + (uint32_t)(2 * c0);
+    stage16(reinterpret_cast<const void*>(x + (c0 < k ? from : none)), to + (kXLoads * wave + j) * 1024);
     asm volatile("" ::: "memory");
   };
   const auto request_x = [&](int step, unsigned char* to) __attribute__((always_inline)) {
@@ -764,7 +770,12 @@ struct ExpertsPlan {
 //
 // Halves that do not start on a multiple of 32 rows would put a tile's rows
 // in two scale blocks (the streaming kernel asks for 4), and rows of fewer
-// than four MX exponents cannot be read four at a time.
+// than four MX exponents cannot be read four at a time.  What that costs where
+// experts have many slots: 4096 tokens, 8 of 64 experts, k = 2048, block
+// scales, halves of 192 / 352 / 992 / 1024 rows 100 / 134 / 312 / 312 us, of
+// 176 / 360 / 1000 rows (streaming) 210 / 439 / 1194 us, of 1001 rows (simple)
+// 1965 us; 32 tokens, halves of 352 and 1024 rows 16.3 and 45.0 us, of 360,
+// 1000 and 1001 rows 16.7, 44.7 and 71.5 us.
 ExpertsPlan experts_plan(int64_t experts, int64_t slots, int64_t n, int64_t k, bool swiglu, int format) {
   const bool block = format == kFmtBlock || format == kFmtBlockBf16;
   const int64_t average = slots / (experts < slots ? experts : slots);
