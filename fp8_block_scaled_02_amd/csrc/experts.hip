@@ -266,7 +266,7 @@ typedef uint32_t u32_unaligned __attribute__((aligned(1)));
 // would need as many registers as the accumulators, and with TW = 2 some 16
 // registers a lane are spilled as it is); MX scales multiply the codes as
 // they become bf16 (exact); row and tensor scales the results.  The same
-// prefill, gate and up, by format: block 312 us, bf16 block 317, MX 275, row
+// prefill, gate and up, by format: block 312 us, bf16 block 309, MX 275, row
 // 270, tensor 268.
 template <int FMT, bool SWIGLU, int MT, int TW>
 __device__ __forceinline__ void experts_run(const ExpertsCall& c, const TileAt& at, unsigned char* ws, unsigned char* xs0,

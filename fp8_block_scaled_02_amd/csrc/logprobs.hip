@@ -622,7 +622,15 @@ int64_t lp_units(int64_t vocab) { return (vocab + kLpSegUnit - 1) / kLpSegUnit; 
 int logprobs_segments(int64_t tokens, int64_t vocab) {
   if (tokens < 1) return 1;
   const int64_t units = lp_units(vocab);
-  int64_t want = (1024 + tokens - 1) / tokens;   // four workgroups a CU
+  // Four workgroups a CU, which is what fits without alternatives; with them
+  // it is three.  A sweep (bf16; rows x vocabulary: us at 512 / 768 / 1024 /
+  // 2048 workgroups):
+  //   top 5   4 x 151936: 11.3 everywhere    64 x 151936: 16.5 17.1 17.3 21.2
+  //           256 x 32000: 15.2 15.1 21.7 21.9    256 x 151936: 28.2 27.5 31.8 37.2
+  //           600 x 14500: 13.9 25.4 25.4 25.4    1000 x 32000: 27.2 27.4 37.0 37.3
+  //   none    64 x 151936: 10.4 11.0 11.1 13.0    600 x 14500: 9.1 15.2 15.2 15.2
+  // so fewer would serve some hundred rows better, up to twofold.
+  int64_t want = (1024 + tokens - 1) / tokens;
   if (want > units) want = units;
   if (want > kLpMaxSegs) want = kLpMaxSegs;
   if (want <= 1) return 1;

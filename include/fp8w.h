@@ -64,15 +64,18 @@
  * calls (fp8w_grouped_plan_init, fp8w_quant_plan_init).
  * fp8w_quantize_act_noalloc resolves its device array on its first call on
  * a device; make that call outside capture too.  Results are bitwise
- * reproducible run to run (no atomics, fixed reduction order).
+ * reproducible run to run: sums have a fixed order, and atomics stand only
+ * where their order cannot show (bits of a mask, integer counts, a running
+ * maximum, the places of keys that are ranked afterwards).
  *
  * Errors: arguments are checked on the host before anything is enqueued; on
  * any error nothing is launched and no output byte is written.  A fault
  * during execution surfaces at the caller's next synchronization of
  * `stream`.  Non-finite inputs are outside the contract: the calls do not
- * fault on them but their outputs are unspecified.  Mis-shaped calls fail
- * loudly instead of miscomputing, as the bounds contract of "feat: add FP8
- * blockwise weight quantization ..." (Security and Safety) asks.
+ * fault on them but their outputs are unspecified, unless a call says what
+ * they give.  Mis-shaped calls fail loudly instead of miscomputing, as the
+ * bounds contract of "feat: add FP8 blockwise weight quantization ..."
+ * (Security and Safety) asks.
  */
 #ifndef FP8W_H_
 #define FP8W_H_
@@ -561,7 +564,8 @@ fp8w_status fp8w_route_experts(const void* logits, fp8w_dtype dtype, int64_t str
  * their ranges are not followed: a slot of such a row gets the products of a
  * row of zeros, offsets are cut to [0, slots].
  * Each product meets the bound of fp8w_gemv (|y - y_ref| <= 2^-7 * sum |x|
- * |deq| + 1e-6).
+ * |deq| + 1e-6).  An infinity or NaN of x reaches its own row's slots alone,
+ * as the formula has it; silu(g) is g for gates up to infinity.
  * Requires 16 <= k <= 2^28, k % 16 == 0, 1 <= n <= 2^28 (SWIGLU: n even),
  * 0 <= slots <= 2^30 (0: no launch), 1 <= experts <= 2^28, x_rows >= 1
  * (x_rows >= slots without rows).
