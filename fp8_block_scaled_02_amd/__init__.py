@@ -182,22 +182,42 @@ def _stream_handle(stream) -> Optional[int]:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _record(stream, handle: int, used) -> None:
+    """Tensors recorded on a stream (a Stream, a handle, or None for the
+    current one): their memory is not handed out again before what the stream
+    was given until then has run."""
+    cuda = _torch().cuda
+    if stream is None:
+        stream = cuda.current_stream()
+    elif not isinstance(stream, cuda.Stream):   # 0 would make an ExternalStream one of the pool's
+        stream = cuda.ExternalStream(handle) if handle else cuda.default_stream()
+    for t in used:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _launch_stream(stream, *used):
     """The handle of the stream a call goes to.  The call's outputs and
     workspaces belong to the stream they were made on, the current one as a
-    rule: used on another, they are recorded there, so that their memory is
-    not handed out again before the kernels have run."""
+    rule: used on another, they are recorded there."""
     handle = _current_handle()
     if stream is None:
         return handle
     current, handle = handle, _stream_handle(stream)
     if handle != current:
-        cuda = _torch().cuda
-        if not isinstance(stream, cuda.Stream):   # 0 would make an ExternalStream one of the pool's
-            stream = cuda.ExternalStream(handle) if handle else cuda.default_stream()
-        for t in used:
-            if t is not None:
-                t.record_stream(stream)
+        _record(stream, handle, used)
+    return handle
+
+
+def _plan_stream(plan, stream, *used):
+    """The same for a plan, whose table and outputs were made some time ago,
+    under any stream: recorded on each stream that the plan is used on, once,
+    since a recording lasts until the memory is freed.  A plan may then be
+    dropped behind its call."""
+    handle = _stream_handle(stream)
+    if handle not in plan.streams:
+        _record(stream, handle, (plan.table, *used))
+        plan.streams.add(handle)
     return handle
 
 
@@ -628,6 +648,7 @@ class GroupedPlan:
                "fp8w_grouped_plan_init")
         self.xs, self.codes, self.scales, self.ys = list(xs), list(codes), list(scales), list(ys)
         self.m, self.fmt = m, fmt
+        self.streams = set()   # handles that the table and ys are recorded on
 
     @property
     def blocks(self) -> int:
@@ -645,7 +666,7 @@ def fp8w_grouped_plan_init(xs, codes, scales, ys=None, fmt="block", route=ROUTE_
 
 def fp8w_gemv_grouped(plan: GroupedPlan, stream=None):
     """Enqueue every GEMV of ``plan`` in one launch; returns the ``y`` list."""
-    _check(lib().fp8w_gemv_grouped(ctypes.byref(plan.plan), _stream_handle(stream)),
+    _check(lib().fp8w_gemv_grouped(ctypes.byref(plan.plan), _plan_stream(plan, stream, *plan.ys)),
            "fp8w_gemv_grouped")
     return plan.ys
 
@@ -685,6 +706,7 @@ class QuantPlan:
         _check(lib().fp8w_quant_plan_init(descs, len(ws), fid, self.table.data_ptr(), ctypes.byref(self.plan)),
                "fp8w_quant_plan_init")
         self.ws, self.codes, self.scales, self.fmt = list(ws), list(codes), list(scales), fmt
+        self.streams = set()   # handles that the table, codes and scales are recorded on
 
     @property
     def blocks(self) -> int:
@@ -700,7 +722,7 @@ def fp8w_quant_plan_init(ws, fmt="block", codes=None, scales=None) -> QuantPlan:
 def fp8w_quantize_grouped(plan: QuantPlan, stream=None):
     """Enqueue the quantization of every weight of ``plan`` in one launch;
     returns (codes list, scales list)."""
-    _check(lib().fp8w_quantize_grouped(ctypes.byref(plan.plan), _stream_handle(stream)),
+    _check(lib().fp8w_quantize_grouped(ctypes.byref(plan.plan), _plan_stream(plan, stream, *plan.codes, *plan.scales)),
            "fp8w_quantize_grouped")
     return plan.codes, plan.scales
 

@@ -57,3 +57,34 @@ def test_default_stream_by_its_handle(F):
         got = F.fp8w_quantize(w, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("by", ["stream", "handle", "current"])
+def test_plans_dropped_behind_their_call(F, by):
+    """A plan made and dropped around one call on a busy stream: its table,
+    which names every buffer, is not reused before the call has run."""
+    a = torch.ones(8192, 8192, dtype=torch.bfloat16, device=dev())
+    ws = [torch.randn(256, 512, device=dev()).to(torch.bfloat16) for _ in range(5)]
+    want = F.fp8w_quantize_grouped(F.fp8w_quant_plan_init(ws))
+    x = torch.randn(2, 512, device=dev()).to(torch.bfloat16)
+    ys = [y.clone() for y in F.fp8w_gemv_grouped(F.fp8w_grouped_plan_init([x] * 5, *want))]
+    side = torch.cuda.Stream()
+    torch.mm(a, a)
+    torch.cuda.synchronize()
+    plan, gemv = F.fp8w_quant_plan_init(ws), F.fp8w_grouped_plan_init([x] * 5, *want)
+    table, other = plan.table.data_ptr(), gemv.table.data_ptr()
+    _occupy(side, a)
+    if by == "current":
+        with torch.cuda.stream(side):
+            got, out = F.fp8w_quantize_grouped(plan), F.fp8w_gemv_grouped(gemv)
+    else:
+        s = side if by == "stream" else side.cuda_stream
+        got, out = F.fp8w_quantize_grouped(plan, s), F.fp8w_gemv_grouped(gemv, s)
+    size = plan.table.numel(), gemv.table.numel()
+    busy = not side.query()
+    del plan, gemv
+    fresh = [torch.empty(n, dtype=torch.uint8, device=dev()) for n in size for _ in range(4)]
+    assert not busy or not {table, other} & {f.data_ptr() for f in fresh}
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip((*got[0], *got[1]), (*want[0], *want[1])))
+    assert all(torch.equal(p, q) for p, q in zip(out, ys))

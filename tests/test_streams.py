@@ -38,6 +38,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t, s)))
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h: ("stream", h))
     monkeypatch.setattr(torch.cuda, "default_stream", lambda: "the default stream")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: "the current stream")
     return made, recorded
 
 
@@ -93,3 +94,28 @@ def test_nothing_is_recorded_on_the_current_stream(calls, name, stream):
     made, recorded = calls
     CALLS[name](stream)
     assert made and not recorded
+
+
+PLANS = {
+    "gemv": (lambda: F.fp8w_grouped_plan_init([x, x], [codes, codes], [block, block]), F.fp8w_gemv_grouped, 3),
+    "quantize": (lambda: F.fp8w_quant_plan_init([w, w]), F.fp8w_quantize_grouped, 5),
+}
+
+
+@pytest.mark.parametrize("name", PLANS)
+@pytest.mark.parametrize("stream,recorded_as", [(Raw(), ("stream", SIDE)), (SIDE, ("stream", SIDE)),
+                                                (0, "the default stream"), (None, "the current stream")])
+def test_plans_are_recorded_once_a_stream(calls, name, stream, recorded_as):
+    """Table and outputs, also on the current stream: the plan may have been
+    made under another."""
+    made, recorded = calls
+    make, use, count = PLANS[name]
+    plan = make()
+    assert len(made) == count and not recorded
+    use(plan, stream)
+    assert {t.data_ptr() for t, _ in recorded} == {t.data_ptr() for t in made}
+    assert all(s == recorded_as for _, s in recorded)
+    use(plan, stream)
+    assert len(recorded) == count
+    use(plan, 33)
+    assert len(recorded) == 2 * count and recorded[-1][1] == ("stream", 33)
