@@ -40,7 +40,7 @@ def terms_of_the_wrong_base(x):
     m = x.max(axis=1, keepdims=True)
     e = (x - m).astype(np.float64)
     p = np.exp(e)
-    return lp, (np.log(p.sum(1)) - (e * p).sum(1) / p.sum(1) * 0.6932).astype(F32)   # ln 2 of four digits, once too often
+    return lp, (np.log(p.sum(1)) - 0.6932 * (e * p).sum(1) / p.sum(1)).astype(F32)   # ln 2 once too often
 
 
 def eight_bits(x):

@@ -17,6 +17,6 @@ def test_softmax_of_the_chosen_however_far_below():
 def test_sigmoid_scores_that_are_zero_in_fp32():
     x = np.array([[-103.0, -104.5], [-104.5, -105.0], [-np.inf, -200.0], [-60.0, -61.0]])
     ids, w, *_ = S.route(x, 2, "sigmoid")
-    assert np.allclose(w[[0, 3]], [[1 / (1 + np.exp(-1.5)), 1 / (1 + np.exp(1.5))], [1 / (1 + np.exp(-1)), 1 / (1 + np.exp(1))]])
+    assert np.allclose(w[[0, 3]], [[1 / (1 + np.exp(-d)), 1 / (1 + np.exp(d))] for d in (1.5, 1.0)])
     assert (w[1:3] == 0).all() and ids.tolist() == [[0, 1], [0, 1], [1, -1], [0, 1]]
     assert (S.route(x, 2, "sigmoid", renorm=False)[1][:2] > 0).all()
