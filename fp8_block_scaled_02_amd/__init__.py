@@ -209,6 +209,16 @@ def _launch_stream(stream, *used):
     return handle
 
 
+def _table(nbytes: int, device):
+    """Device memory for a plan's table, which the set-up call writes at once,
+    not in a stream's order: what the current stream may still do with the
+    memory it is made of comes first."""
+    torch = _torch()
+    table = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    torch.cuda.current_stream().synchronize()
+    return table
+
+
 def _plan_stream(plan, stream, *used):
     """The same for a plan, whose table and outputs were made some time ago,
     under any stream: recorded on each stream that the plan is used on, once,
@@ -641,7 +651,7 @@ class GroupedPlan:
                 raise ValueError(f"grouped GEMV {i}: inconsistent shapes")
             descs[i] = GemvDesc(x.data_ptr(), c.data_ptr(), s.data_ptr(), y.data_ptr(), n, k)
         nbytes = int(lib().fp8w_grouped_table_bytes(len(xs)))
-        self.table = torch.empty(nbytes, dtype=torch.uint8, device=codes[0].device)
+        self.table = _table(nbytes, codes[0].device)
         self.plan = GroupedPlanC()
         _check(lib().fp8w_grouped_plan_init(descs, len(xs), m, fmt_id, int(route),
                                             self.table.data_ptr(), ctypes.byref(self.plan)),
@@ -701,7 +711,7 @@ class QuantPlan:
             _check_scales(torch, fmt, sc, n, k, "fp8w_quant_plan_init")
             descs[i] = QuantDesc(w.data_ptr(), c.data_ptr(), sc.data_ptr(), n, k)
         nbytes = int(lib().fp8w_quant_table_bytes(len(ws)))
-        self.table = torch.empty(nbytes, dtype=torch.uint8, device=ws[0].device)
+        self.table = _table(nbytes, ws[0].device)
         self.plan = QuantPlanC()
         _check(lib().fp8w_quant_plan_init(descs, len(ws), fid, self.table.data_ptr(), ctypes.byref(self.plan)),
                "fp8w_quant_plan_init")

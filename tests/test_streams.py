@@ -12,12 +12,26 @@ CURRENT, SIDE = 11, 22
 
 class Library:
     def __getattr__(self, name):
-        return (lambda *a: 64) if name.endswith("_bytes") else (lambda *a: 0)
+        if name.endswith("_bytes"):
+            return lambda *a: 64
+        Current.order.append(name)
+        return lambda *a: 0
 
 
 class Raw:
     """A stream of another library: a handle and nothing else."""
     cuda_stream = SIDE
+
+
+class Current:
+    """The current stream; `order` is what happened to it and in the library."""
+    order = []
+
+    def synchronize(self):
+        Current.order.append("synchronize")
+
+    def __eq__(self, other):
+        return isinstance(other, Current)
 
 
 @pytest.fixture
@@ -38,7 +52,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t, s)))
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h: ("stream", h))
     monkeypatch.setattr(torch.cuda, "default_stream", lambda: "the default stream")
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda: "the current stream")
+    monkeypatch.setattr(torch.cuda, "current_stream", Current)
     return made, recorded
 
 
@@ -104,7 +118,7 @@ PLANS = {
 
 @pytest.mark.parametrize("name", PLANS)
 @pytest.mark.parametrize("stream,recorded_as", [(Raw(), ("stream", SIDE)), (SIDE, ("stream", SIDE)),
-                                                (0, "the default stream"), (None, "the current stream")])
+                                                (0, "the default stream"), (None, Current())])
 def test_plans_are_recorded_once_a_stream(calls, name, stream, recorded_as):
     """Table and outputs, also on the current stream: the plan may have been
     made under another."""
@@ -119,3 +133,12 @@ def test_plans_are_recorded_once_a_stream(calls, name, stream, recorded_as):
     assert len(recorded) == count
     use(plan, 33)
     assert len(recorded) == 2 * count and recorded[-1][1] == ("stream", 33)
+
+
+@pytest.mark.parametrize("name", PLANS)
+def test_tables_are_written_behind_the_current_stream(calls, name):
+    """The set-up call writes the table at once; memory from the allocator may
+    still be in use by what the current stream was given before."""
+    Current.order.clear()
+    PLANS[name][0]()
+    assert Current.order == ["synchronize", {"gemv": "fp8w_grouped_plan_init", "quantize": "fp8w_quant_plan_init"}[name]]
