@@ -29,6 +29,10 @@ Functions carry the names of the C entry points:
   token's experts
 * ``fp8w_logprobs(logits, targets, top) -> Logprobs``: log probabilities of
   given tokens, entropy and top alternatives
+* ``fp8w_linear(x, codes, scales, bias, act, residual) -> y``: the product for
+  any m with bias, activation and residual in its epilogue
+* ``fp8w_sample(logits, uniforms, temperature, top_k, top_p, min_p) -> Sampled``:
+  a token drawn from each row
 
 plus ``Fp8Experts``, the fp8 weights of a layer's experts, and ``Fp8Weight``,
 a format-tagged weight whose GEMV asserts the format before dispatch (a scale
@@ -87,10 +91,16 @@ SIGNATURES = {
     "fp8w_route_experts_workspace_bytes": (_I64, [_I64, _I64]),
     "fp8w_route_experts": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I, _P, _I, ctypes.c_float, _P, _P, _P, _P, _P,
                                 _P, _I64, _P]),
+    "fp8w_route_experts_grouped": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I, _P, _I64, _I64, _I, _I, ctypes.c_float,
+                                        _P, _P, _P, _P, _P, _P, _I64, _P]),
     "fp8w_gemm_experts": (_I, [_P, _I64, _P, _P, _I64, _I64, _P, _P, _I, _I64, _I64, _I, _P, _P]),
     "fp8w_combine_experts": (_I, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _P]),
     "fp8w_logprobs_workspace_bytes": (_I64, [_I64, _I64, _I64]),
     "fp8w_logprobs": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P]),
+    "fp8w_linear_workspace_bytes": (_I64, [_I64, _I64, _I64, _I, _I]),
+    "fp8w_linear": (_I, [_P, _I64, _I64, _P, _P, _I, _I64, _I64, _P, _I, _I, _P, _I64, _P, _I, _I64, _P, _I64, _P]),
+    "fp8w_sample_workspace_bytes": (_I64, [_I64, _I64]),
+    "fp8w_sample": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
     "fp8w_block_scale_count": (_I64, [_I64, _I64]),
     "fp8w_mx_scale_count": (_I64, [_I64, _I64]),
     "fp8w_status_string": (ctypes.c_char_p, [_I]),
@@ -740,6 +750,7 @@ def fp8w_quantize_grouped(plan: QuantPlan, stream=None):
 # ---------------------------------------------------------------- experts --
 
 SCORE_IDS = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE_IDS = {"max": 0, "top2": 1}
 ACT_IDS = {"none": 0, "swiglu": 1}
 
 
@@ -793,6 +804,14 @@ def _buffer(t, shape, dtype, device, what: str):
     raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
 
 
+def _on_current_device(*tensors) -> None:
+    """Calls go to the current device: tensors of another one are refused."""
+    current = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"tensors must be on the current device (cuda:{current}), got {t.device}")
+
+
 def _workspace_bytes(t) -> int:
     """The size of a caller's workspace, any GPU tensor without gaps."""
     if not t.is_cuda or not t.is_contiguous():
@@ -802,15 +821,21 @@ def _workspace_bytes(t) -> int:
 
 def fp8w_route_experts(logits, top_k: int, score: str = "softmax", bias=None, renorm: bool = True,
                        scale: float = 1.0, ids=None, weights=None, slots=None, rows=None, offsets=None,
-                       workspace=None, stream=None) -> ExpertRouting:
+                       workspace=None, stream=None, groups: int = 1, top_groups: Optional[int] = None,
+                       group_score: str = "max") -> ExpertRouting:
     """Router logits [tokens, experts] (bf16 or f32) -> each token's ``top_k``
-    experts, their weights, and the map that sorts the tokens by expert."""
+    experts, their weights, and the map that sorts the tokens by expert.  With
+    ``groups`` the experts are chosen from the token's ``top_groups`` best
+    groups (all, if None) of neighbouring experts, rated by their best key
+    (``group_score="max"``) or the sum of their two best (``"top2"``)."""
     torch = _torch()
     dtype, stride = _logits(logits, "logits")
     t, e = logits.shape
     k = int(top_k)
     if score not in SCORE_IDS:
         raise ValueError(f"unknown score {score!r}")
+    if group_score not in GROUP_SCORE_IDS:
+        raise ValueError(f"unknown group_score {group_score!r}")
     if bias is not None:
         _require(bias, (torch.float32,), "bias", 1)
         if bias.shape[0] != e:
@@ -829,8 +854,9 @@ def fp8w_route_experts(logits, top_k: int, score: str = "softmax", bias=None, re
     elif t > 32:
         need = lib().fp8w_route_experts_workspace_bytes(t, e)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(lib().fp8w_route_experts(
+    _check(lib().fp8w_route_experts_grouped(
         logits.data_ptr(), dtype, stride, t, e, k, SCORE_IDS[score], None if bias is None else bias.data_ptr(),
+        groups, groups if top_groups is None else top_groups, GROUP_SCORE_IDS[group_score],
         1 if renorm else 0, scale, ids.data_ptr(), weights.data_ptr(), slots.data_ptr(), rows.data_ptr(),
         offsets.data_ptr(), None if workspace is None else workspace.data_ptr(), need,
         _launch_stream(stream, ids, weights, slots, rows, offsets, workspace)), "fp8w_route_experts")
@@ -959,6 +985,127 @@ def fp8w_logprobs(logits, targets=None, top: int = 0, logprob=None, entropy=None
     return Logprobs(logprob, entropy, top_ids, top_logprobs)
 
 
+# ----------------------------------------------------------------- linear --
+
+LINEAR_ACT_IDS = {"none": 0, "swiglu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "relu": 5, "geglu": 6}
+
+
+def _rows_of(t, dtypes, shape, what: str) -> int:
+    """The row stride of a matrix whose rows are contiguous, after a check."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: must be a GPU tensor (libfp8w has no CPU path)")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{what}: expected shape {shape or '[rows, columns]'}, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    stride = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or stride < cols:
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap")
+    return stride
+
+
+def fp8w_linear(x, codes, scales, fmt: str = "block", bias=None, act: str = "none", residual=None, y=None,
+                out_dtype=None, workspace=None, stream=None):
+    """y = act(x . deq(W)^T + bias) + residual for any number of rows: x bf16
+    [m,k], codes u8 [n,k], bias bf16 or f32 [n], residual bf16, y bf16 or f32
+    (``out_dtype``, bf16 as a rule) [m,n]; x, residual and y may be parts of
+    wider rows.  ``act="swiglu"`` and ``"geglu"`` multiply the activated first
+    half of columns by the second: y and residual are [m,n/2].  y may be the
+    residual itself."""
+    torch = _torch()
+    bf16 = _bf16_like(torch)
+    x_stride = _rows_of(x, bf16, None, "x")
+    _require(codes, (torch.uint8,), "codes", 2)
+    if act not in LINEAR_ACT_IDS:
+        raise ValueError(f"unknown act {act!r}")
+    fid, aid = _format_id(fmt), LINEAR_ACT_IDS[act]
+    m, k = x.shape
+    n = codes.shape[0]
+    if codes.shape[1] != k:
+        raise ValueError(f"fp8w_linear: x has {k} columns, the weights {codes.shape[1]}")
+    _check_scales(torch, fmt, scales, n, k, "fp8w_linear")
+    gated = act in ("swiglu", "geglu")
+    if gated and n % 2:
+        raise Fp8wError(ERR_SHAPE, "fp8w_linear")
+    shape = (m, n // 2 if gated else n)
+    bias_dtype = 0
+    if bias is not None:
+        _require(bias, (*bf16, torch.float32), "bias", 1)
+        if bias.shape[0] != n:
+            raise ValueError(f"bias: expected shape {(n,)}, got {tuple(bias.shape)}")
+        bias_dtype = 1 if bias.dtype is torch.float32 else 0
+    residual_stride = 0 if residual is None else _rows_of(residual, bf16, shape, "residual")
+    if y is None:
+        y = torch.empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=x.device)
+    elif out_dtype is not None and y.dtype is not out_dtype:
+        raise TypeError(f"y: dtype {y.dtype} is not out_dtype {out_dtype}")
+    y_stride = _rows_of(y, (*bf16, torch.float32), shape, "y")
+    _on_current_device(x, codes, scales, bias, residual, y, workspace)
+    if workspace is not None:
+        need = _workspace_bytes(workspace)
+    else:
+        need = lib().fp8w_linear_workspace_bytes(m, n, k, fid, aid)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _check(lib().fp8w_linear(
+        x.data_ptr(), x_stride, m, codes.data_ptr(), scales.data_ptr(), fid, n, k,
+        None if bias is None else bias.data_ptr(), bias_dtype, aid, None if residual is None else residual.data_ptr(),
+        residual_stride, y.data_ptr(), 1 if y.dtype is torch.float32 else 0, y_stride,
+        None if workspace is None else workspace.data_ptr(), need, _launch_stream(stream, y, workspace)), "fp8w_linear")
+    return y
+
+
+# ----------------------------------------------------------------- sample --
+
+class Sampled(NamedTuple):
+    """``tokens`` [rows] (-1 for a row masked throughout), ``logprob`` of each
+    among the tokens it was drawn from, and ``kept``, how many those were."""
+    tokens: object
+    logprob: object
+    kept: object
+
+
+def fp8w_sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprob=None,
+                kept=None, workspace=None, stream=None) -> Sampled:
+    """A token drawn from each row of logits (bf16 or f32 [rows, vocab]) by one
+    random number in [0, 1) (f32 [rows]), under the rows' own settings: f32
+    ``temperature`` (0 takes the most likely token), ``top_p`` and ``min_p``, i32
+    ``top_k``, each [rows] or None for off."""
+    torch = _torch()
+    dtype, stride = _logits(logits, "logits")
+    t, v = logits.shape
+    dev, f32 = logits.device, torch.float32
+    given = []
+    for what, s, d in (("uniforms", uniforms, f32), ("temperature", temperature, f32), ("top_k", top_k, torch.int32),
+                       ("top_p", top_p, f32), ("min_p", min_p, f32)):
+        if s is None and what != "uniforms":
+            given.append(None)
+            continue
+        _require(s, (d,), what, 1)
+        if s.shape[0] != t:
+            raise ValueError(f"{what}: expected shape {(t,)}, got {tuple(s.shape)}")
+        given.append(s.data_ptr())
+    tokens = _buffer(tokens, (t,), torch.int32, dev, "tokens")
+    logprob = _buffer(logprob, (t,), f32, dev, "logprob")
+    kept = _buffer(kept, (t,), torch.int32, dev, "kept")
+    _on_current_device(logits, uniforms, temperature, top_k, top_p, min_p, tokens, logprob, kept, workspace)
+    if workspace is not None:
+        need = _workspace_bytes(workspace)
+    else:
+        need = lib().fp8w_sample_workspace_bytes(t, v)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib().fp8w_sample(
+        logits.data_ptr(), dtype, stride, t, v, *given, tokens.data_ptr(), logprob.data_ptr(), kept.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), need,
+        _launch_stream(stream, tokens, logprob, kept, workspace)), "fp8w_sample")
+    return Sampled(tokens, logprob, kept)
+
+
 # ----------------------------------------------------------- tagged weight --
 
 BLOCK128, MX32, BLOCK128_BF16, ROW, TENSOR = "block128", "mx32", "block128_bf16", "row", "tensor"
@@ -1014,6 +1161,13 @@ class Fp8Weight:
         if int(x.shape[0]) <= MAX_M:
             return self.gemv(x, y, ROUTE_AUTO, stream)
         return fp8w_gemm(x, self.codes, self.scales, self.format, y, workspace, stream)
+
+    def linear(self, x, bias=None, act: str = "none", residual=None, y=None, out_dtype=None, workspace=None,
+               stream=None):
+        """act(x . deq(W)^T + bias) + residual (``fp8w_linear``)."""
+        self.check_format()
+        return fp8w_linear(x, self.codes, self.scales, self.format, bias, act, residual, y, out_dtype, workspace,
+                           stream)
 
     def gemv_w8a8(self, x_codes, x_scale, y=None, stream=None):
         self.check_format()

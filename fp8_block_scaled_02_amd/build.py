@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8w.so")
 SOURCES = ["quantize.hip", "gemv.hip", "dequant.hip", "read_ceiling.hip", "route.hip",
-           "experts.hip", "logprobs.hip", "gemm.cpp", "api.cpp"]
+           "experts.hip", "logprobs.hip", "linear.hip", "sample.hip", "gemm.cpp", "api.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -563,6 +563,7 @@ namespace {
 // Workgroups of one launch: the runtime counts a grid's threads in 32 bits.
 constexpr int64_t kMaxBlocks256 = 0xFFFFFFFF / 256;
 constexpr int64_t kMaxBlocks512 = 0xFFFFFFFF / 512;
+constexpr int64_t kMaxBlocks1024 = 0xFFFFFFFF / 1024;
 
 // The grouped products step past the end of rows, columns and slots in 32
 // bits (whole tiles; eight rows of codes from one) before they compare.
@@ -591,10 +592,26 @@ FP8W_API fp8w_status fp8w_route_experts(const void* logits, fp8w_dtype dtype, in
                                         int renorm, float scale, int32_t* ids, float* weights, int32_t* slots,
                                         int32_t* rows, int32_t* offsets, void* workspace,
                                         int64_t workspace_bytes, void* stream) {
+  return fp8w_route_experts_grouped(logits, dtype, stride, tokens, experts, top_k, score, bias, 1, 1, FP8W_GROUP_MAX,
+                                    renorm, scale, ids, weights, slots, rows, offsets, workspace, workspace_bytes,
+                                    stream);
+}
+
+FP8W_API fp8w_status fp8w_route_experts_grouped(const void* logits, fp8w_dtype dtype, int64_t stride, int64_t tokens,
+                                                int64_t experts, int64_t top_k, fp8w_score score, const float* bias,
+                                                int64_t groups, int64_t top_groups, fp8w_group_score group_score,
+                                                int renorm, float scale, int32_t* ids, float* weights, int32_t* slots,
+                                                int32_t* rows, int32_t* offsets, void* workspace,
+                                                int64_t workspace_bytes, void* stream) {
   if (!offsets || (tokens != 0 && (!logits || !ids || !weights || !slots || !rows))) return FP8W_ERR_NULL;
-  if (!dtype_ok(dtype) || (score != FP8W_SCORE_SOFTMAX && score != FP8W_SCORE_SIGMOID)) return FP8W_ERR_UNSUPPORTED;
+  if (!dtype_ok(dtype) || (score != FP8W_SCORE_SOFTMAX && score != FP8W_SCORE_SIGMOID) ||
+      (group_score != FP8W_GROUP_MAX && group_score != FP8W_GROUP_TOP2))
+    return FP8W_ERR_UNSUPPORTED;
   if (!route_shape_ok(tokens, experts) || top_k < 1 || top_k > experts || top_k > FP8W_MAX_TOP_K ||
       tokens * top_k > kMaxDim || stride < experts || stride > kMaxDim)
+    return FP8W_ERR_SHAPE;
+  if (groups < 1 || groups > FP8W_MAX_GROUPS || experts % groups != 0 || top_groups < 1 || top_groups > groups ||
+      top_k > top_groups * (experts / groups))
     return FP8W_ERR_SHAPE;
   const int64_t need = fp8w::route_workspace_bytes(tokens, experts);
   if (need > 0 && !workspace) return FP8W_ERR_NULL;
@@ -608,9 +625,11 @@ FP8W_API fp8w_status fp8w_route_experts(const void* logits, fp8w_dtype dtype, in
   const Span in[2] = {{logits, strided_bytes(tokens, experts, stride, dtype_bytes(dtype))},
                       {bias, bias ? (uint64_t)experts * 4 : 0}};
   if (any_overlap(out, 6, in, 2)) return FP8W_ERR_OVERLAP;
+  const bool open = top_groups == groups;   // no group is shut: the choice among all
   const fp8w::RouteCall c{logits, bias, ids, weights, slots, rows, offsets, workspace, stride, scale,
                           (int32_t)tokens, (int32_t)experts, (int32_t)top_k, score, renorm ? 1 : 0,
-                          dtype == FP8W_DTYPE_F32};
+                          dtype == FP8W_DTYPE_F32, open ? 1 : (int32_t)groups, open ? 1 : (int32_t)top_groups,
+                          group_score == FP8W_GROUP_TOP2};
   return from_hip(fp8w::launch_route_experts(c, static_cast<hipStream_t>(stream)));
 }
 
@@ -701,6 +720,106 @@ FP8W_API fp8w_status fp8w_logprobs(const void* logits, fp8w_dtype dtype, int64_t
   const fp8w::LogprobsCall c{logits, targets, logprob, entropy, top_ids, top_logprobs, workspace, stride,
                              (int32_t)tokens, (int32_t)vocab, (int32_t)top, dtype == FP8W_DTYPE_F32};
   return from_hip(fp8w::launch_logprobs(c, static_cast<hipStream_t>(stream)));
+}
+
+// -------------------------------------------------------------- linear --
+
+namespace {
+
+bool act_ok(int a) { return a >= FP8W_ACT_NONE && a <= FP8W_ACT_GEGLU; }
+bool act_gated(int a) { return a == FP8W_ACT_SWIGLU || a == FP8W_ACT_GEGLU; }
+
+// The products step past the end of rows, columns and tokens in 32 bits
+// (whole tiles; eight rows of codes from one) before they compare.
+constexpr int64_t kMaxLinearNK = 1 << 28, kMaxLinearM = 1 << 30;
+
+bool linear_shape_ok(int64_t m, int64_t n, int64_t k, int act) {
+  return m >= 0 && m <= kMaxLinearM && n >= 1 && n <= kMaxLinearNK && k >= 16 && k <= kMaxLinearNK &&
+         !(act_gated(act) && n % 2 != 0);
+}
+
+}  // namespace
+
+FP8W_API int64_t fp8w_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, fp8w_format format, fp8w_act act) {
+  if (!format_ok(format) || !act_ok(act) || !linear_shape_ok(m, n, k, act) || m == 0) return 0;
+  return fp8w::linear_workspace_bytes(m, n, k, format, act);
+}
+
+FP8W_API fp8w_status fp8w_linear(const uint16_t* x, int64_t x_stride, int64_t m, const uint8_t* codes,
+                                 const void* scales, fp8w_format format, int64_t n, int64_t k, const void* bias,
+                                 fp8w_dtype bias_dtype, fp8w_act act, const uint16_t* residual,
+                                 int64_t residual_stride, void* y, fp8w_dtype y_dtype, int64_t y_stride,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!codes || !scales || (m != 0 && (!x || !y))) return FP8W_ERR_NULL;
+  if (!format_ok(format) || !act_ok(act) || !dtype_ok(y_dtype) || (bias && !dtype_ok(bias_dtype)))
+    return FP8W_ERR_UNSUPPORTED;
+  if (!linear_shape_ok(m, n, k, act)) return FP8W_ERR_SHAPE;
+  const int64_t n_out = act_gated(act) ? n / 2 : n;
+  if (x_stride < k || x_stride > kMaxDim || y_stride < n_out || y_stride > kMaxDim ||
+      (residual && (residual_stride < n_out || residual_stride > kMaxDim)))
+    return FP8W_ERR_SHAPE;
+  if (k % 16 != 0 || x_stride % 8 != 0 || !aligned(x, 16) || !aligned(codes, 16) ||
+      !aligned(scales, scale_align(format)) || !aligned(bias, dtype_bytes(bias_dtype)) || !aligned(residual, 2) ||
+      !aligned(y, dtype_bytes(y_dtype)))
+    return FP8W_ERR_ALIGN;
+  if (m == 0) return FP8W_OK;
+  const int64_t need = fp8w::linear_workspace_bytes(m, n, k, format, act);
+  if (need > 0 && !workspace) return FP8W_ERR_NULL;
+  if (need > 0 && workspace_bytes < need) return FP8W_ERR_SHAPE;
+  if (need > 0 && !aligned(workspace, 16)) return FP8W_ERR_ALIGN;
+  // in place: each value of the residual is read by the thread that writes it
+  const bool in_place = residual == y && y_dtype == FP8W_DTYPE_BF16 && residual_stride == y_stride;
+  const Span out[2] = {{y, strided_bytes(m, n_out, y_stride, dtype_bytes(y_dtype))}, {workspace, (uint64_t)need}};
+  const Span in[5] = {{x, strided_bytes(m, k, x_stride, 2)}, {codes, (uint64_t)n * k},
+                      {scales, scale_bytes(format, n, k)}, {bias, bias ? (uint64_t)n * dtype_bytes(bias_dtype) : 0},
+                      {residual, residual && !in_place ? strided_bytes(m, n_out, residual_stride, 2) : 0}};
+  if (any_overlap(out, 2, in, 5)) return FP8W_ERR_OVERLAP;
+  if (fp8w::linear_blocks(m, n, k, format, act) > kMaxBlocks512) return FP8W_ERR_SHAPE;
+  const fp8w::LinearCall c{x, codes, scales, bias, residual, y, workspace, (int32_t)x_stride,
+                           (int32_t)residual_stride, (int32_t)y_stride, (int32_t)m, (int32_t)n, (int32_t)k, format, act,
+                           bias_dtype == FP8W_DTYPE_F32, y_dtype == FP8W_DTYPE_F32};
+  return from_hip(fp8w::launch_linear(c, static_cast<hipStream_t>(stream)));
+}
+
+// -------------------------------------------------------------- sample --
+
+namespace {
+
+bool sample_shape_ok(int64_t tokens, int64_t vocab) {
+  return tokens >= 0 && tokens <= kMaxDim && vocab >= 1 && vocab <= kMaxDim - 63;
+}
+
+}  // namespace
+
+FP8W_API int64_t fp8w_sample_workspace_bytes(int64_t tokens, int64_t vocab) {
+  return sample_shape_ok(tokens, vocab) ? fp8w::sample_workspace_bytes(tokens, vocab) : 0;
+}
+
+FP8W_API fp8w_status fp8w_sample(const void* logits, fp8w_dtype dtype, int64_t stride, int64_t tokens, int64_t vocab,
+                                 const float* uniforms, const float* temperature, const int32_t* top_k,
+                                 const float* top_p, const float* min_p, int32_t* ids, float* logprob, int32_t* kept,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+  if (tokens != 0 && (!logits || !uniforms || !ids)) return FP8W_ERR_NULL;
+  if (!dtype_ok(dtype)) return FP8W_ERR_UNSUPPORTED;
+  if (!sample_shape_ok(tokens, vocab) || stride < vocab || stride > kMaxDim) return FP8W_ERR_SHAPE;
+  const int64_t need = fp8w::sample_workspace_bytes(tokens, vocab);
+  if (need > 0 && !workspace) return FP8W_ERR_NULL;
+  if (need > 0 && workspace_bytes < need) return FP8W_ERR_SHAPE;
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(uniforms, 4) || !aligned(temperature, 4) ||
+      !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(ids, 4) || !aligned(logprob, 4) ||
+      !aligned(kept, 4) || (need > 0 && !aligned(workspace, 16)))
+    return FP8W_ERR_ALIGN;
+  if (tokens == 0) return FP8W_OK;
+  const uint64_t row = (uint64_t)tokens * 4;
+  const Span out[4] = {{ids, row}, {logprob, logprob ? row : 0}, {kept, kept ? row : 0}, {workspace, (uint64_t)need}};
+  const Span in[6] = {{logits, strided_bytes(tokens, vocab, stride, dtype_bytes(dtype))}, {uniforms, row},
+                      {temperature, temperature ? row : 0}, {top_k, top_k ? row : 0}, {top_p, top_p ? row : 0},
+                      {min_p, min_p ? row : 0}};
+  if (any_overlap(out, 4, in, 6)) return FP8W_ERR_OVERLAP;
+  if (tokens * fp8w::sample_segments(tokens, vocab) > kMaxBlocks1024) return FP8W_ERR_SHAPE;
+  const fp8w::SampleCall c{logits, uniforms, temperature, top_k, top_p, min_p, ids, logprob, kept, workspace, stride,
+                           (int32_t)tokens, (int32_t)vocab, dtype == FP8W_DTYPE_F32};
+  return from_hip(fp8w::launch_sample(c, static_cast<hipStream_t>(stream)));
 }
 
 // ------------------------------------------------------------- helpers --

@@ -12,6 +12,7 @@
 
 #include <type_traits>
 
+#include "act.hpp"
 #include "device.hpp"
 #include "internal.hpp"
 
@@ -120,21 +121,6 @@ struct Runs {
 __device__ __forceinline__ TileAt tile_at(const int32_t* offsets, int experts, int slots, int height, int n_groups) {
   if (experts <= kRunsFew) return Runs<true>(offsets, experts, slots, height, n_groups).at(blockIdx.x >> 3);
   return Runs<false>(offsets, experts, slots, height, n_groups).at(blockIdx.x >> 3);
-}
-
-// silu(g) * u within a few units of the last place of fp32: exp(-g) as 2^t
-// times a first-order correction for what rounding t = -g log2 e lost, and
-// the hardware reciprocal (an IEEE division of every output cost as many
-// instructions as a third of the products at k = 2048).
-__device__ __forceinline__ float silu_times(float g, float u) {
-  constexpr float kLog2E = 0x1.715476p+0f, kLog2ELow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  // Beyond 200 either way 2^t is infinite and the result zero, or it is zero
-  // and silu(g) is g, up to infinity.
-  const float a = -__builtin_amdgcn_fmed3f(g, -200.0f, 200.0f);
-  const float t = a * kLog2E;
-  const float lost = __builtin_fmaf(a, kLog2ELow, __builtin_fmaf(a, kLog2E, -t));
-  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(lost, kLn2, 1.0f);
-  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
 // The simple kernel: one wave takes 16 weight rows (with SWIGLU 16 of each

@@ -16,6 +16,9 @@ constexpr int kFmtBlockBf16 = 2;   // bf16 per 128x128 tile
 constexpr int kFmtRow = 3;         // fp32 per row
 constexpr int kFmtTensor = 4;      // one fp32 for the whole weight
 
+// Activations (the values of fp8w_act).
+constexpr int kActNone = 0, kActSwiglu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActRelu = 5, kActGeglu = 6;
+
 // One GEMV y[m, n] = x[m, k] . deq(codes)^T.  The same layout is the row of
 // a grouped launch's device table (fp8w_grouped_plan_init writes it).
 struct GemvJob {
@@ -149,6 +152,7 @@ struct RouteCall {
   int64_t stride;
   float scale;
   int32_t tokens, experts, top_k, score, renorm, f32;
+  int32_t groups, top_groups, group_top2;   // groups 1: every expert is open
 };
 int64_t route_workspace_bytes(int64_t tokens, int64_t experts);
 hipError_t launch_route_experts(const RouteCall& c, hipStream_t stream);
@@ -189,5 +193,40 @@ struct LogprobsCall {
 int logprobs_segments(int64_t tokens, int64_t vocab);
 int64_t logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t top);
 hipError_t launch_logprobs(const LogprobsCall& c, hipStream_t stream);
+
+// A product with its epilogue: see linear.hip.
+struct LinearCall {
+  const uint16_t* x;        // bf16 [m, k]
+  const uint8_t* codes;     // e4m3fn [n, k]
+  const void* scales;       // in `format`
+  const void* bias;         // bf16 or f32 [n], or null
+  const uint16_t* residual; // bf16 [m, n_out], or null
+  void* y;                  // bf16 or f32 [m, n_out]
+  void* workspace;          // linear_workspace_bytes
+  int32_t x_stride, residual_stride, y_stride;   // elements
+  int32_t m, n, k, format, act, bias_f32, y_f32;
+};
+int64_t linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int format, int act);
+int64_t linear_blocks(int64_t m, int64_t n, int64_t k, int format, int act);   // largest grid of the call
+hipError_t launch_linear(const LinearCall& c, hipStream_t stream);
+
+// Drawn tokens: see sample.hip.
+struct SampleCall {
+  const void* logits;
+  const float* uniforms;
+  const float* temperature; // null: 1
+  const int32_t* top_k;     // null: all
+  const float* top_p;       // null: 1
+  const float* min_p;       // null: 0
+  int32_t* ids;
+  float* logprob;           // may be null
+  int32_t* kept;            // may be null
+  void* workspace;          // sample_workspace_bytes
+  int64_t stride;
+  int32_t tokens, vocab, f32;
+};
+int sample_segments(int64_t tokens, int64_t vocab);
+int64_t sample_workspace_bytes(int64_t tokens, int64_t vocab);
+hipError_t launch_sample(const SampleCall& c, hipStream_t stream);
 
 }  // namespace fp8w

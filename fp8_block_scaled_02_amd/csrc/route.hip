@@ -13,7 +13,9 @@
 //   softmax  w = exp(l - max) / sum      over the chosen (renorm) or all experts
 //   sigmoid  w = 1 / (1 + exp(-l)),      over the sum of the chosen if renorm
 //                                        (0 if all of them are 0 in fp32)
-// times `scale`.  The pairs (t, j) sorted by expert, then token, are the
+// times `scale`.  With experts in groups only those of the token's best groups
+// can be chosen: a group is rated by its experts' best key or by the sum of
+// its two best (scores, in fp64).  The pairs (t, j) sorted by expert, then token, are the
 // slots of the grouped products: offsets[e] .. offsets[e + 1) are expert e's
 // and rows[slot] = t.
 //
@@ -129,6 +131,8 @@ struct RouteArgs {
   int64_t stride;        // logits row stride, elements
   float scale;
   int32_t tokens, experts, top_k, score, renorm;
+  int32_t groups, top_groups, top2;   // groups 1: none
+  int32_t log_lanes;                  // a group's lanes are 2^log_lanes
 };
 
 template <typename T>
@@ -137,20 +141,63 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t at) {
   return bf16_lo(ld_global<uint16_t>(p, (size_t)at * 2));
 }
 
+// Shuts the groups that are not among the token's best: their experts' keys
+// become -inf.  2^log_lanes neighbouring lanes hold a group's experts (lanes
+// past the last group hold none), so a group's two best keys meet in steps of
+// lane exchanges, and its rank is the number of groups that beat it.  The
+// ratings are of the scores in fp64 where two keys are added, since sums of
+// logits would be another order.
+template <typename Key, int L, int R>
+__device__ __forceinline__ void shut_groups(const RouteArgs& a, const float (&x)[R], float top, Key (&key)[R]) {
+  const int lane = threadIdx.x & (L - 1), mine = lane >> a.log_lanes;
+  const double ninf = -(double)__builtin_inff();
+  double first = ninf, second = ninf;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    double k = (double)key[r];
+    if (sizeof(Key) == 4 && a.top2 && x[r] > -__builtin_inff())
+      k = a.score == 0 ? exp((double)x[r] - (double)top) : 1.0 / (1.0 + exp(-(double)x[r]));
+    second = pick_max(second, first < k ? first : k);
+    first = pick_max(first, k);
+  }
+  for (int off = 1; off < 1 << a.log_lanes; off <<= 1) {
+    const double f = __shfl_xor(first, off), s = __shfl_xor(second, off);
+    second = pick_max(pick_max(second, s), first < f ? first : f);
+    first = pick_max(first, f);
+  }
+  const double rating = a.top2 && second > ninf ? first + second : first;
+  int better = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const double other = __shfl(rating, g << a.log_lanes, L);
+    better += other > rating || (other == rating && g < mine) ? 1 : 0;
+  }
+  if (better >= a.top_groups) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) key[r] = -(Key)__builtin_inff();
+  }
+}
+
 // A token's choice by L lanes with R experts each (expert r * L + lane of
-// the group): lane j of the group ends with the j-th expert (-1: none) and
-// its weight.  A step takes the largest key left, and among its equals the
-// lowest expert.
-template <typename T, typename Key, int L, int R>
+// the group of lanes; with groups of experts, a group's experts go round its own
+// lanes): lane j ends with the j-th expert (-1: none) and its weight.  A step
+// takes the largest key left, and among its equals the lowest expert.
+template <typename T, typename Key, int L, int R, bool GROUPS>
 __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_id, float& my_w) {
   constexpr bool kBias = sizeof(Key) == 8;
   const int lane = threadIdx.x & (L - 1);
   const float ninf = -__builtin_inff();
+  // past the experts there are, or past its group's: none
+  const int size = GROUPS ? a.experts / a.groups : 0, part = GROUPS ? lane >> a.log_lanes : 0;
+  const auto expert = [&](int r) {
+    if (!GROUPS) return r * L + lane;
+    const int in = (r << a.log_lanes) + (lane & ((1 << a.log_lanes) - 1));
+    return part < a.groups && in < size ? part * size + in : kRouteMaxE;
+  };
   float x[R];
   Key key[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int e = r * L + lane;
+    const int e = expert(r);
     const float v = load_logit<T>(a.logits, (int64_t)t * a.stride + (e < a.experts ? e : 0));
     x[r] = v == v && e < a.experts ? v : ninf;
   }
@@ -174,7 +221,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_i
     zd = a.score == 0 ? group_total<L>(zd) : 1.0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int e = r * L + lane;
+      const int e = expert(r);
       const double k = key[r] / zd + (double)ld_global<float>(a.bias, (size_t)(e < a.experts ? e : 0) * 4);
       key[r] = x[r] > ninf && k == k ? k : (double)ninf;
     }
@@ -182,6 +229,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_i
 #pragma unroll
     for (int r = 0; r < R; ++r) key[r] = x[r];
   }
+  if constexpr (GROUPS) shut_groups<Key, L, R>(a, x, top, key);
 
   my_id = -1;
   float my_x = ninf;
@@ -194,10 +242,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_i
     if (!__ballot(live)) break;   // no token of the wave has an expert left
     int first = kRouteMaxE;
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) first = key[r] == best ? r * L + lane : first;
+    for (int r = R - 1; r >= 0; --r) first = key[r] == best ? expert(r) : first;
     const int id = group_min<L>(first);
 #pragma unroll
-    for (int r = 0; r < R; ++r) key[r] = r * L + lane == id ? (Key)ninf : key[r];
+    for (int r = 0; r < R; ++r) key[r] = expert(r) == id ? (Key)ninf : key[r];
     if (live && lane == j) {
       my_id = id;
       if constexpr (!kBias) my_x = (float)best;
@@ -210,9 +258,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_i
   }
   float w;
   if (a.score == 0) {
-    // Of the chosen alone, their own largest: under a bias the row's may not
-    // be among them, and terms taken from it could all be zero.
-    if constexpr (kBias) {
+    // Of the chosen alone, their own largest: under a bias, or in a group that
+    // is shut, the row's may not be among them, and terms taken from it could all be zero.
+    if constexpr (kBias || GROUPS) {
       if (a.renorm) top = group_max<L>(my_x);
     }
     w = live ? expf(my_x - top) : 0.0f;
@@ -262,7 +310,7 @@ __device__ __forceinline__ int scan_experts(int* count, int experts, int* wave_s
 
 // The choice of 32 tokens, and their places among them.  ONE: this group is
 // the whole call, so the map is finished here.
-template <typename T, typename Key, int L, int R, bool ONE>
+template <typename T, typename Key, int L, int R, bool GROUPS, bool ONE>
 __global__ __launch_bounds__(kRouteThreads) void k_route_choose(RouteArgs a) {
   __shared__ uint32_t mask[kRouteMaxE];
   __shared__ int16_t chosen_id[kRouteTokens * kRouteMaxK];
@@ -279,7 +327,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_choose(RouteArgs a) {
     if (L == kWave ? i >= nt : i - i % (kWave / L) >= nt) break;   // a wave's lanes stay together
     int id;
     float w;
-    route_token<T, Key, L, R>(a, t0 + min(i, nt - 1), id, w);
+    route_token<T, Key, L, R, GROUPS>(a, t0 + min(i, nt - 1), id, w);
     if (i < nt && lane < a.top_k) {
       const int64_t at = (int64_t)(t0 + i) * a.top_k + lane;
       a.ids[at] = id;
@@ -377,14 +425,14 @@ __global__ void k_route_empty(int32_t* offsets, int experts) {
   if (e <= experts) offsets[e] = 0;
 }
 
-template <typename T, typename Key, int L, int R>
+template <typename T, typename Key, int L, int R, bool GROUPS = false>
 hipError_t route_launch(const RouteArgs& a, hipStream_t stream) {
   const int groups = (a.tokens + kRouteTokens - 1) / kRouteTokens;
   if (groups == 1) {
-    k_route_choose<T, Key, L, R, true><<<1, kRouteThreads, 0, stream>>>(a);
+    k_route_choose<T, Key, L, R, GROUPS, true><<<1, kRouteThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
-  k_route_choose<T, Key, L, R, false><<<groups, kRouteThreads, 0, stream>>>(a);
+  k_route_choose<T, Key, L, R, GROUPS, false><<<groups, kRouteThreads, 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   k_route_place<<<groups, kRouteThreads, 0, stream>>>(a, groups);
@@ -395,7 +443,22 @@ hipError_t route_launch(const RouteArgs& a, hipStream_t stream) {
 // choice of it: four tokens share a wave's instructions, and no value has to
 // cross rows.
 template <typename T, typename Key>
-hipError_t route_by_experts(const RouteArgs& a, hipStream_t stream) {
+hipError_t route_by_experts(RouteArgs a, hipStream_t stream) {
+  if (a.groups > 1) {
+    // Lanes of a group: as many as 16 or 64 lanes have for the next power of
+    // two groups, and enough registers for its experts.
+    int parts = 2;
+    while (parts < a.groups) parts *= 2;
+    const int size = a.experts / a.groups;
+    const auto lanes = [&](int l) {
+      a.log_lanes = 0;
+      while (parts << (a.log_lanes + 1) <= l) ++a.log_lanes;
+      return parts <= l ? (size + (1 << a.log_lanes) - 1) >> a.log_lanes : kRouteMaxE;   // experts of a lane
+    };
+    if (a.top_k <= 16 && lanes(16) <= 16) return route_launch<T, Key, 16, 16, true>(a, stream);
+    if (lanes(64) <= 8) return route_launch<T, Key, 64, 8, true>(a, stream);
+    return route_launch<T, Key, 64, 32, true>(a, stream);   // up to 1024 / groups over 64 / parts >= 32 / groups lanes
+  }
   if (a.top_k <= 16) {
     if (a.experts <= 64) return route_launch<T, Key, 16, 4>(a, stream);
     if (a.experts <= 128) return route_launch<T, Key, 16, 8>(a, stream);
@@ -494,7 +557,8 @@ hipError_t launch_route_experts(const RouteCall& c, hipStream_t stream) {
     return hipGetLastError();
   }
   const RouteArgs a{c.logits, c.bias, c.ids, c.weights, c.slots, c.rows, c.offsets, static_cast<uint8_t*>(c.workspace),
-                    c.stride, c.scale, c.tokens, c.experts, c.top_k, c.score, c.renorm};
+                    c.stride, c.scale, c.tokens, c.experts, c.top_k, c.score, c.renorm, c.groups, c.top_groups,
+                    c.group_top2, 0};
   if (c.f32) return c.bias ? route_by_experts<float, double>(a, stream) : route_by_experts<float, float>(a, stream);
   return c.bias ? route_by_experts<uint16_t, double>(a, stream) : route_by_experts<uint16_t, float>(a, stream);
 }

@@ -21,6 +21,12 @@
  *               a gated SiLU, and the weighted sum of a token's experts
  *   logprobs    lm_head logits -> log probability of given tokens, entropy,
  *               top alternatives
+ * those of a dense layer and of the token that is answered:
+ *
+ *   linear      the product for any m with bias, activation (gated ones
+ *               too) and residual in its epilogue, bf16 or f32 results
+ *   sample      logits and a random number a row -> a token, under
+ *               temperature, top-k, top-p and min-p
  *
  * and a measurement aid: a read-only pass over device memory with the
  * GEMV's loads (fp8w_read_ceiling).
@@ -502,10 +508,16 @@ typedef enum fp8w_score {
   FP8W_SCORE_SIGMOID = 1      /* 1 / (1 + exp(-l))                   */
 } fp8w_score;
 
-/* What the grouped products write. */
+/* What a product ends with (the products grouped by expert: NONE and SWIGLU).
+ * The gated ones take W's rows 0..n/2 as gates g and n/2..n as values u. */
 typedef enum fp8w_act {
   FP8W_ACT_NONE = 0,
-  FP8W_ACT_SWIGLU = 1         /* silu(g) * u of W's two halves of rows */
+  FP8W_ACT_SWIGLU = 1,        /* silu(g) * u                              */
+  FP8W_ACT_SILU = 2,          /* v / (1 + exp(-v))                        */
+  FP8W_ACT_GELU = 3,          /* v * (1 + erf(v / sqrt 2)) / 2            */
+  FP8W_ACT_GELU_TANH = 4,     /* v * (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+  FP8W_ACT_RELU = 5,          /* max(v, 0)                                */
+  FP8W_ACT_GEGLU = 6          /* gelu_tanh(g) * u                         */
 } fp8w_act;
 
 /* Largest number of experts and of choices a token (fp8w_route_experts,
@@ -544,6 +556,34 @@ fp8w_status fp8w_route_experts(const void* logits, fp8w_dtype dtype, int64_t str
                                int renorm, float scale, int32_t* ids, float* weights, int32_t* slots,
                                int32_t* rows, int32_t* offsets, void* workspace,
                                int64_t workspace_bytes, void* stream);
+
+/* How a group of experts is rated: by the best key of its experts, or by the
+ * sum of its two best (of its only one, where it has no second that may be
+ * chosen). */
+typedef enum fp8w_group_score {
+  FP8W_GROUP_MAX = 0,
+  FP8W_GROUP_TOP2 = 1
+} fp8w_group_score;
+
+/* Largest number of groups of experts. */
+#define FP8W_MAX_GROUPS 64
+
+/* fp8w_route_experts for experts in groups: expert e is in group e / (experts
+ * / groups), and a token's experts are chosen from its `top_groups` best
+ * groups alone.  A group's rating takes its experts' keys (a logit without
+ * bias counts by its score under TOP2, in fp64), ties to the lower group; an
+ * expert that is never chosen (-inf or NaN) has no key, and a group of such
+ * experts is never among the best.  Everything else as there, workspace too;
+ * with groups = 1, or top_groups = groups, the same result.  Requires groups
+ * >= 1, experts % groups == 0, groups <= 64, 1 <= top_groups <= groups,
+ * top_k <= top_groups * (experts / groups).
+ * Errors: as fp8w_route_experts (UNSUPPORTED also: group_score). */
+fp8w_status fp8w_route_experts_grouped(const void* logits, fp8w_dtype dtype, int64_t stride, int64_t tokens,
+                                       int64_t experts, int64_t top_k, fp8w_score score, const float* bias,
+                                       int64_t groups, int64_t top_groups, fp8w_group_score group_score,
+                                       int renorm, float scale, int32_t* ids, float* weights, int32_t* slots,
+                                       int32_t* rows, int32_t* offsets, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
 
 /* Products grouped by expert.  For every slot i of expert e, offsets[e] <= i
  * < offsets[e + 1]:
@@ -589,6 +629,40 @@ fp8w_status fp8w_combine_experts(const uint16_t* y, int64_t slot_rows, const flo
                                  const int32_t* slots, int64_t tokens, int64_t top_k, int64_t n,
                                  uint16_t* out, void* stream);
 
+/* -------------------------------------------------------------- linear -- */
+
+/* A dense layer's product with its epilogue, for any m:
+ *   y = act(x . deq(W)^T + bias) + residual
+ * with v[i][j] = sum_k x[i][k] deq[j][k] + bias[j] in fp32, the activation in
+ * fp32, the residual added, and one rounding to y's type at the end.  Gated
+ * activations take v's two halves of columns and give n/2 columns.
+ *   x        : bf16 [m, k], 16-byte aligned, row stride x_stride elements,
+ *              a multiple of 8                                       input
+ *   codes    : u8 [n, k], 16-byte aligned                            input
+ *   scales   : the scale buffer of `format`                          input
+ *   bias     : bf16 or f32 [n], or NULL                              input
+ *   residual : bf16 [m, n_out], row stride residual_stride, or NULL  input
+ *   y        : bf16 or f32 [m, n_out], row stride y_stride           output
+ *   workspace: fp8w_linear_workspace_bytes(...) bytes, 16-byte aligned (0 for
+ *              many shapes: sums of slices of k, where that fills the chip)
+ * n_out = n, or n/2 with SWIGLU and GEGLU.  y may be the residual itself (the
+ * same address and stride, y of bf16), and is then added to in place; any
+ * other overlap is refused.  The space between y's rows is left as it was.
+ * v meets the bound of fp8w_gemv (2^-7 sum |x| |deq| + 1e-6) with room: its
+ * error is fp32 rounding of the sums alone.  An infinity or NaN of x reaches its own row
+ * alone, as the formula has it; gates and values beyond fp32's range pass as
+ * the formula's limit.
+ * Requires 0 <= m <= 2^30 (0: no launch), 1 <= n <= 2^28 (gated: even),
+ * 16 <= k <= 2^28, k % 16 == 0, strides >= the columns and <= 2^31 - 1.
+ * Errors: NULL, SHAPE (also: workspace too small), UNSUPPORTED (format, act,
+ * dtype), ALIGN, OVERLAP, HIP. */
+int64_t fp8w_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, fp8w_format format, fp8w_act act);
+fp8w_status fp8w_linear(const uint16_t* x, int64_t x_stride, int64_t m, const uint8_t* codes, const void* scales,
+                        fp8w_format format, int64_t n, int64_t k, const void* bias, fp8w_dtype bias_dtype,
+                        fp8w_act act, const uint16_t* residual, int64_t residual_stride, void* y,
+                        fp8w_dtype y_dtype, int64_t y_stride, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
 /* ------------------------------------------------------------ logprobs -- */
 
 /* Largest number of alternatives a row. */
@@ -621,6 +695,49 @@ fp8w_status fp8w_logprobs(const void* logits, fp8w_dtype dtype, int64_t stride, 
                           int64_t vocab, const int32_t* targets, int64_t top, float* logprob,
                           float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
                           int64_t workspace_bytes, void* stream);
+
+/* -------------------------------------------------------------- sample -- */
+
+/* A token drawn from each row of logits, under that row's settings, by one
+ * given random number.
+ *   logits      : bf16 or f32 [tokens, vocab], row stride `stride` elements   input
+ *   uniforms    : f32 [tokens], in [0, 1)                                    input
+ *   temperature : f32 [tokens] or NULL (1)                                   input
+ *   top_k       : i32 [tokens] or NULL (all)                                 input
+ *   top_p       : f32 [tokens] or NULL (1)                                   input
+ *   min_p       : f32 [tokens] or NULL (0)                                   input
+ *   ids         : i32 [tokens]  the drawn token                              output
+ *   logprob     : f32 [tokens] or NULL  log of the probability that it was
+ *                 drawn with (over the tokens left, at the temperature)      output
+ *   kept        : i32 [tokens] or NULL  how many tokens were left            output
+ * A row's tokens are put in order, larger logits first and lower tokens first
+ * among equals, with weights w_j = exp((x_j - x_0) / temperature), and the
+ * first n of them are kept:
+ *   top_k   at most top_k of them (0 or less: all)
+ *   top_p   token j while the weights before it are less than top_p times
+ *           the weights of those that top_k leaves (1 or more: all)
+ *   min_p   token j while w_j >= min_p, as (x_j - x_0) / temperature >= ln
+ *           min_p (0 or less: all)
+ * but the first always.  Drawn is the first token whose weight and all before
+ * it add up to more than u times the weights of the kept.  Uniforms outside
+ * [0, 1) give the first or the last kept token, NaN the first; a setting that
+ * is NaN is off.  A temperature of 0 (or less, or NaN) takes the first token
+ * (log probability 0, one kept).  Masked tokens (-inf, NaN) are never drawn nor
+ * counted; where +inf stands, only such tokens have weight.  A row masked
+ * throughout gives token -1, log probability -inf and none kept.
+ * Weights are fixed-point numbers of at least 31 bits below the largest (44
+ * for 2^18 tokens) out of fp64 exponentials, so that the choice does not
+ * depend on the order of sums, and hardly on their rounding.
+ * workspace: fp8w_sample_workspace_bytes(tokens, vocab) bytes, 16-byte
+ * aligned (0 where there are enough rows to fill the chip).  tokens may be 0.
+ * Requires 1 <= vocab <= 2^31 - 64, stride >= vocab.
+ * Errors: NULL, SHAPE (also: workspace too small), UNSUPPORTED (dtype),
+ * ALIGN, OVERLAP, HIP. */
+int64_t fp8w_sample_workspace_bytes(int64_t tokens, int64_t vocab);
+fp8w_status fp8w_sample(const void* logits, fp8w_dtype dtype, int64_t stride, int64_t tokens, int64_t vocab,
+                        const float* uniforms, const float* temperature, const int32_t* top_k,
+                        const float* top_p, const float* min_p, int32_t* ids, float* logprob, int32_t* kept,
+                        void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------- helpers -- */
 
