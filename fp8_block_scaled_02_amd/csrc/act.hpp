@@ -35,11 +35,13 @@ __device__ __forceinline__ float gelu_tanh_times(float g, float u) {
   return sigmoid_times(g, kTwoRoot * __builtin_fmaf(0.044715f * g * g, g, g), u);
 }
 
-// One value's activation, or a gate times its value.  `act` is the call's.
+__device__ __forceinline__ float gelu(float v) { return 0.5f * v * erfcf(-0.70710678118654752f * v); }
+
+// One value's activation (but erf's), or a gate times its value.  `act` is the
+// call's.
 __device__ __forceinline__ float activated(int act, float v) {
   switch (act) {
     case kActSilu: return silu_times(v, 1.0f);
-    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
     case kActGeluTanh: return gelu_tanh_times(v, 1.0f);
     case kActRelu: return v > 0.0f || v != v ? v : 0.0f;   // NaN stays
     default: return v;

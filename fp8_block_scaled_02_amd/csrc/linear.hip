@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "act.hpp"
 #include "device.hpp"
 #include "internal.hpp"
@@ -92,30 +94,568 @@ __global__ __launch_bounds__(256) void k_linear_simple(LinearCall c, int n_group
       if (c.format == kFmtTensor) s = ld_global<float>(c.scales, 0);
       r[q] = __builtin_fmaf(s, acc[q][v], bias_of(c, nq));
     }
-    store_one(c, m0 + i, n, GATED ? gated(c.act, r[0], r[1]) : activated(c.act, r[0]));
+    store_one(c, m0 + i, n, GATED ? gated(c.act, r[0], r[1]) : c.act == kActGelu ? gelu(r[0]) : activated(c.act, r[0]));
   }
+}
+
+// 16 bytes a lane from memory to LDS at `to` + 16 * lane (`to` uniform).
+__device__ __forceinline__ void stage16(const void* from, unsigned char* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+// What x holds past its columns.
+__device__ const uint4 kNoColumns = {0, 0, 0, 0};
+
+// s_waitcnt vmcnt(n) lgkmcnt(0), n < 64, then the workgroup's barrier.  The
+// LDS reads before it have returned, so that what they read may be
+// overwritten after it; and all but the wave's last n loads have landed.
+template <int N>
+__device__ __forceinline__ void land_and_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// These 16 values are computed here, not where the compiler would rather.
+__device__ __forceinline__ void settle(float (&v)[16]) {
+  asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7]),
+               "+v"(v[8]), "+v"(v[9]), "+v"(v[10]), "+v"(v[11]), "+v"(v[12]), "+v"(v[13]), "+v"(v[14]), "+v"(v[15]));
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32_unaligned __attribute__((aligned(1)));
+
+// Where a workgroup works: a tile of x's rows and of outputs, and a slice of
+// k's 128-column blocks.
+struct LinearTile {
+  int m0, count, group, kb0, kb1;
+};
+
+// How the tiles of a call are laid out.  Workgroups go round the 8 XCDs in
+// turn, and each XCD has its own L2: it gets one contiguous eighth of the
+// tiles, the tiles of one group of weight rows next to each other.
+struct LinearGrid {
+  int tiles_m, groups, splits;
+  __device__ __forceinline__ bool at(int height, int m, int nkb, LinearTile& t, int64_t& id) const {
+    const int64_t total = (int64_t)tiles_m * groups * splits, share = (total + 7) / 8;
+    id = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= share || id >= total) return false;
+    const uint32_t pair = (uint32_t)id / (uint32_t)tiles_m;
+    t.m0 = (int)((uint32_t)id - pair * (uint32_t)tiles_m) * height;
+    t.count = min(height, m - t.m0);
+    const uint32_t split = pair / (uint32_t)groups;
+    t.group = (int)(pair - split * (uint32_t)groups);
+    t.kb0 = (int)((int64_t)nkb * split / splits);
+    t.kb1 = (int)((int64_t)nkb * (split + 1) / splits);
+    return true;
+  }
+};
+
+// The tiled kernels' wave: 32 * TW weight rows (gated: half of them of each
+// half of W) against 32 * MT rows of x.
+template <bool GATED, int TW>
+struct WaveRows {
+  static constexpr int kRows = 32 * TW;
+  static constexpr int kCols = GATED ? kRows / 2 : kRows;   // outputs of a row
+  int n0, n_out;
+  __device__ __forceinline__ WaveRows(const LinearCall& c, int group, int wave)
+      : n0((group * 4 + wave) * kCols), n_out(GATED ? c.n / 2 : c.n) {}
+  // Row r of the wave's (r may be uniform or a lane's): output out_row(r),
+  // weight row half(r) further on.
+  __device__ __forceinline__ int out_row(int r) const { return n0 + r % kCols; }
+  __device__ __forceinline__ int half(int r) const { return r >= kCols ? n_out : 0; }
+};
+
+// The end of a tile.  A lane holds x's row 32q + l%32 and, for each v4, weight
+// rows 8 v4 + 4 (l / 32) .. + 3 of each tile of 32: sums are scaled, and the
+// bias added, where they are; 32 rows at a time then go through the wave's own
+// LDS in fp32 (16-byte units swizzled), so that the residual is read and the
+// results written as whole lines.
+template <int FMT, bool GATED, int MT, int TW, typename Acc>
+__device__ __forceinline__ void finish_tile(const LinearCall& c, const LinearTile& at, Acc (&acc)[TW][MT], unsigned char* wl) {
+  using Rows = WaveRows<GATED, TW>;
+  constexpr int kCols = Rows::kCols, kUnits = kCols / 4;   // 16-byte units of a row of results
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int i = lane & 31, hh = lane >> 5;
+  const Rows w(c, at.group, wave);
+  if (FMT == kFmtRow || FMT == kFmtTensor || c.bias) {
+#pragma unroll
+    for (int t = 0; t < TW; ++t)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int r = 32 * t + 8 * (v >> 2) + 4 * hh + (v & 3), n = min(w.out_row(r), w.n_out - 1) + w.half(r);
+        const float s = FMT == kFmtRow ? ld_global<float>(c.scales, (size_t)n * 4) : FMT == kFmtTensor ? ld_global<float>(c.scales, 0) : 1.0f;
+        const float b = bias_of(c, n);
+#pragma unroll
+        for (int q = 0; q < MT; ++q) acc[t][q][v] = __builtin_fmaf(s, acc[t][q][v], b);
+      }
+  }
+  if (!GATED && (c.act == kActSilu || c.act == kActGeluTanh || c.act == kActRelu)) {
+#pragma unroll
+    for (int t = 0; t < TW; ++t)
+#pragma unroll
+      for (int q = 0; q < MT; ++q)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[t][q][v] = activated(c.act, acc[t][q][v]);
+  }
+  const bool vec = c.y_stride % 8 == 0 && reinterpret_cast<uintptr_t>(c.y) % 16 == 0 &&
+                   (!c.residual || (c.residual_stride % 8 == 0 && reinterpret_cast<uintptr_t>(c.residual) % 16 == 0));
+#pragma unroll
+  for (int q = 0; q < MT; ++q) {
+    if (32 * q >= at.count) break;
+#pragma unroll
+    for (int u = 0; u < kCols / 8; ++u) {   // outputs 8u + 4 (l / 32) .. + 3 of the wave's
+      const auto sum = [&](int r, int v) { return acc[r / 32][q][r % 32 / 2 + v]; };   // of row r + 4 (l / 32) + v
+      f32x4 r;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) r[v] = GATED ? gated(c.act, sum(8 * u, v), sum(8 * u + kCols, v)) : sum(8 * u, v);
+      *reinterpret_cast<f32x4*>(wl + i * 4 * kCols + 16 * ((2 * u + hh) ^ (i & (kUnits - 1)))) = r;
+    }
+    asm volatile("" ::: "memory");
+    if (!GATED && c.act == kActGelu) {   // erfc is long: once in the code, not for every sum
+#pragma unroll 1
+      for (int j = 0; j < kCols / 8; ++j) {
+        f32x4* at4 = reinterpret_cast<f32x4*>(wl + 16 * (j * kWave + lane));
+        f32x4 r = *at4;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) r[v] = gelu(r[v]);
+        *at4 = r;
+      }
+      asm volatile("" ::: "memory");
+    }
+#pragma unroll
+    for (int j = 0; j < kCols / 16; ++j) {   // 8 outputs a lane
+      constexpr int kLanes = kCols / 8;      // lanes of a row
+      const int r = j * (kWave / kLanes) + lane / kLanes, u = lane % kLanes, n = w.n0 + 8 * u;
+      const f32x4 v0 = *reinterpret_cast<const f32x4*>(wl + r * 4 * kCols + 16 * ((2 * u) ^ (r & (kUnits - 1))));
+      const f32x4 v1 = *reinterpret_cast<const f32x4*>(wl + r * 4 * kCols + 16 * ((2 * u + 1) ^ (r & (kUnits - 1))));
+      if (32 * q + r >= at.count || n >= w.n_out) continue;
+      const int row = at.m0 + 32 * q + r;
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[e] = v0[e];
+        o[4 + e] = v1[e];
+      }
+      if (!vec || n + 8 > w.n_out) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < w.n_out) store_one(c, row, n + e, o[e]);
+        continue;
+      }
+      if (c.residual) {
+        const uint4 x = ld_global_u4(c.residual, ((size_t)row * c.residual_stride + n) * 2);
+        const uint32_t d[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] += bf16_lo(d[e]);
+          o[2 * e + 1] += bf16_hi(d[e]);
+        }
+      }
+      const size_t to = (size_t)row * c.y_stride + n;
+      if (c.y_f32) {
+        st_global<f32x4>(c.y, to * 4, f32x4{o[0], o[1], o[2], o[3]});
+        st_global<f32x4>(c.y, to * 4 + 16, f32x4{o[4], o[5], o[6], o[7]});
+      } else {
+        st_global<u32x4>(c.y, to * 2, u32x4{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]), bf16_pair(o[4], o[5]), bf16_pair(o[6], o[7])});
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+}
+
+// A slice's sums to the workspace as the lanes hold them, and back: whole
+// lines either way.
+template <int MT, int TW, typename Acc, typename F>
+__device__ __forceinline__ void each_sum(Acc (&acc)[TW][MT], const F& f) {
+#pragma unroll
+  for (int t = 0; t < TW; ++t)
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) f(((t * MT + q) * 4 + a) * 4096, &acc[t][q], 4 * a);
+}
+template <int MT, int TW>
+constexpr int64_t slice_bytes() { return (int64_t)TW * MT * 4 * 4096; }
+
+// The tiled kernel: 128 * TW weight rows against 32 * MT rows of x on the
+// 32x32x16 MFMA, four waves of 32 * TW rows (gated: half of them of each half
+// of W), two (TW = 2) or four workgroups a CU.
+//
+// Everything reaches LDS by loads that write it directly, in whole 128-byte
+// lines.
+//   * Weights: a wave's rows of a 128-column block are its own 4 * TW KB.  At
+//     the start of a block it takes them into registers in the A layout and
+//     asks for the next block at once: a block's time to arrive.
+//   * x: 64 columns of the rows for all four waves, three buffers, asked for
+//     two steps ahead; one barrier a step.
+// The waits name how many younger loads may still be on their way; a wait
+// for everything would put the memory's latency into every step.
+//
+// A lane's 16 bytes of codes are two MFMA steps of 8 columns each, so step
+// (p, s) takes columns 32p + 16(l/32) + 8s of the step, for weights and x
+// alike.  LDS rows are 128 bytes, their 16-byte units XOR-swizzled by row / 2,
+// so that any 16 consecutive rows fall into 16 different bank groups.
+//
+// A block scale multiplies its sums every 64 columns (a full block's sums
+// would need as many registers as the accumulators); MX scales multiply the
+// codes as they become bf16 (exact); row and tensor scales the results.
+template <int FMT, bool GATED, int MT, int TW>
+__device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile& at, float* partial, unsigned char* ws,
+                                           unsigned char* xs0, unsigned char* xs1, unsigned char* xs2) {
+  constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
+  constexpr bool kMx = FMT == kFmtMx;
+  using Rows = WaveRows<GATED, TW>;
+  constexpr int kRows = Rows::kRows;
+  constexpr int kXLoads = MT;          // x loads of a wave and step (1 KB each)
+  constexpr int kWLoads = 4 * TW;      // weight loads of a wave and block
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int i = lane & 31, hh = lane >> 5;
+  const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32, kb1 = at.kb1;
+  const Rows w(c, at.group, wave);
+  const int n_out = w.n_out;
+  unsigned char* wl = ws + wave * kRows * 128;
+
+  // Load j of a wave's weights brings rows 8j + l/8; LDS place l%8 of a row
+  // holds its unit (l%8) ^ (row / 2 % 8), so j odd the unit of j even ^ 4.
+  // Rows past the end are the last one, columns past it the first ones (zeroed
+  // by take_w; x has zeros there, so that no infinity of a column that is read
+  // in their place meets them).  No branches: a load that two paths share is
+  // one the compiler takes to write any of the arrays.  Offsets pass through
+  // an empty asm statement where they are used: the addresses of all loads
+  // would otherwise be kept in registers throughout.
+  const int wu = (lane & 7) ^ (lane >> 4);
+  uint32_t wrow = (uint32_t)(lane >> 3) * (uint32_t)k;
+  int wcol = 16 * wu;
+  const auto load_w = [&](int kb, int j) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(wrow), "+v"(wcol)::"memory");
+    const int c0 = kb * 128 + (wcol ^ (j & 1) * 64);
+    const int row = min(w.out_row(8 * j), n_out - 1);
+    const uint32_t within = (uint32_t)min(n_out - 1 - row, 7) * (uint32_t)k;
+    stage16(c.codes + (size_t)(row + w.half(8 * j)) * k + (min(wrow, within) + (uint32_t)(c0 < k ? c0 : 0)), wl + j * 1024);
+    asm volatile("" ::: "memory");
+  };
+  const auto request_w = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kWLoads; ++j) load_w(kb, j);
+  };
+  // x rows a wave stages: 8 (MT * wave + j) + l/8, the same places (row / 2 % 8
+  // = 4 (row / 8 % 2) + l/16)
+  uint32_t xrow[kXLoads];
+#pragma unroll
+  for (int j = 0; j < kXLoads; ++j) xrow[j] = (uint32_t)(at.m0 + min(8 * (kXLoads * wave + j) + (lane >> 3), at.count - 1));
+  int xcol = 8 * (wu ^ (kXLoads * wave & 1) * 4);
+  const auto load_x = [&](int step, int j, unsigned char* to) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(xcol), "+v"(xrow[j])::"memory");
+    const int c0 = step * 64 + (xcol ^ (j & 1) * 32);
+    // An offset from x either way: chosen between two addresses the MX tile
+    // spilled.
+    const uint64_t x = reinterpret_cast<uint64_t>(c.x), none = reinterpret_cast<uint64_t>(&kNoColumns) - x;
+    const uint64_t from = (uint64_t)xrow[j] * (2 * (uint32_t)c.x_stride) + (uint32_t)(2 * c0);
+    stage16(reinterpret_cast<const void*>(x + (c0 < k ? from : none)), to + (kXLoads * wave + j) * 1024);
+    asm volatile("" ::: "memory");
+  };
+  const auto request_x = [&](int step, unsigned char* to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j) load_x(step, j, to);
+  };
+
+  // scales of the next block: a float a run of rows that lie in one scale
+  // block (a half's, or a 32-row tile; scalar loads), or the four MX exponents
+  // of the lane's row in each tile
+  constexpr int kScales = kMx ? TW : GATED ? 2 : TW;
+  const auto scale_of = [](int t, int v) { return GATED && TW == 1 ? v >> 3 : t; };   // of sum v of tile t
+  const char* sp[kScales];
+  float sc[kScales];
+  uint32_t ex[kScales];
+#pragma unroll
+  for (int t = 0; t < kScales; ++t) {
+    const int first = t * (kRows / kScales);
+    const char* scales = static_cast<const char*>(c.scales);
+    if (kBlock) sp[t] = scales + (size_t)((min(w.out_row(first), n_out - 1) + w.half(first)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
+    if (kMx) sp[t] = scales + (size_t)(min(w.out_row(32 * t + i), n_out - 1) + w.half(32 * t + i)) * ng;
+  }
+  const auto request_s = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < kScales; ++t) {
+      if (FMT == kFmtBlock) sc[t] = reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(sp[t]))[kb];
+      if (FMT == kFmtBlockBf16)
+        sc[t] = bf16_lo(reinterpret_cast<const __attribute__((address_space(4))) uint16_t*>(reinterpret_cast<uintptr_t>(sp[t]))[kb]);
+      // four bytes that end with the row's last, where the block has fewer
+      if (kMx) ex[t] = ld_global<u32_unaligned>(sp[t], (size_t)min(4 * kb, ng - 4));
+    }
+  };
+
+  // the sums: single registers where scales are applied to them, else the
+  // MFMA's own
+  std::conditional_t<kBlock, float[16], f32x16> acc[TW][MT];
+#pragma unroll
+  for (int t = 0; t < TW; ++t)
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[t][q][v] = 0.0f;
+
+  uint4 wr[TW][4];                 // tile, 32-column pair of the block
+  float s[kScales];
+  uint32_t e[TW];
+  const auto take_w = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < TW; ++t)
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        wr[t][p] = *reinterpret_cast<const uint4*>(&wl[(32 * t + i) * 128 + 16 * ((2 * p + hh) ^ (i >> 1 & 7))]);
+    if (kb * 128 + 128 > k) {
+      const int from = kb * 128 + 16 * (lane_fresh() >> 5);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int t = 0; t < TW; ++t)
+          if (from + 32 * p >= k) wr[t][p] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < kScales; ++t) {
+      if (kBlock) s[t] = sc[t];
+      if (kMx) e[t] = ex[t] >> 8 * (4 * kb - min(4 * kb, ng - 4));
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0): the codes are in registers
+    request_s(kb + 1 < kb1 ? kb + 1 : at.kb0);    // the last block asks for one nobody takes
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // 64 columns.  Scaled sums are settled after every 32 rows: left alone the
+  // compiler starts all products first, each with sums of its own, and spills.
+  const auto step = [&](int h, const unsigned char* xb, const auto& load) __attribute__((always_inline)) {
+    const auto read_b = [&](int q, int u) __attribute__((always_inline)) {
+      return *reinterpret_cast<const bf16x8*>(&xb[(32 * q + i) * 128 + 16 * ((4 * (u >> 1) + 2 * hh + (u & 1)) ^ (i >> 1 & 7))]);
+    };
+    bf16x8 a[TW][4], b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) b[u] = read_b(0, u);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int t = 0; t < TW; ++t)
+        a_operands<kMx>(wr[t][2 * h + p], kMx ? mx_scale((uint8_t)(e[t] >> 8 * (2 * h + p))) : 1.0f, a[t][2 * p], a[t][2 * p + 1]);
+#pragma unroll
+    for (int q = 0; q < MT; ++q) {
+      f32x16 part[TW];
+#pragma unroll
+      for (int t = 0; t < TW; ++t) {
+        if constexpr (kBlock) {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) part[t][v] = 0.0f;
+        } else {
+          part[t] = acc[t][q];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int t = 0; t < TW; ++t) part[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[t][u], b[u], part[t], 0, 0, 0);
+        // the operand's register is free: the next 32 rows' into it, three
+        // products ahead of their use
+        if (q + 1 < MT) b[u] = read_b(q + 1, u);
+        if (TW == 2) load(4 * q + u);
+        if (q + 1 < MT || u < 3) __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int t = 0; t < TW; ++t) {
+        if constexpr (kBlock) {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[t][q][v] = __builtin_fmaf(s[scale_of(t, v)], part[t][v], acc[t][q][v]);
+          settle(acc[t][q]);
+        } else {
+          acc[t][q] = part[t];
+        }
+      }
+    }
+  };
+  // A block of 128 columns: x steps 2kb and 2kb + 1 are in x0 and x1, and
+  // the two after them go to x2 and x0.
+  const auto block = [&](int kb, unsigned char* x0, unsigned char* x1, unsigned char* x2) __attribute__((always_inline)) {
+    take_w(kb);
+    const int next = kb + 1 < kb1 ? kb + 1 : at.kb0;
+    const auto first = [&](int n) __attribute__((always_inline)) {   // 4 MT places for 8 + MT loads
+      const int to = (n + 1) * (kWLoads + kXLoads) / (4 * MT);
+#pragma unroll
+      for (int j = n * (kWLoads + kXLoads) / (4 * MT); j < to; ++j) {
+        if (j < kWLoads)
+          load_w(next, j);
+        else
+          load_x(2 * next, j - kWLoads, x2);
+      }
+    };
+    const auto second = [&](int n) __attribute__((always_inline)) {
+      if (n % 4 == 0) load_x(2 * next + 1, n / 4, x0);
+    };
+    if (TW == 1) {
+      request_w(next);
+      request_x(2 * next, x2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    step(0, x0, first);
+    land_and_meet<kWLoads + kXLoads>();           // younger than x1's: weights and x2's
+    if (TW == 1) request_x(2 * next + 1, x0);
+    step(1, x1, second);
+    land_and_meet<kXLoads>();                     // the weights and x2's have landed
+  };
+
+  request_s(at.kb0);
+  request_w(at.kb0);
+  request_x(2 * at.kb0, xs0);
+  request_x(2 * at.kb0 + 1, xs1);
+  land_and_meet<kXLoads>();
+  int kb = at.kb0;
+#pragma unroll 1
+  for (; kb + 2 < kb1; kb += 3) {
+    block(kb, xs0, xs1, xs2);
+    block(kb + 1, xs2, xs0, xs1);
+    block(kb + 2, xs1, xs2, xs0);
+  }
+  if (kb < kb1) block(kb, xs0, xs1, xs2);
+  if (kb + 1 < kb1) block(kb + 1, xs2, xs0, xs1);
+  vm_wait_all();   // nothing may land in LDS that is no longer ours
+
+  if (partial) {
+    each_sum<MT, TW>(acc, [&](int off, auto* sums, int a) {
+      st_global<f32x4>(partial, (size_t)off + threadIdx.x * 16, f32x4{(*sums)[a], (*sums)[a + 1], (*sums)[a + 2], (*sums)[a + 3]});
+    });
+    return;
+  }
+  finish_tile<FMT, GATED, MT, TW>(c, at, acc, wl);
+}
+
+template <int FMT, bool GATED, int MT, int TW>
+__global__ __launch_bounds__(256, TW == 2 ? 2 : 4) void k_linear_tile(LinearCall c, LinearGrid grid) {
+  // separate arrays: the compiler then knows that reads of one need not wait
+  // for what is on its way into another
+  __shared__ __attribute__((aligned(16))) unsigned char ws[4 * 32 * TW * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs0[32 * MT * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs1[32 * MT * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs2[32 * MT * 128];
+  LinearTile at;
+  int64_t id;
+  if (!grid.at(32 * MT, c.m, (c.k + 127) / 128, at, id)) return;
+  float* partial = grid.splits == 1 ? nullptr
+                                    : reinterpret_cast<float*>(static_cast<char*>(c.workspace) + id * slice_bytes<MT, TW>());
+  linear_run<FMT, GATED, MT, TW>(c, at, partial, ws, xs0, xs1, xs2);
+}
+
+// The slices' sums added, in their order, and the tile's end.
+template <int FMT, bool GATED, int MT, int TW>
+__global__ __launch_bounds__(256) void k_linear_join(LinearCall c, LinearGrid grid) {
+  __shared__ __attribute__((aligned(16))) unsigned char ws[4 * 32 * TW * 128];
+  const int splits = grid.splits;
+  grid.splits = 1;
+  LinearTile at;
+  int64_t id;
+  if (!grid.at(32 * MT, c.m, 1, at, id)) return;
+  const int64_t stride = (int64_t)grid.tiles_m * grid.groups * slice_bytes<MT, TW>();
+  float acc[TW][MT][16];
+  each_sum<MT, TW>(acc, [&](int off, auto* sums, int a) {
+    f32x4 v = ld_global<f32x4>(c.workspace, (size_t)(id * slice_bytes<MT, TW>() + off) + threadIdx.x * 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) (*sums)[a + e] = v[e];
+  });
+  for (int p = 1; p < splits; ++p)
+    each_sum<MT, TW>(acc, [&](int off, auto* sums, int a) {
+      f32x4 v = ld_global<f32x4>(c.workspace, (size_t)(p * stride + id * slice_bytes<MT, TW>() + off) + threadIdx.x * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) (*sums)[a + e] += v[e];
+    });
+  finish_tile<FMT, GATED, MT, TW>(c, at, acc, ws + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * 32 * TW * 128);
 }
 
 bool is_gated(int act) { return act == kActSwiglu || act == kActGeglu; }
 
+// The kernel of a call, by its sizes.
+struct LinearPlan {
+  enum Kind { kSimple, kSkinny, kNarrow, kWide } kind;
+  int height, width;   // x's rows and outputs of a tile
+  LinearGrid grid;
+  int64_t slice;       // workspace of one tile and slice
+};
+
+LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, int format, int act) {
+  const bool gate = is_gated(act), block = format == kFmtBlock || format == kFmtBlockBf16;
+  const int outputs = gate ? 1 : 2;   // of two weight rows
+  const int64_t n_out = gate ? n / 2 : n, nkb = (k + 127) / 128;
+  const int64_t split = gate && block ? n_out : 0;   // where the second half's scale blocks start
+  LinearPlan p{LinearPlan::kSimple, 16, 64, {1, 1, 1}, 0};
+  int64_t fill = 1;   // workgroups that fill the chip
+  if (split % 32 == 0 && !(format == kFmtMx && k <= 96)) {
+    if (m <= 32)
+      p = {LinearPlan::kSkinny, 32, 64 * outputs, {1, 1, 1}, slice_bytes<1, 1>()}, fill = 1024;
+    else if (m <= 256)
+      p = {LinearPlan::kNarrow, 64, 64 * outputs, {1, 1, 1}, slice_bytes<2, 1>()}, fill = 1024;
+    else
+      p = {LinearPlan::kWide, 128, 128 * outputs, {1, 1, 1}, slice_bytes<4, 2>()}, fill = 512;
+  }
+  p.grid.tiles_m = (int)((m + p.height - 1) / p.height);
+  p.grid.groups = (int)((n_out + p.width - 1) / p.width);
+  const int64_t tiles = (int64_t)p.grid.tiles_m * p.grid.groups;
+  int64_t splits = fill / tiles;
+  if (splits > nkb / 4) splits = nkb / 4;
+  p.grid.splits = splits < 1 ? 1 : (int)splits;
+  return p;
+}
+
+template <int FMT, bool GATED>
+hipError_t launch_plan(const LinearCall& c, const LinearPlan& p, hipStream_t stream) {
+  const int64_t tiles = (int64_t)p.grid.tiles_m * p.grid.groups;
+  const unsigned blocks = (unsigned)((tiles * p.grid.splits + 7) / 8 * 8), joins = (unsigned)((tiles + 7) / 8 * 8);
+  switch (p.kind) {
+    case LinearPlan::kSkinny: k_linear_tile<FMT, GATED, 1, 1><<<blocks, 256, 0, stream>>>(c, p.grid); break;
+    case LinearPlan::kNarrow: k_linear_tile<FMT, GATED, 2, 1><<<blocks, 256, 0, stream>>>(c, p.grid); break;
+    default: k_linear_tile<FMT, GATED, 4, 2><<<blocks, 256, 0, stream>>>(c, p.grid); break;
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.grid.splits == 1) return e;
+  switch (p.kind) {
+    case LinearPlan::kSkinny: k_linear_join<FMT, GATED, 1, 1><<<joins, 256, 0, stream>>>(c, p.grid); break;
+    case LinearPlan::kNarrow: k_linear_join<FMT, GATED, 2, 1><<<joins, 256, 0, stream>>>(c, p.grid); break;
+    default: k_linear_join<FMT, GATED, 4, 2><<<joins, 256, 0, stream>>>(c, p.grid); break;
+  }
+  return hipGetLastError();
+}
+
+template <int FMT>
+hipError_t launch_gate(const LinearCall& c, const LinearPlan& p, hipStream_t stream) {
+  return is_gated(c.act) ? launch_plan<FMT, true>(c, p, stream) : launch_plan<FMT, false>(c, p, stream);
+}
+
 }  // namespace
 
-int64_t linear_workspace_bytes(int64_t, int64_t, int64_t, int, int) { return 0; }
+int64_t linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int format, int act) {
+  const LinearPlan p = linear_plan(m, n, k, format, act);
+  return p.grid.splits == 1 ? 0 : (int64_t)p.grid.tiles_m * p.grid.groups * p.grid.splits * p.slice;
+}
 
-int64_t linear_blocks(int64_t m, int64_t n, int64_t, int, int act) {
-  const int64_t n_out = is_gated(act) ? n / 2 : n;
-  return (m + 15) / 16 * ((n_out + 63) / 64);
+int64_t linear_blocks(int64_t m, int64_t n, int64_t k, int format, int act) {
+  const LinearPlan p = linear_plan(m, n, k, format, act);
+  return ((int64_t)p.grid.tiles_m * p.grid.groups * p.grid.splits + 7) / 8 * 8;
 }
 
 hipError_t launch_linear(const LinearCall& c, hipStream_t stream) {
-  const bool gated = is_gated(c.act);
-  const int groups = ((gated ? c.n / 2 : c.n) + 63) / 64;
-  const unsigned blocks = (unsigned)linear_blocks(c.m, c.n, c.k, c.format, c.act);
-  if (gated)
-    k_linear_simple<true><<<blocks, 256, 0, stream>>>(c, groups);
-  else
-    k_linear_simple<false><<<blocks, 256, 0, stream>>>(c, groups);
-  return hipGetLastError();
+  const LinearPlan p = linear_plan(c.m, c.n, c.k, c.format, c.act);
+  if (p.kind == LinearPlan::kSimple) {
+    const unsigned blocks = (unsigned)((int64_t)p.grid.tiles_m * p.grid.groups);
+    if (is_gated(c.act))
+      k_linear_simple<true><<<blocks, 256, 0, stream>>>(c, p.grid.groups);
+    else
+      k_linear_simple<false><<<blocks, 256, 0, stream>>>(c, p.grid.groups);
+    return hipGetLastError();
+  }
+  switch (c.format) {
+    case kFmtBlock: return launch_gate<kFmtBlock>(c, p, stream);
+    case kFmtMx: return launch_gate<kFmtMx>(c, p, stream);
+    case kFmtBlockBf16: return launch_gate<kFmtBlockBf16>(c, p, stream);
+    case kFmtRow: return launch_gate<kFmtRow>(c, p, stream);
+    default: return launch_gate<kFmtTensor>(c, p, stream);
+  }
 }
 
 }  // namespace fp8w
