@@ -98,6 +98,83 @@ __global__ __launch_bounds__(256) void k_linear_simple(LinearCall c, int n_group
   }
 }
 
+// Four neighbouring outputs of a row: what they take besides their sums
+// (gated: g's and u's), asked for ahead of its use and kept as it comes (a
+// conversion next to its load would wait for it), and the end.
+template <int FMT, bool GATED>
+struct FourOutputs {
+  static constexpr int kHalves = GATED ? 2 : 1;
+  f32x4 scale[kHalves];
+  uint32_t bias[kHalves][4], residual[4];
+  int row, n, n_out;
+
+  __device__ __forceinline__ FourOutputs(const LinearCall& c, int r, int at) : row(r), n(at), n_out(GATED ? c.n / 2 : c.n) {
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int w = min(n + j, n_out - 1) + h * n_out;
+        scale[h][j] = FMT == kFmtRow ? ld_global<float>(c.scales, (size_t)w * 4) : FMT == kFmtTensor ? ld_global<float>(c.scales, 0) : 1.0f;
+        bias[h][j] = 0;
+      }
+    if (c.bias) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int w = min(n + j, n_out - 1) + h * n_out;
+          bias[h][j] = c.bias_f32 ? ld_global<uint32_t>(c.bias, (size_t)w * 4) : ld_global<uint16_t>(c.bias, (size_t)w * 2);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) residual[j] = 0;
+    if (c.residual) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        residual[j] = ld_global<uint16_t>(c.residual, ((size_t)row * c.residual_stride + min(n + j, n_out - 1)) * 2);
+    }
+  }
+  __device__ __forceinline__ float biased(const LinearCall& c, int h, int j, float sum) const {
+    return __builtin_fmaf(scale[h][j], sum, __uint_as_float(c.bias_f32 ? bias[h][j] : bias[h][j] << 16));
+  }
+  __device__ __forceinline__ void finish(const LinearCall& c, f32x4 v, f32x4 u) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = biased(c, 0, j, v[j]);
+      if constexpr (GATED) v[j] = gated(c.act, v[j], biased(c, 1, j, u[j]));
+    }
+    if constexpr (!GATED) {
+      if (c.act == kActGelu) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = gelu(v[j]);
+      } else if (c.act != kActNone) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = activated(c.act, v[j]);
+      }
+    }
+    if (c.residual) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += bf16_lo(residual[j]);
+    }
+    const size_t to = (size_t)row * c.y_stride + n;
+    if (n + 4 <= n_out && c.y_stride % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % 16 == 0) {
+      if (c.y_f32)
+        st_global<f32x4>(c.y, to * 4, v);
+      else
+        st_global<u32x2>(c.y, to * 2, u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + j >= n_out) break;
+      if (c.y_f32)
+        st_global<float>(c.y, (to + j) * 4, v[j]);
+      else
+        st_global<uint16_t>(c.y, (to + j) * 2, (uint16_t)f32_to_bf16_rne(v[j]));
+    }
+  }
+};
+
 // 16 bytes a lane from memory to LDS at `to` + 16 * lane (`to` uniform).
 __device__ __forceinline__ void stage16(const void* from, unsigned char* to) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
@@ -569,11 +646,221 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearCall c, LinearGrid gr
   finish_tile<FMT, GATED, MT, TW>(c, at, acc, ws + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * 32 * TW * 128);
 }
 
+// The streaming kernel, for few rows of x: 16 * NT weight rows (gated: half of
+// them of each half of W) against 16 * MT rows of x, bound by the weights' way
+// from HBM.
+//
+// The NW waves share k: wave w takes the 128-column blocks w, w + NW, ...
+// (each workgroup from another one on), so that a workgroup reads NW * 128
+// bytes of each row at about the same time.  A wave asks for its weights (2 KB
+// a 16-row tile, in whole lines) and its operands of x D blocks ahead, into
+// registers; weights pass through LDS of the wave's own into the A layout.
+// Nothing is shared between waves until their sums meet in LDS at the end.
+// There is no branch between the loads, whose number the compiler must know
+// to wait for one block alone: blocks past a wave's last one are zeros.
+// (Weights straight to LDS: the compiler then waits for every load before it
+// uses one of x's.)
+template <int FMT, bool GATED, int NT, int MT, int NW, int D>
+__global__ __launch_bounds__(NW * kWave) void k_linear_stream(LinearCall c) {
+  constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
+  constexpr bool kMx = FMT == kFmtMx;
+  constexpr int kOut = GATED ? NT / 2 : NT;        // 16-row tiles of outputs
+  __shared__ __attribute__((aligned(16))) unsigned char ws[NW * NT * 2048];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int i = lane & 15, g = lane >> 4;
+  const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
+  const int n_out = GATED ? c.n / 2 : c.n;
+  const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32;
+  int kb0 = 0, blocks = nkb;
+  if (splits > 1) {   // nkb <= 2^21, splits <= 64
+    kb0 = nkb * split / splits;
+    blocks = nkb * (split + 1) / splits - kb0;
+  }
+  // where the workgroup starts: not all at the same columns
+  const int turn = (int)((uint32_t)tile * NW & ((1u << (31 - __builtin_clz((uint32_t)blocks))) - 1));
+  const int n0 = tile * 16 * kOut;
+  const auto out_row = [&](int t) { return n0 + 16 * (t % kOut); };
+  const auto half = [&](int t) { return t >= kOut ? n_out : 0; };
+  unsigned char* const wl = ws + wave * NT * 2048;
+  const uint64_t zeros = reinterpret_cast<uint64_t>(&kNoColumns);
+
+  // Load j of a block brings rows 8j + l/8 (tile j / 2), unit l%8, which goes
+  // to the row's LDS place (l%8) ^ (row / 2 % 8).  Rows past the end are the
+  // last one; past k weights and x are zeros.
+  uint64_t wp[2 * NT];
+#pragma unroll
+  for (int j = 0; j < 2 * NT; ++j)
+    wp[j] = reinterpret_cast<uint64_t>(c.codes) +
+            (uint64_t)(min(out_row(j >> 1) + 8 * (j & 1) + (lane >> 3), n_out - 1) + half(j >> 1)) * (uint32_t)k;
+  const int place = (lane & 7) ^ (lane >> 4);   // j odd: ^ 4
+  uint64_t xp[MT];
+#pragma unroll
+  for (int q = 0; q < MT; ++q) xp[q] = reinterpret_cast<uint64_t>(c.x) + (uint64_t)min(16 * q + i, c.m - 1) * (2 * (uint32_t)c.x_stride);
+  // A tile's 16 rows lie in one scale block, or in two from row `border` on
+  // (halves that start anywhere).
+  const char* sp[NT];
+  int border[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int first = min(out_row(t), n_out - 1) + half(t);
+    border[t] = 128 - first % 128;
+    if (kBlock) sp[t] = static_cast<const char*>(c.scales) + (size_t)(first / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
+    if (kMx) sp[t] = static_cast<const char*>(c.scales) + (size_t)(min(out_row(t) + i, n_out - 1) + half(t)) * ng;
+  }
+  const bool two = kBlock && GATED && n_out % 16 != 0;
+  const int last_block = (c.n - 1) / 128;
+
+  struct Slot {
+    uint4 w[2 * NT], x[MT][4];
+    float s[NT][2];
+    uint32_t ex[NT];
+  };
+  const auto block_at = [&](int p) {
+    const int b = p < blocks ? p + turn : 0;
+    return kb0 + (b < blocks ? b : b - blocks);
+  };
+  const auto request = [&](int p, Slot& slot) __attribute__((always_inline)) {
+    const int kb = block_at(p), from = p < blocks ? kb * 128 : 1 << 29;   // past every column
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) {
+      const int col = from + 16 * (lane & 7);
+      slot.w[j] = ld_stream_u4(reinterpret_cast<const void*>(col < k ? wp[j] + (uint32_t)col : zeros), 0);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (kBlock) {
+        const auto scale = [&](int down) {
+          const char* p = sp[t] + (size_t)(down * nkb + kb) * (FMT == kFmtBlock ? 4 : 2);
+          return FMT == kFmtBlock ? *reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(p))
+                                  : bf16_lo(*reinterpret_cast<const __attribute__((address_space(4))) uint16_t*>(reinterpret_cast<uintptr_t>(p)));
+        };
+        slot.s[t][0] = scale(0);
+        if (GATED) slot.s[t][1] = scale(two && (min(out_row(t), n_out - 1) + half(t)) / 128 < last_block ? 1 : 0);
+      }
+      // four bytes that end with the row's last, where the block has fewer
+      if (kMx) slot.ex[t] = ld_global<u32_unaligned>(sp[t], (size_t)min(4 * kb, ng - 4));
+    }
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int col = from + 64 * (u >> 1) + 16 * g + 8 * (u & 1);
+        slot.x[q][u] = ld_global_u4(reinterpret_cast<const void*>(col < k ? xp[q] + (uint32_t)(2 * col) : zeros), 0);
+      }
+    asm volatile("" ::: "memory");
+  };
+
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < MT; ++q) acc[t][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const auto consume = [&](int p, Slot& slot) __attribute__((always_inline)) {
+    const int kb = block_at(p);
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j)
+      *reinterpret_cast<uint4*>(wl + j * 1024 + (lane >> 3) * 128 + 16 * (place ^ (j & 1) * 4)) = slot.w[j];
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      f32x4 part[MT] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 w = *reinterpret_cast<const uint4*>(wl + (16 * t + i) * 128 + 16 * ((4 * h + g) ^ (i >> 1)));
+        bf16x8 a0, a1;
+        a_operands<kMx>(w, kMx ? mx_scale((uint8_t)(slot.ex[t] >> 8 * (4 * kb - min(4 * kb, ng - 4)) >> 8 * (2 * h + (g >> 1)))) : 1.0f, a0, a1);
+#pragma unroll
+        for (int q = 0; q < MT; ++q) {
+          part[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, slot.x[q][2 * h]), part[q], 0, 0, 0);
+          part[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, slot.x[q][2 * h + 1]), part[q], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float s = 1.0f;
+        if (kBlock) s = GATED && 4 * g + v >= border[t] ? slot.s[t][1] : slot.s[t][0];
+#pragma unroll
+        for (int q = 0; q < MT; ++q) acc[t][q][v] = __builtin_fmaf(s, part[q][v], acc[t][q][v]);
+      }
+    }
+    asm volatile("" ::: "memory");
+  };
+  Slot slot[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) request(wave + d * NW, slot[d]);
+  // what a thread's four outputs take besides their sums
+  const int mt = MT == 1 ? 0 : threadIdx.x / kWave % MT, ml = threadIdx.x % kWave, mo = threadIdx.x / (MT * kWave);
+  static_assert(NT * MT <= NW, "a thread finishes no more than four outputs");
+  const bool mine = mo < (splits > 1 ? NT : kOut) && 16 * mt + (ml & 15) < c.m && out_row(mo) + 4 * (ml >> 4) < n_out;
+  FourOutputs<FMT, GATED> four(c, min(16 * mt + (ml & 15), c.m - 1), min(out_row(mo) + 4 * (ml >> 4), n_out - 1));
+#pragma unroll 1
+  for (int p = wave; p - wave < blocks; p += D * NW) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      consume(p + d * NW, slot[d]);
+      request(p + (D + d) * NW, slot[d]);
+    }
+  }
+
+  // the waves' sums meet, each in its own part of LDS
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < MT; ++q) *reinterpret_cast<f32x4*>(wl + ((t * MT + q) * kWave + lane) * 16) = acc[t][q];
+  __syncthreads();
+  if (!mine) return;
+  const auto total = [&](int t) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(ws + ((t * MT + mt) * kWave + ml) * 16);
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      const f32x4 o = *reinterpret_cast<const f32x4*>(ws + w * NT * 2048 + ((t * MT + mt) * kWave + ml) * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += o[j];
+    }
+    return v;
+  };
+  const f32x4 v = total(mo);
+  if (splits > 1) {   // rows of n sums (padded to four) for each slice
+    const size_t stride = (size_t)(GATED ? 2 : 1) * ((n_out + 3) & ~3);
+    st_global<f32x4>(c.workspace, (((size_t)split * c.m + four.row) * stride + (mo >= kOut ? stride / 2 : 0) + four.n) * 4, v);
+  } else if constexpr (GATED) {
+    four.finish(c, v, total(mo + kOut));
+  } else {
+    four.finish(c, v, v);
+  }
+}
+
+// The slices' sums of the streaming kernel added, in their order: a thread
+// takes four outputs of a row.
+template <int FMT, bool GATED>
+__global__ __launch_bounds__(256) void k_linear_rows(LinearCall c, int splits) {
+  const int n_out = GATED ? c.n / 2 : c.n, quads = (n_out + 3) / 4;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int row = (int)(e / quads), n = 4 * (int)(e - (int64_t)row * quads);
+  if (row >= c.m) return;
+  const size_t stride = (size_t)(GATED ? 2 : 1) * 4 * quads;
+  f32x4 v[2] = {};
+  for (int p = 0; p < splits; ++p)
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+      const f32x4 o = ld_global<f32x4>(c.workspace, (((size_t)p * c.m + row) * stride + h * (stride / 2) + n) * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[h][j] += o[j];
+    }
+  FourOutputs<FMT, GATED>(c, row, n).finish(c, v[0], v[1]);
+}
+
 bool is_gated(int act) { return act == kActSwiglu || act == kActGeglu; }
+
+constexpr int kStreamRows = 16;   // x's rows that the streaming kernel takes
+constexpr int kStreamTiles = 2, kStreamWaves = 4;
+constexpr int kMaxSplits = 64;
+
 
 // The kernel of a call, by its sizes.
 struct LinearPlan {
-  enum Kind { kSimple, kSkinny, kNarrow, kWide } kind;
+  enum Kind { kSimple, kStream, kSkinny, kNarrow, kWide } kind;
   int height, width;   // x's rows and outputs of a tile
   LinearGrid grid;
   int64_t slice;       // workspace of one tile and slice
@@ -585,8 +872,13 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, int format, int act) {
   const int64_t n_out = gate ? n / 2 : n, nkb = (k + 127) / 128;
   const int64_t split = gate && block ? n_out : 0;   // where the second half's scale blocks start
   LinearPlan p{LinearPlan::kSimple, 16, 64, {1, 1, 1}, 0};
-  int64_t fill = 1;   // workgroups that fill the chip
-  if (split % 32 == 0 && !(format == kFmtMx && k <= 96)) {
+  int64_t fill = 1;    // workgroups that fill the chip
+  int64_t least = 4;   // blocks of a slice
+  if (format == kFmtMx && k <= 96) {
+    // rows of fewer than four exponents, which the others read at a time
+  } else if (m <= kStreamRows) {
+    p = {LinearPlan::kStream, kStreamRows, 8 * kStreamTiles * outputs, {1, 1, 1}, 0}, fill = 512, least = 16;
+  } else if (split % 32 == 0) {
     if (m <= 32)
       p = {LinearPlan::kSkinny, 32, 64 * outputs, {1, 1, 1}, slice_bytes<1, 1>()}, fill = 1024;
     else if (m <= 256)
@@ -598,13 +890,26 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, int format, int act) {
   p.grid.groups = (int)((n_out + p.width - 1) / p.width);
   const int64_t tiles = (int64_t)p.grid.tiles_m * p.grid.groups;
   int64_t splits = fill / tiles;
-  if (splits > nkb / 4) splits = nkb / 4;
+  if (splits > nkb / least) splits = nkb / least;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   p.grid.splits = splits < 1 ? 1 : (int)splits;
   return p;
 }
 
 template <int FMT, bool GATED>
+hipError_t launch_stream(const LinearCall& c, const LinearPlan& p, hipStream_t stream) {
+  k_linear_stream<FMT, GATED, kStreamTiles, 1, kStreamWaves, 2>
+      <<<dim3(p.grid.groups, p.grid.splits), kStreamWaves * kWave, 0, stream>>>(c);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.grid.splits == 1) return e;
+  const int64_t quads = (int64_t)c.m * (((GATED ? c.n / 2 : c.n) + 3) / 4);
+  k_linear_rows<FMT, GATED><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(c, p.grid.splits);
+  return hipGetLastError();
+}
+
+template <int FMT, bool GATED>
 hipError_t launch_plan(const LinearCall& c, const LinearPlan& p, hipStream_t stream) {
+  if (p.kind == LinearPlan::kStream) return launch_stream<FMT, GATED>(c, p, stream);
   const int64_t tiles = (int64_t)p.grid.tiles_m * p.grid.groups;
   const unsigned blocks = (unsigned)((tiles * p.grid.splits + 7) / 8 * 8), joins = (unsigned)((tiles + 7) / 8 * 8);
   switch (p.kind) {
@@ -631,7 +936,10 @@ hipError_t launch_gate(const LinearCall& c, const LinearPlan& p, hipStream_t str
 
 int64_t linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int format, int act) {
   const LinearPlan p = linear_plan(m, n, k, format, act);
-  return p.grid.splits == 1 ? 0 : (int64_t)p.grid.tiles_m * p.grid.groups * p.grid.splits * p.slice;
+  if (p.grid.splits == 1) return 0;
+  if (p.kind == LinearPlan::kStream)   // rows of sums, padded to four
+    return m * p.grid.splits * 4 * (is_gated(act) ? 2 * ((n / 2 + 3) & ~(int64_t)3) : (n + 3) & ~(int64_t)3);
+  return (int64_t)p.grid.tiles_m * p.grid.groups * p.grid.splits * p.slice;
 }
 
 int64_t linear_blocks(int64_t m, int64_t n, int64_t k, int format, int act) {
