@@ -877,7 +877,7 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, int format, int act) {
   if (format == kFmtMx && k <= 96) {
     // rows of fewer than four exponents, which the others read at a time
   } else if (m <= kStreamRows) {
-    p = {LinearPlan::kStream, kStreamRows, 8 * kStreamTiles * outputs, {1, 1, 1}, 0}, fill = 512, least = 16;
+    p = {LinearPlan::kStream, kStreamRows, 8 * kStreamTiles * outputs, {1, 1, 1}, 0}, fill = 256, least = 32;
   } else if (split % 32 == 0) {
     if (m <= 32)
       p = {LinearPlan::kSkinny, 32, 64 * outputs, {1, 1, 1}, slice_bytes<1, 1>()}, fill = 1024;

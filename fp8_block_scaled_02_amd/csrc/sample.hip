@@ -17,12 +17,16 @@
 // 2^-45 of a weight's rounding alone.  fp32 would turn over one of some
 // thousand choices among 10^5 tokens.  (fp64 multiply-adds run at the rate of fp32's.)
 //
-// A workgroup takes a row in passes over it (out of L2 from the second on):
-// its largest and smallest logit; a histogram of the distance from the
-// largest, counts and weights; and the tokens of the bins that matter, into
-// LDS, where they are sorted.  Bins that hold more than that has room for are
-// divided again by the values' bits, down to a single value, whose tokens
-// differ by their place alone.
+// A row is taken in passes: its largest and smallest logit; a histogram of the
+// distance from the largest, counts and weights; and the tokens of the bins
+// that matter, into LDS, where they are sorted.  Bins that hold more than that
+// has room for are divided again by the values' bits, down to a single value,
+// whose tokens differ by their place alone.
+//
+// With rows enough one workgroup does all of it, and keeps a row of up to 64
+// KB of its registers' 128 there from pass to pass (longer ones come out of
+// the caches again).  With fewer the first two passes are launches of their
+// own over pieces of rows, and a third workgroup adds the pieces' histograms.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -36,6 +40,7 @@ constexpr int kSmThreads = 1024;
 constexpr int kSmWaves = kSmThreads / kWave;
 constexpr int kSmBins = kSmThreads;   // a thread a bin
 constexpr int kSmCap = 2048;          // tokens of a sorted list
+constexpr int kSmSmall = 256;         // of one that is ranked by counting, four threads a token
 constexpr uint32_t kFirstLive = 0x00800000u;   // the ordered bits of the lowest value; -inf is one below
 
 // Value bits whose unsigned order is the values' order (-0 equal to +0).
@@ -59,6 +64,11 @@ struct SampleArgs {
   int32_t* kept;
   int64_t stride;
   int32_t tokens, vocab, bits;   // bits: S
+  int32_t segs, per;             // pieces of a row, and places of a piece
+  // of the pieces, where there is more than one
+  float2* ranges;                // [tokens][segs]: largest and smallest logit
+  uint64_t* masses;              // [tokens][segs][bins]
+  uint32_t* counts;
 };
 
 // What turns a row's logits into weights and bins.
@@ -96,53 +106,141 @@ struct RowScale {
   }
 };
 
-// Every token of the row once: f(logit, token).
-template <typename T, typename F>
-__device__ __forceinline__ void walk(const SampleArgs& a, int t, const F& f) {
-  constexpr int kVec = 16 / sizeof(T);
+// A row's logits, or those of one piece of it, as the workgroup's threads read
+// them: 16 bytes at a time, KEEP of them a thread loaded once and kept, or (0)
+// all of them at each pass.
+//
+// A pass's code runs but once or a few times a wave, so its time is that of
+// fetching it: what is done for each value is written out for two values of a
+// load, with the registers moved on under it, not for each of eight (32 copies
+// of the exponential, and a place of the order looked for in five copies,
+// took 50 us where the row had 5000 tokens).
+template <typename T, int KEEP>
+struct Logits {
+  static constexpr int kVec = 16 / sizeof(T);
+  static constexpr int kBatch = KEEP ? KEEP : 4;   // loads that leave at once
   // Places are counted from the 16-byte boundary at or below the row's start;
   // only 16 bytes that lie in the row are loaded whole.
-  const char* row = static_cast<const char*>(a.logits) + (size_t)t * a.stride * sizeof(T);
-  const int skew = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-  const char* base = row - skew * sizeof(T);
-  const int64_t end = (int64_t)a.vocab + skew;
-  const int64_t v0 = skew ? 1 : 0, v1 = end / kVec;
-  const int tid = threadIdx.x;
-  const auto value = [&](int64_t at) {
-    float x;
-    if constexpr (sizeof(T) == 4)
-      x = ld_global<float>(base, (size_t)at * 4);
-    else
-      x = bf16_lo(ld_global<uint16_t>(base, (size_t)at * 2));
-    f(x, (int)(at - skew));
-  };
-#pragma unroll 4
-  for (int64_t v = v0 + tid; v < v1; v += kSmThreads) {
-    const uint4 r = ld_global_u4(base, (size_t)v * 16);
+  const char* base;
+  int skew;
+  int64_t v0, v1, end, tail;   // whole 16 bytes, and the values behind them
+  uint4 kept[KEEP ? KEEP : 1];
+
+  __device__ __forceinline__ Logits(const SampleArgs& a, int t, int seg) {
+    const char* row = static_cast<const char*>(a.logits) + (size_t)t * a.stride * sizeof(T);
+    skew = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    base = row - skew * sizeof(T);
+    end = (int64_t)a.vocab + skew;
+    v0 = skew ? 1 : 0;
+    v1 = end / kVec;
+    tail = (v1 > v0 ? v1 : v0) * kVec;
+    if (a.segs > 1 && seg >= 0) {   // a piece: whole units of 16 bytes
+      const int64_t lo = (int64_t)seg * (a.per / kVec), hi = lo + a.per / kVec;
+      if (seg + 1 < a.segs) {
+        v1 = hi < v1 ? hi : v1;
+        end = 0;   // its end is not the row's
+      }
+      if (seg > 0) {
+        v0 = lo > v0 ? lo : v0;
+        skew |= 0x40000000;   // nor its start
+      }
+    }
+    if constexpr (KEEP > 0) {
+#pragma unroll
+      for (int i = 0; i < KEEP; ++i) kept[i] = load(v0 + threadIdx.x + i * kSmThreads);
+    }
+  }
+  // Nothing to see in what is not there: NaN.
+  __device__ __forceinline__ uint4 load(int64_t v) const {
+    constexpr uint32_t kNan = 0xFFFFFFFFu;
+    return v < v1 ? ld_global_u4(base, (size_t)v * 16) : make_uint4(kNan, kNan, kNan, kNan);
+  }
+  __device__ __forceinline__ float value(int64_t at) const {
+    if constexpr (sizeof(T) == 4) return ld_global<float>(base, (size_t)at * 4);
+    return bf16_lo(ld_global<uint16_t>(base, (size_t)at * 2));
+  }
+  // The row's two ends: f(logit, token) of what its whole 16 bytes leave.
+  template <typename F>
+  __device__ __forceinline__ void ends(const F& f) const {
+    const int tid = threadIdx.x;
+    if (tid >= 2 * kVec) return;
+    const int64_t at = tid < kVec ? tid : tail + tid - kVec;
+    const bool there = tid < kVec ? skew > 0 && skew < kVec && tid >= skew && (end == 0 || tid < end) : at < end;
+    if (there) f(value(at), (int)at - (skew & 0xFF));
+  }
+  // The kVec values of 16 bytes in one expression each.
+  template <typename F>
+  static __device__ __forceinline__ void values(const uint4& r, const F& f) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    const int at = (int)(v * kVec - skew);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (sizeof(T) == 4) {
-        f(__uint_as_float(w[i]), at + i);
+        f(__uint_as_float(w[i]));
       } else {
-        f(bf16_lo(w[i]), at + 2 * i);
-        f(bf16_hi(w[i]), at + 2 * i + 1);
+        f(bf16_lo(w[i]));
+        f(bf16_hi(w[i]));
       }
     }
   }
-  if (tid < kVec) {   // the row's two ends
-    if (v0 == 1 && tid >= skew && tid < end) value(tid);
-    const int64_t at = (v1 > v0 ? v1 : v0) * kVec + tid;
-    if (at < end) value(at);
+  // 16 bytes at a time, a few at once: g(16 bytes, token of their first).
+  template <typename G>
+  __device__ __forceinline__ void loads(const G& g) const {
+    const int tid = threadIdx.x;
+#pragma unroll 1
+    for (int64_t v = v0 + tid; v < v1; v += kBatch * kSmThreads) {
+      uint4 r[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) r[i] = KEEP ? kept[i] : load(v + i * kSmThreads);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) g(r[i], (int)((v + i * kSmThreads) * kVec) - (skew & 0xFF));
+    }
   }
-}
+  // Each of 16 bytes' values, f(logit, token), two copies of f.
+  template <typename F>
+  static __device__ __forceinline__ void one_by_one(uint4 r, int id, const F& f) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f(__uint_as_float(r.x), id + i);
+      } else {
+        f(bf16_lo(r.x), id + 2 * i);
+        f(bf16_hi(r.x), id + 2 * i + 1);
+      }
+      r.x = r.y;
+      r.y = r.z;
+      r.z = r.w;
+    }
+  }
+  // Every token once, for what takes long: f(logit, token).
+  template <typename F>
+  __device__ __forceinline__ void walk(const F& f) const {
+    uint4 r[kBatch];
+    int64_t v = v0 + threadIdx.x;
+    const auto fetch = [&](int64_t from) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) r[i] = KEEP ? kept[i] : load(from + i * kSmThreads);
+    };
+    fetch(v);
+#pragma unroll 1
+    for (; v < v1; v += kBatch * kSmThreads) {
+#pragma unroll 1
+      for (int i = 0; i < kBatch; ++i) {
+        one_by_one(r[0], (int)((v + i * kSmThreads) * kVec) - (skew & 0xFF), f);
+#pragma unroll
+        for (int j = 0; j + 1 < kBatch; ++j) r[j] = r[j + 1];
+      }
+      if constexpr (KEEP == 0) fetch(v + kBatch * kSmThreads);
+    }
+    ends(f);
+  }
+};
 
 struct Shared {
   uint64_t list[kSmCap];        // ordered bits, then the token's complement
   uint64_t list_mass[kSmCap];   // weights of the list up to and with each
   uint64_t mass[2][kSmBins];    // of the whole row's bins, of one bin's parts
   uint32_t count[2][kSmBins];
+  int rank[4][kSmSmall];
   uint64_t wave_mass[kSmWaves];
   uint32_t wave_count[kSmWaves];
   float wave_max[kSmWaves], wave_min[kSmWaves];
@@ -151,24 +249,49 @@ struct Shared {
   uint32_t found, found_count;
 };
 
+// A value from the lane n places below in its row of 16 (0 from none).
+template <int N>
+__device__ __forceinline__ uint32_t lanes_below(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x110 + N, 0xF, 0xF, false);
+}
+template <int N>
+__device__ __forceinline__ uint64_t lanes_below(uint64_t v) {
+  return (uint64_t)lanes_below<N>((uint32_t)(v >> 32)) << 32 | lanes_below<N>((uint32_t)v);
+}
+__device__ __forceinline__ uint32_t of_lane(uint32_t v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, int l) {
+  return (uint64_t)of_lane((uint32_t)(v >> 32), l) << 32 | of_lane((uint32_t)v, l);
+}
+
+// A value that all threads have alike, taken into scalar registers.
+__device__ __forceinline__ uint32_t alike(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int32_t alike(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t alike(uint64_t v) {
+  return (uint64_t)alike((uint32_t)(v >> 32)) << 32 | alike((uint32_t)v);
+}
+__device__ __forceinline__ float alike(float v) { return __uint_as_float(alike(__float_as_uint(v))); }
+
 // Sums up to and with each thread's; the total in `total`.
 template <typename V>
 __device__ __forceinline__ V block_prefix(V v, V* waves, V& total) {
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const V up = __shfl_up(v, off);
-    if (lane >= off) v += up;
-  }
+  v += lanes_below<1>(v);
+  v += lanes_below<2>(v);
+  v += lanes_below<4>(v);
+  v += lanes_below<8>(v);
+  const V a = of_lane(v, 15), b = a + of_lane(v, 31), c = b + of_lane(v, 47), all = c + of_lane(v, 63);
+  const int row = lane >> 4;
+  v += row == 0 ? 0 : row == 1 ? a : row == 2 ? b : c;
   __syncthreads();   // the last sums have been read
-  if (lane == kWave - 1) waves[w] = v;
+  if (lane == 0) waves[w] = all;
   __syncthreads();
   V before = 0;
   total = 0;
 #pragma unroll
   for (int i = 0; i < kSmWaves; ++i) {
-    if (i < w) before += waves[i];
-    total += waves[i];
+    const V o = waves[i];
+    if (i < w) before += o;
+    total += o;
   }
   return v + before;
 }
@@ -186,48 +309,61 @@ struct Place {
 };
 
 // One workgroup's view of its row.
-template <typename T>
+template <typename T, int KEEP>
 struct Row {
   const SampleArgs& a;
   const int t;
   Shared& s;
+  const Logits<T, KEEP>& logits;
   RowScale scale;
   uint32_t top;             // ordered bits of the largest
-  // what s.list holds: the tokens of these bits, and what stands before them
-  uint32_t lo = 1, hi = 0, before = 0, length = 0;
+  // what s.list holds: the tokens of these bits and these bins, and what
+  // stands before them
+  uint32_t lo = 1, hi = 0, bin0 = 0, bin1 = 0, before = 0, length = 0;
   uint64_t before_mass = 0, mass = 0;
 
-  // The smallest bits whose bin is b or an earlier one: 64 places of the
-  // range at a time, the same in every wave.
-  __device__ uint32_t first_key(uint32_t b) const {
+  // The smallest bits for which `yes` holds, as it does for the largest logit's
+  // and for all above the answer: 64 places of the range at a time, the same
+  // in every wave.
+  template <typename Yes>
+  __device__ uint32_t least_key(const Yes& yes) const {
     const int lane = threadIdx.x & (kWave - 1);
-    uint32_t from = kFirstLive, to = top;   // bin(to) <= b
+    uint32_t from = kFirstLive, to = top;
     while (from < to) {
       const uint32_t step = (to - from) / kWave + 1;
       const uint64_t at = (uint64_t)from + (uint64_t)step * lane;
-      const uint64_t yes = __ballot(at >= to || scale.bin(unordered((uint32_t)at)) <= b);
-      if (yes == 0) {
+      const uint64_t holds = __ballot(at >= to || yes((uint32_t)at));
+      if (holds == 0) {
         from += step * (kWave - 1) + 1;
         continue;
       }
-      const int l = __builtin_ctzll(yes);
+      const int l = __builtin_ctzll(holds);
       const uint64_t next = (uint64_t)from + (uint64_t)step * l;
       if (next < to) to = (uint32_t)next;
       if (l > 0) from += step * (l - 1) + 1;
     }
     return to;
   }
+  // The smallest bits whose bin is b or an earlier one.
+  __device__ uint32_t first_key(uint32_t b) const {
+    return least_key([&](uint32_t k) { return scale.bin(unordered(k)) <= b; });
+  }
 
   // Counts, and weights if they are wanted, by `where` (a bin, or none for
   // kSmBins and above) of the tokens, up to and with each bin.
   template <typename Where>
   __device__ void histogram(int at, bool weights, const Where& where) {
+    fill(at, weights, where);
+    sum_up(at);
+  }
+  template <typename Where>
+  __device__ void fill(int at, bool weights, const Where& where) {
     const int tid = threadIdx.x;
     __syncthreads();
     s.count[at][tid] = 0;
     s.mass[at][tid] = 0;
     __syncthreads();
-    walk<T>(a, t, [&](float x, int) {
+    logits.walk([&](float x, int) __attribute__((always_inline)) {
       if (!(x > -__builtin_inff())) return;
       const uint32_t b = where(x);
       if (b >= kSmBins) return;
@@ -238,6 +374,9 @@ struct Row {
       }
     });
     __syncthreads();
+  }
+  __device__ void sum_up(int at) {
+    const int tid = threadIdx.x;
     uint32_t all;
     uint64_t all_mass;
     const uint32_t n = block_prefix(s.count[at][tid], s.wave_count, all);
@@ -256,43 +395,96 @@ struct Row {
     __syncthreads();
     if (less < goal && upto >= goal) s.found = tid;
     __syncthreads();
-    const uint32_t b = s.found;
+    const uint32_t b = alike(s.found);
     __syncthreads();
     return b;
   }
 
-  // The tokens of these bits (no more than the list holds) into the list, in order.
-  __device__ void load(uint32_t from, uint32_t to, uint32_t n0, uint64_t m0) {
+  // The list in order, larger first: each key's place is the number of larger
+  // ones, counted by four threads.
+  __device__ void rank_list(int n) {
+    const int tid = threadIdx.x, e = tid % kSmSmall, part = tid / kSmSmall;
+    static_assert(kSmThreads == 4 * kSmSmall, "four threads a token");
+    const uint64_t key = e < n ? s.list[e] : 0;
+    const int per = (n + 3) / 4, last = min((part + 1) * per, n);
+    int rank = 0;
+    if (e < n) {
+#pragma unroll 4
+      for (int j = part * per; j < last; ++j) rank += s.list[j] > key ? 1 : 0;
+    }
+    s.rank[part][e] = rank;
+    __syncthreads();
+    if (part == 0 && e < n) s.list[s.rank[0][e] + s.rank[1][e] + s.rank[2][e] + s.rank[3][e]] = key;
+    __syncthreads();
+  }
+
+  // The same for more of them, bitonic: keys are unique but for the filling.
+  // Steps of up to 64 places stay within a wave's own 128.
+  __device__ void sort_list(int n) {
+    const int tid = threadIdx.x;
+    int size = 2 * kSmSmall;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kSmThreads) s.list[i] = 0;
+    __syncthreads();
+    const auto step = [&](int k, int j) {
+      if (tid >= size / 2) return;
+      const int i = 2 * tid - (tid & (j - 1));   // bit j clear
+      const uint64_t x = s.list[i], y = s.list[i + j];
+      if ((x < y) == ((i & k) == 0)) {
+        s.list[i] = y;
+        s.list[i + j] = x;
+      }
+    };
+    for (int k = 2; k <= size; k *= 2) {
+      int j = k / 2;
+      for (; j > kWave; j /= 2) {
+        step(k, j);
+        __syncthreads();
+      }
+      for (; j > 0; j /= 2) {
+        step(k, j);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+      }
+      __syncthreads();
+    }
+  }
+
+  // A value that no logit of bin b or an earlier one is below: the bin's far
+  // edge with room for the roundings of a distance and its product.
+  __device__ __forceinline__ float floor_of(uint32_t b) const {
+    if (b + 1 >= kSmBins || !(scale.inv > 0.0f) || !(scale.m < __builtin_inff())) return -__builtin_inff();
+    const float d = (float)(b + 1) / scale.inv;
+    return scale.m - d - (__builtin_fabsf(scale.m) + d) * 0x1p-20f;
+  }
+
+  // The tokens of these bits and bins (no more than the list holds) into the
+  // list, in order.
+  __device__ void load(uint32_t from, uint32_t to, uint32_t b0, uint32_t b1, uint32_t n0, uint64_t m0) {
     const int tid = threadIdx.x;
     __syncthreads();
     if (tid == 0) s.length = 0;
     __syncthreads();
-    walk<T>(a, t, [&](float x, int id) {
-      const uint32_t k = ordered(x);
-      if (!(x > -__builtin_inff()) || k < from || k > to) return;
+    const float least = __builtin_fmaxf(unordered(from), floor_of(b1));
+    const auto take = [&](float x, int id) __attribute__((always_inline)) {
+      if (!(x >= least) || !(x > -__builtin_inff())) return;   // NaN too
+      const uint32_t k = ordered(x), b = scale.bin(x);
+      if (k < from || k > to || b < b0 || b > b1) return;
       const int at = atomicAdd(&s.length, 1);
       if (at < kSmCap) s.list[at] = ((uint64_t)k << 32) | (uint32_t)~id;
+    };
+    logits.loads([&](const uint4& r, int id) __attribute__((always_inline)) {
+      float largest = -__builtin_inff();
+      logits.values(r, [&](float x) __attribute__((always_inline)) { largest = __builtin_fmaxf(largest, x); });
+      if (largest >= least) logits.one_by_one(r, id, take);
     });
+    logits.ends(take);
     __syncthreads();
-    const int n = min(s.length, kSmCap);
-    int size = 2;
-    while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kSmThreads) s.list[i] = 0;
-    __syncthreads();
-    // bitonic, larger first; keys are unique but for the filling
-    for (int k = 2; k <= size; k *= 2) {
-      for (int j = k / 2; j > 0; j /= 2) {
-        if (tid < size / 2) {
-          const int i = 2 * tid - (tid & (j - 1));   // bit j clear
-          const uint64_t x = s.list[i], y = s.list[i + j];
-          if ((x < y) == ((i & k) == 0)) {
-            s.list[i] = y;
-            s.list[i + j] = x;
-          }
-        }
-        __syncthreads();
-      }
-    }
+    const int n = alike(min(s.length, kSmCap));
+    if (n <= kSmSmall)
+      rank_list(n);
+    else
+      sort_list(n);
     const int i0 = 2 * tid, i1 = 2 * tid + 1;
     const uint64_t q0 = i0 < n ? scale.weight(unordered((uint32_t)(s.list[i0] >> 32))) : 0;
     const uint64_t q1 = i1 < n ? scale.weight(unordered((uint32_t)(s.list[i1] >> 32))) : 0;
@@ -303,17 +495,22 @@ struct Row {
     __syncthreads();
     lo = from;
     hi = to;
+    bin0 = b0;
+    bin1 = b1;
     before = n0;
     before_mass = m0;
     length = (uint32_t)n;
-    mass = all;
+    mass = alike(all);
   }
 
   __device__ bool listed(By by, uint64_t goal) const {
     switch (by) {
       case By::kCount: return goal > before && goal <= (uint64_t)before + length;
       case By::kMass: return goal > before_mass && goal <= before_mass + mass;
-      default: return lo <= hi && goal >= lo && goal <= hi;
+      default: {
+        const uint32_t b = scale.bin(unordered((uint32_t)goal));
+        return lo <= hi && goal >= lo && goal <= hi && b >= bin0 && b <= bin1;
+      }
     }
   }
 
@@ -331,11 +528,11 @@ struct Row {
       }
     }
     __syncthreads();
-    const uint32_t n = by == By::kCount ? (uint32_t)goal - before : s.found;
+    const uint32_t n = by == By::kCount ? (uint32_t)goal - before : alike(s.found);
     __syncthreads();
     if (n == 0) return Place{before, before_mass, top, -1};
-    const uint64_t e = s.list[n - 1];
-    return Place{before + n, s.list_mass[n - 1], (uint32_t)(e >> 32), (int32_t)~(uint32_t)e};
+    const uint64_t e = alike(s.list[n - 1]);
+    return Place{before + n, alike(s.list_mass[n - 1]), (uint32_t)(e >> 32), (int32_t)~(uint32_t)e};
   }
 
   // The n-th token, by place in the row, of those with these bits.
@@ -365,7 +562,7 @@ struct Row {
       s.found = (uint32_t)i;
     }
     __syncthreads();
-    const int32_t id = (int32_t)s.found;
+    const int32_t id = alike((int32_t)s.found);
     __syncthreads();
     return id;
   }
@@ -375,12 +572,21 @@ struct Row {
   __device__ Place find(By by, uint64_t goal) {
     if (listed(by, goal)) return in_list(by, goal);
     uint32_t b = by == By::kKey ? scale.bin(unordered((uint32_t)goal)) : bin_of(0, by, goal, 0, 0);
-    uint32_t n0 = b ? s.count[0][b - 1] : 0, n = s.count[0][b] - n0;
-    uint64_t m0 = b ? s.mass[0][b - 1] : 0;
-    uint32_t from = first_key(b), to = b ? first_key(b - 1) - 1 : top;
-    if (n0 + n <= kSmCap) {   // all that stands before it too: the next goal is likely among them
-      load(from, top, 0, 0);
-      return in_list(by, goal);
+    uint32_t n0 = b ? alike(s.count[0][b - 1]) : 0, n = alike(s.count[0][b]) - n0;
+    uint64_t m0 = b ? alike(s.mass[0][b - 1]) : 0;
+    const uint32_t first = b;
+    uint32_t from = kFirstLive, to = top, b0 = b;
+    if (n0 + n <= kSmSmall || (n0 + n <= kSmCap && alike(s.mass[0][kSmBins - 1]) == 0)) {
+      // all that stands before it too: the next goal is likely among them, and
+      // is where no weights were counted
+      b0 = 0;
+      n += n0;
+      n0 = 0;
+      m0 = 0;
+    }
+    if (n > kSmCap) {
+      from = first_key(b);
+      to = b ? first_key(b - 1) - 1 : top;
     }
     while (n > kSmCap && from < to) {   // too many: by their bits
       int shift = 0;
@@ -390,15 +596,15 @@ struct Row {
         return k < from || k > to ? kSmBins : (to - k) >> shift;
       });
       b = by == By::kKey ? (to - (uint32_t)goal) >> shift : bin_of(1, by, goal, n0, m0);
-      const uint32_t nb = b ? s.count[1][b - 1] : 0;
-      n = s.count[1][b] - nb;
+      const uint32_t nb = b ? alike(s.count[1][b - 1]) : 0;
+      n = alike(s.count[1][b]) - nb;
       n0 += nb;
-      m0 += b ? s.mass[1][b - 1] : 0;
+      m0 += b ? alike(s.mass[1][b - 1]) : 0;
       to -= b << shift;
       from = to - from < (1u << shift) ? from : to - (1u << shift) + 1;
     }
     if (n <= kSmCap) {
-      load(from, to, n0, m0);
+      load(from, to, b0, first, n0, m0);
       return in_list(by, goal);
     }
     const uint64_t q = scale.weight(unordered(to));   // n tokens of one value
@@ -407,16 +613,41 @@ struct Row {
   }
 };
 
-template <typename T>
-__global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
-  __shared__ Shared s;
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1);
-  const float inf = __builtin_inff();
-  float most = -inf, least = inf;
-  walk<T>(a, t, [&](float x, int) {
+// A row's settings, with those that are off in numbers that keep all.
+struct Settings {
+  float temperature, p, low;
+  int64_t k;
+  bool few;   // a few tokens alone are asked for: no weight is needed but theirs
+  __device__ __forceinline__ Settings(const SampleArgs& a, int t)
+      : temperature(a.temperature ? a.temperature[t] : 1.0f), p(a.top_p ? a.top_p[t] : 1.0f),
+        low(a.min_p ? a.min_p[t] : 0.0f), k(a.top_k ? a.top_k[t] : 0) {
+    if (!(temperature > 0.0f)) {
+      temperature = 1.0f;
+      k = 1;
+      p = 1.0f;
+      low = 0.0f;
+    }
+    few = k > 0 && k <= kSmCap / 2;
+  }
+  // Bins reach to where weights are zero, or as far as the row does.
+  __device__ __forceinline__ RowScale scale(float most, float least, int bits) const {
+    const float far = __builtin_fminf(temperature * (float)((bits + 1) * 0.6931472), most - least);
+    return RowScale{most, 1.4426950408889634 / (double)temperature,
+                    far > 0.0f ? __builtin_fminf(kSmBins / far, 3.0e38f) : 0.0f, bits};
+  }
+};
+
+// The largest and smallest live logit, in every thread.
+template <typename T, int KEEP>
+__device__ __forceinline__ float2 range_of(const Logits<T, KEEP>& logits, Shared& s) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  float most = -__builtin_inff(), least = __builtin_inff();
+  const auto take = [&](float x) __attribute__((always_inline)) {
     most = __builtin_fmaxf(most, x);   // NaN passes by
-    if (x > -inf) least = __builtin_fminf(least, x);
-  });
+    least = __builtin_fminf(least, x > -__builtin_inff() ? x : __builtin_inff());
+  };
+  logits.loads([&](const uint4& r, int) __attribute__((always_inline)) { logits.values(r, take); });
+  logits.ends([&](float x, int) __attribute__((always_inline)) { take(x); });
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
     most = __builtin_fmaxf(most, __shfl_xor(most, off));
@@ -427,104 +658,175 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
     s.wave_min[tid / kWave] = least;
   }
   __syncthreads();
+#pragma unroll
   for (int w = 0; w < kSmWaves; ++w) {
     most = __builtin_fmaxf(most, s.wave_max[w]);
     least = __builtin_fminf(least, s.wave_min[w]);
   }
-  if (most == -inf) {   // masked throughout
+  return make_float2(alike(most), alike(least));
+}
+
+// The same of a row whose pieces' are known.
+__device__ __forceinline__ float2 joined_range(const SampleArgs& a, int t) {
+  float2 r = a.ranges[(size_t)t * a.segs];
+  for (int i = 1; i < a.segs; ++i) {
+    const float2 o = a.ranges[(size_t)t * a.segs + i];
+    r = make_float2(__builtin_fmaxf(r.x, o.x), __builtin_fminf(r.y, o.y));
+  }
+  return make_float2(alike(r.x), alike(r.y));
+}
+
+template <typename T>
+__global__ __launch_bounds__(kSmThreads) void k_sample_range(SampleArgs a) {
+  __shared__ Shared s;
+  const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs;
+  const Logits<T, 0> logits(a, t, seg);
+  const float2 r = range_of(logits, s);
+  if (threadIdx.x == 0) a.ranges[blockIdx.x] = r;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kSmThreads) void k_sample_bins(SampleArgs a) {
+  __shared__ Shared s;
+  const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs, tid = threadIdx.x;
+  const float2 range = joined_range(a, t);
+  if (range.x == -__builtin_inff()) return;
+  const Logits<T, 0> logits(a, t, seg);
+  const Settings set(a, t);
+  Row<T, 0> row{a, t, s, logits, set.scale(range.x, range.y, a.bits), ordered(range.x)};
+  row.fill(0, !set.few, [&](float x) __attribute__((always_inline)) { return row.scale.bin(x); });
+  a.counts[(size_t)blockIdx.x * kSmBins + tid] = s.count[0][tid];
+  if (!set.few) a.masses[(size_t)blockIdx.x * kSmBins + tid] = s.mass[0][tid];
+}
+
+// The choice.  PIECES: the pieces' histograms are there.
+template <typename T, int KEEP, bool PIECES>
+__global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
+  __shared__ Shared s;
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const Logits<T, KEEP> logits(a, t, -1);
+  const float2 range = PIECES ? joined_range(a, t) : range_of(logits, s);
+  const float most = range.x, least = range.y;
+  if (most == -__builtin_inff()) {   // masked throughout
     if (tid == 0) {
       a.ids[t] = -1;
-      if (a.logprob) a.logprob[t] = -inf;
+      if (a.logprob) a.logprob[t] = -__builtin_inff();
       if (a.kept) a.kept[t] = 0;
     }
     return;
   }
-
-  float temp = a.temperature ? a.temperature[t] : 1.0f;
-  int64_t k = a.top_k ? a.top_k[t] : 0;
-  float p = a.top_p ? a.top_p[t] : 1.0f, low = a.min_p ? a.min_p[t] : 0.0f;
-  if (!(temp > 0.0f)) {
-    temp = 1.0f;
-    k = 1;
-    p = 1.0f;
-    low = 0.0f;
-  }
-  // Bins reach to where weights are zero, or as far as the row does.
-  const float far = __builtin_fminf(temp * (float)((a.bits + 1) * 0.6931472), most - least);
-  Row<T> row{a, t, s, RowScale{most, 1.4426950408889634 / (double)temp, far > 0.0f ? __builtin_fminf(kSmBins / far, 3.0e38f) : 0.0f, a.bits},
-             ordered(most)};
-  // A few tokens alone are asked for: no weight is needed but theirs.
-  const bool few = k > 0 && k <= kSmCap / 2;
-  row.histogram(0, !few, [&](float x) { return row.scale.bin(x); });
-  const uint32_t live = s.count[0][kSmBins - 1];
-  if (few) {
-    const uint32_t want = k < live ? (uint32_t)k : live;
-    if (s.count[0][row.bin_of(0, By::kCount, want, 0, 0)] > kSmCap)
-      row.histogram(0, true, [&](float x) { return row.scale.bin(x); });
-    else
-      row.find(By::kCount, want);
-  }
-  Place cut{live, s.mass[0][kSmBins - 1], ordered(least), -1};
-  if (k > 0 && k < live) cut = row.find(By::kCount, (uint64_t)k);
-  else if (few) cut = row.find(By::kCount, live);
-  if (p < 1.0f) {
-    const double goal = __builtin_ceil((double)p * (double)cut.mass);
-    cut = row.find(By::kMass, goal < 1.0 ? 1 : goal >= (double)cut.mass ? cut.mass : (uint64_t)goal);
-  }
-  if (low > 0.0f) {
-    // The least bits that pass: found from the bound's own value, 64 at a time
-    // as first_key does.
-    const double bound = log((double)low);
-    const auto passes = [&](uint32_t key) {
-      const float x = unordered(key);
-      return x == most || ((double)x - (double)most) / (double)temp >= bound;
-    };
-    uint32_t from = kFirstLive, to = row.top;
-    while (from < to) {
-      const uint32_t step = (to - from) / kWave + 1;
-      const uint64_t at = (uint64_t)from + (uint64_t)step * lane;
-      const uint64_t yes = __ballot(at >= to || passes((uint32_t)at));
-      if (yes == 0) {
-        from += step * (kWave - 1) + 1;
-        continue;
-      }
-      const int l = __builtin_ctzll(yes);
-      const uint64_t next = (uint64_t)from + (uint64_t)step * l;
-      if (next < to) to = (uint32_t)next;
-      if (l > 0) from += step * (l - 1) + 1;
+  const Settings set(a, t);
+  Row<T, KEEP> row{a, t, s, logits, set.scale(most, least, a.bits), ordered(most)};
+  if constexpr (PIECES) {
+    uint32_t count = 0;
+    uint64_t mass = 0;
+#pragma unroll 8
+    for (int i = 0; i < a.segs; ++i) {
+      const size_t at = ((size_t)t * a.segs + i) * kSmBins + tid;
+      count += a.counts[at];
+      if (!set.few) mass += a.masses[at];
     }
-    if (cut.key < to) cut = row.find(By::kKey, to);
+    s.count[0][tid] = count;
+    s.mass[0][tid] = mass;
+    __syncthreads();
+    row.sum_up(0);
+  } else {
+    row.histogram(0, !set.few, [&](float x) __attribute__((always_inline)) { return row.scale.bin(x); });
   }
-  const float u = a.uniforms[t];
-  const double at = __builtin_floor((double)u * (double)cut.mass);
-  const uint64_t goal = !(at > 0.0) ? 0 : at >= (double)cut.mass ? cut.mass - 1 : (uint64_t)at;
-  const Place drawn = row.find(By::kMass, (goal < cut.mass ? goal : cut.mass - 1) + 1);
+  const int64_t k = set.k;
+  const uint32_t live = alike(s.count[0][kSmBins - 1]);
+  if (set.few) {   // more equal ones than the list holds: weights after all
+    const uint32_t want = k < live ? (uint32_t)k : live;
+    if (alike(s.count[0][row.bin_of(0, By::kCount, want, 0, 0)]) > kSmCap)
+      row.histogram(0, true, [&](float x) __attribute__((always_inline)) { return row.scale.bin(x); });
+  }
+  // The places that cut the order, then the one that is drawn, by one copy of
+  // the search.
+  Place cut{live, alike(s.mass[0][kSmBins - 1]), ordered(least), -1}, drawn = cut;
+#pragma unroll 1
+  for (int step = 0; step < 4; ++step) {
+    By by = By::kMass;
+    uint64_t goal = 0;   // none
+    if (step == 0 && (set.few || (k > 0 && k < live))) {
+      by = By::kCount;
+      goal = k < live ? (uint64_t)k : live;
+    } else if (step == 1 && set.p < 1.0f) {
+      const double at = __builtin_ceil((double)set.p * (double)cut.mass);
+      goal = at < 1.0 ? 1 : at >= (double)cut.mass ? cut.mass : (uint64_t)at;
+    } else if (step == 2 && set.low > 0.0f) {
+      const double bound = log((double)set.low);   // the least bits that pass
+      const uint32_t key = row.least_key([&](uint32_t key) __attribute__((always_inline)) {
+        const float x = unordered(key);
+        return x == most || ((double)x - (double)most) / (double)set.temperature >= bound;
+      });
+      by = By::kKey;
+      goal = cut.key < key ? key : 0;
+    } else if (step == 3) {
+      const double at = __builtin_floor((double)a.uniforms[t] * (double)cut.mass);
+      const uint64_t below = !(at > 0.0) ? 0 : at >= (double)cut.mass ? cut.mass - 1 : (uint64_t)at;
+      goal = (below < cut.mass ? below : cut.mass - 1) + 1;
+    }
+    if (goal == 0) continue;
+    drawn = row.find(by, goal);
+    if (step < 3) cut = drawn;
+  }
   if (tid == 0) {
     a.ids[t] = drawn.id;
     if (a.kept) a.kept[t] = (int32_t)cut.n;
     if (a.logprob) {
       const float x = unordered(drawn.key);
-      const double d = x == most ? 0.0 : ((double)x - (double)most) / (double)temp;
+      const double d = x == most ? 0.0 : ((double)x - (double)most) / (double)set.temperature;
       a.logprob[t] = (float)(d - (log((double)cut.mass) - a.bits * 0.6931471805599453));
     }
   }
 }
 
+// Pieces of a row: two workgroups a CU for the whole call, and no less than
+// one pass of the workgroup's threads over 16 bytes each.
+int64_t pieces_of(int64_t tokens, int64_t vocab) {
+  int64_t segs = 512 / (tokens > 0 ? tokens : 1);
+  if (segs > 16) segs = 16;
+  if (segs > vocab / 8192) segs = vocab / 8192;
+  return segs < 2 ? 1 : segs;
+}
+
+template <typename T>
+hipError_t sample_launch(const SampleArgs& a, hipStream_t stream) {
+  constexpr int kVec = 16 / sizeof(T);
+  if (a.segs > 1) {
+    k_sample_range<T><<<a.tokens * a.segs, kSmThreads, 0, stream>>>(a);
+    k_sample_bins<T><<<a.tokens * a.segs, kSmThreads, 0, stream>>>(a);
+    k_sample<T, 0, true><<<a.tokens, kSmThreads, 0, stream>>>(a);
+  } else if (a.vocab <= 4 * kSmThreads * kVec) {
+    k_sample<T, 4, false><<<a.tokens, kSmThreads, 0, stream>>>(a);
+  } else {
+    k_sample<T, 0, false><<<a.tokens, kSmThreads, 0, stream>>>(a);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
-int sample_segments(int64_t, int64_t) { return 1; }
-int64_t sample_workspace_bytes(int64_t, int64_t) { return 0; }
+int sample_segments(int64_t tokens, int64_t vocab) { return (int)pieces_of(tokens, vocab); }
+
+int64_t sample_workspace_bytes(int64_t tokens, int64_t vocab) {
+  const int64_t segs = pieces_of(tokens, vocab);
+  return segs == 1 ? 0 : tokens * segs * (int64_t)(sizeof(float2) + kSmBins * (sizeof(uint64_t) + sizeof(uint32_t)));
+}
 
 hipError_t launch_sample(const SampleCall& c, hipStream_t stream) {
   int log = 0;
   while (((int64_t)1 << log) < c.vocab) ++log;
-  const SampleArgs a{c.logits, c.uniforms, c.temperature, c.top_k, c.top_p, c.min_p, c.ids, c.logprob, c.kept,
-                     c.stride, c.tokens, c.vocab, log > 12 ? 62 - log : 50};
-  if (c.f32)
-    k_sample<float><<<c.tokens, kSmThreads, 0, stream>>>(a);
-  else
-    k_sample<uint16_t><<<c.tokens, kSmThreads, 0, stream>>>(a);
-  return hipGetLastError();
+  const int segs = (int)pieces_of(c.tokens, c.vocab);
+  SampleArgs a{c.logits, c.uniforms, c.temperature, c.top_k, c.top_p, c.min_p, c.ids, c.logprob, c.kept,
+               c.stride, c.tokens, c.vocab, log > 12 ? 62 - log : 50, segs, 0, nullptr, nullptr, nullptr};
+  if (segs > 1) {
+    a.per = (int32_t)(((c.vocab + 7) / segs + 8) & ~7);   // a piece starts at a multiple of 16 bytes
+    a.masses = static_cast<uint64_t*>(c.workspace);
+    a.ranges = reinterpret_cast<float2*>(a.masses + (size_t)c.tokens * segs * kSmBins);
+    a.counts = reinterpret_cast<uint32_t*>(a.ranges + (size_t)c.tokens * segs);
+  }
+  return c.f32 ? sample_launch<float>(a, stream) : sample_launch<uint16_t>(a, stream);
 }
 
 }  // namespace fp8w
