@@ -41,6 +41,7 @@ constexpr int kSmWaves = kSmThreads / kWave;
 constexpr int kSmBins = kSmThreads;   // a thread a bin
 constexpr int kSmCap = 2048;          // tokens of a sorted list
 constexpr int kSmSmall = 256;         // of one that is ranked by counting, four threads a token
+constexpr int kSmPieces = 16;         // of a row, at most
 constexpr uint32_t kFirstLive = 0x00800000u;   // the ordered bits of the lowest value; -inf is one below
 
 // Value bits whose unsigned order is the values' order (-0 equal to +0).
@@ -117,6 +118,7 @@ struct RowScale {
 // took 50 us where the row had 5000 tokens).
 template <typename T, int KEEP>
 struct Logits {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   static constexpr int kVec = 16 / sizeof(T);
   static constexpr int kBatch = KEEP ? KEEP : 4;   // loads that leave at once
   // Places are counted from the 16-byte boundary at or below the row's start;
@@ -182,7 +184,7 @@ struct Logits {
       }
     }
   }
-  // 16 bytes at a time, a few at once: g(16 bytes, token of their first).
+  // 16 bytes at a time, a few at once: g(16 bytes, which of the row's).
   template <typename G>
   __device__ __forceinline__ void loads(const G& g) const {
     const int tid = threadIdx.x;
@@ -192,9 +194,44 @@ struct Logits {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) r[i] = KEEP ? kept[i] : load(v + i * kSmThreads);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) g(r[i], (int)((v + i * kSmThreads) * kVec) - (skew & 0xFF));
+      for (int i = 0; i < kBatch; ++i) g(r[i], (int)(v + i * kSmThreads));
     }
   }
+  __device__ __forceinline__ int first_token(int v) const { return v * kVec - (skew & 0xFF); }
+  // Whether one of 16 bytes' values may lie in [lo, hi], by their bits: on one
+  // side of zero these are in order, and a difference and a minimum for each
+  // value (two of bf16's at once) tell.
+  struct Band {
+    float lo, hi;
+    bool bits;             // both on one side of zero
+    uint32_t first, width;
+    __device__ __forceinline__ Band(float l, float h) : lo(l), hi(h), bits(l > 0.0f || h < 0.0f) {
+      const uint32_t near = __float_as_uint(l > 0.0f ? l : h), far = __float_as_uint(l > 0.0f ? h : l);
+      constexpr int kShift = sizeof(T) == 4 ? 0 : 16;
+      first = near >> kShift;
+      width = (far >> kShift) - first;
+    }
+    __device__ __forceinline__ bool has(const uint4& r) const {
+      if (!bits) {
+        bool any = false;
+        values(r, [&](float x) __attribute__((always_inline)) { any |= x >= lo && x <= hi; });
+        return any;
+      }
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      if constexpr (sizeof(T) == 4) {
+        uint32_t least = w[0] - first;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) least = min(least, w[i] - first);
+        return least <= width;
+      } else {
+        const u16x2 down = {(uint16_t)first, (uint16_t)first};
+        u16x2 least = __builtin_bit_cast(u16x2, w[0]) - down;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, w[i]) - down);
+        return least[0] <= width || least[1] <= width;
+      }
+    }
+  };
   // Each of 16 bytes' values, f(logit, token), two copies of f.
   template <typename F>
   static __device__ __forceinline__ void one_by_one(uint4 r, int id, const F& f) {
@@ -225,7 +262,7 @@ struct Logits {
     for (; v < v1; v += kBatch * kSmThreads) {
 #pragma unroll 1
       for (int i = 0; i < kBatch; ++i) {
-        one_by_one(r[0], (int)((v + i * kSmThreads) * kVec) - (skew & 0xFF), f);
+        one_by_one(r[0], first_token((int)(v + i * kSmThreads)), f);
 #pragma unroll
         for (int j = 0; j + 1 < kBatch; ++j) r[j] = r[j + 1];
       }
@@ -244,9 +281,8 @@ struct Shared {
   uint64_t wave_mass[kSmWaves];
   uint32_t wave_count[kSmWaves];
   float wave_max[kSmWaves], wave_min[kSmWaves];
-  int length;
-  uint64_t found_mass;
-  uint32_t found, found_count;
+  int length, queued;
+  uint32_t found;
 };
 
 // A value from the lane n places below in its row of 16 (0 from none).
@@ -450,35 +486,51 @@ struct Row {
     }
   }
 
-  // A value that no logit of bin b or an earlier one is below: the bin's far
-  // edge with room for the roundings of a distance and its product.
+  // Values that no logit of bin b is below, or above: the bin's edges with
+  // room for the roundings of a distance and its product.
   __device__ __forceinline__ float floor_of(uint32_t b) const {
-    if (b + 1 >= kSmBins || !(scale.inv > 0.0f) || !(scale.m < __builtin_inff())) return -__builtin_inff();
+    if (b + 1 >= kSmBins || !(scale.inv > 0.0f) || !(scale.m < __builtin_inff())) return -3.4028234e38f;
     const float d = (float)(b + 1) / scale.inv;
-    return scale.m - d - (__builtin_fabsf(scale.m) + d) * 0x1p-20f;
+    return __builtin_fmaxf(scale.m - d - (__builtin_fabsf(scale.m) + d) * 0x1p-20f, -3.4028234e38f);
+  }
+  __device__ __forceinline__ float ceiling_of(uint32_t b) const {
+    if (b == 0 || !(scale.inv > 0.0f) || !(scale.m < __builtin_inff())) return scale.m;
+    const float d = (float)b / scale.inv;
+    return __builtin_fminf(scale.m - d + (__builtin_fabsf(scale.m) + d) * 0x1p-20f, scale.m);
   }
 
   // The tokens of these bits and bins (no more than the list holds) into the
-  // list, in order.
+  // list, in order.  What may hold one is noted first, 16 bytes at a time, and
+  // looked at again by all threads together.
   __device__ void load(uint32_t from, uint32_t to, uint32_t b0, uint32_t b1, uint32_t n0, uint64_t m0) {
     const int tid = threadIdx.x;
+    int* const queue = reinterpret_cast<int*>(s.list_mass);
+    constexpr int kQueue = kSmCap * 2;
     __syncthreads();
-    if (tid == 0) s.length = 0;
+    if (tid == 0) s.length = s.queued = 0;
     __syncthreads();
-    const float least = __builtin_fmaxf(unordered(from), floor_of(b1));
+    const typename Logits<T, KEEP>::Band band(alike(__builtin_fmaxf(unordered(from), floor_of(b1))),
+                                              alike(__builtin_fminf(unordered(to), ceiling_of(b0))));
     const auto take = [&](float x, int id) __attribute__((always_inline)) {
-      if (!(x >= least) || !(x > -__builtin_inff())) return;   // NaN too
+      if (!(x >= band.lo && x <= band.hi)) return;   // NaN and -inf too
       const uint32_t k = ordered(x), b = scale.bin(x);
       if (k < from || k > to || b < b0 || b > b1) return;
       const int at = atomicAdd(&s.length, 1);
       if (at < kSmCap) s.list[at] = ((uint64_t)k << 32) | (uint32_t)~id;
     };
-    logits.loads([&](const uint4& r, int id) __attribute__((always_inline)) {
-      float largest = -__builtin_inff();
-      logits.values(r, [&](float x) __attribute__((always_inline)) { largest = __builtin_fmaxf(largest, x); });
-      if (largest >= least) logits.one_by_one(r, id, take);
+    logits.loads([&](const uint4& r, int v) __attribute__((always_inline)) {
+      if (!band.has(r) || v >= logits.v1) return;
+      const int at = atomicAdd(&s.queued, 1);
+      if (at < kQueue) queue[at] = v;
     });
-    logits.ends(take);
+    __syncthreads();
+    if (s.queued <= kQueue) {
+      logits.ends(take);
+#pragma unroll 1
+      for (int e = tid; e < s.queued; e += kSmThreads) logits.one_by_one(logits.load(queue[e]), logits.first_token(queue[e]), take);
+    } else {   // more that may than room to note it
+      logits.walk(take);
+    }
     __syncthreads();
     const int n = alike(min(s.length, kSmCap));
     if (n <= kSmSmall)
@@ -718,13 +770,18 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
   const Settings set(a, t);
   Row<T, KEEP> row{a, t, s, logits, set.scale(most, least, a.bits), ordered(most)};
   if constexpr (PIECES) {
-    uint32_t count = 0;
-    uint64_t mass = 0;
-#pragma unroll 8
-    for (int i = 0; i < a.segs; ++i) {
-      const size_t at = ((size_t)t * a.segs + i) * kSmBins + tid;
-      count += a.counts[at];
-      if (!set.few) mass += a.masses[at];
+    uint32_t counts[kSmPieces], count = 0;
+    uint64_t masses[kSmPieces], mass = 0;
+#pragma unroll
+    for (int i = 0; i < kSmPieces; ++i) {   // all of them on their way at once
+      const size_t at = ((size_t)t * a.segs + (i < a.segs ? i : 0)) * kSmBins + tid;
+      counts[i] = a.counts[at];
+      masses[i] = set.few ? 0 : a.masses[at];
+    }
+#pragma unroll
+    for (int i = 0; i < kSmPieces; ++i) {
+      count += i < a.segs ? counts[i] : 0;
+      mass += i < a.segs ? masses[i] : 0;
     }
     s.count[0][tid] = count;
     s.mass[0][tid] = mass;
@@ -785,7 +842,7 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
 // one pass of the workgroup's threads over 16 bytes each.
 int64_t pieces_of(int64_t tokens, int64_t vocab) {
   int64_t segs = 512 / (tokens > 0 ? tokens : 1);
-  if (segs > 16) segs = 16;
+  if (segs > kSmPieces) segs = kSmPieces;
   if (segs > vocab / 8192) segs = vocab / 8192;
   return segs < 2 ? 1 : segs;
 }
