@@ -53,6 +53,17 @@ __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// A value that all threads have alike, taken into scalar registers.
+__device__ __forceinline__ uint32_t alike(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int32_t alike(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t alike(uint64_t v) {
+  return (uint64_t)alike((uint32_t)(v >> 32)) << 32 | alike((uint32_t)v);
+}
+__device__ __forceinline__ float alike(float v) { return __uint_as_float(alike(__float_as_uint(v))); }
+__device__ __forceinline__ double alike(double v) {
+  return __longlong_as_double((int64_t)alike((uint64_t)__double_as_longlong(v)));
+}
+
 struct SampleArgs {
   const void* logits;
   const float* uniforms;
@@ -65,25 +76,54 @@ struct SampleArgs {
   int32_t* kept;
   int64_t stride;
   int32_t tokens, vocab, bits;   // bits: S
+  int32_t shift, fraction;       // of the histogram's words (RowScale)
   int32_t segs, per;             // pieces of a row, and places of a piece
   // of the pieces, where there is more than one
   float2* ranges;                // [tokens][segs]: largest and smallest logit
-  uint64_t* masses;              // [tokens][segs][bins]
-  uint32_t* counts;
+  uint64_t* words;               // [tokens][segs][bins]
 };
 
-// What turns a row's logits into weights and bins.
+// What turns a row's logits into weights and bins.  Bins are of equal width, and
+// reach to where weights are zero, or as far as the row does.
+//
+// The histogram adds, for each token, one to its bin's count and to the same
+// word the weight relative to that of the bin's middle, less one: |e| < 2^-5,
+// as a whole number of 2^-fraction, so that a bin's weight is that of its
+// middle times (count + sum of e).  An exponential for every token would take
+// twice as long, a second atomic as well.
 struct RowScale {
-  float m;           // the largest logit
-  double per;        // log2 e / T
-  float inv;         // bins for each unit of distance
-  int bits;
+  double m;            // the largest logit (2^200 for infinity)
+  double per;          // log2 e / T
+  double inv, wide;    // bins for each unit of distance; log2 of a bin's weights' ratio
+  double c1, c2, c3, c4;   // e of a place in the bin, times 2^fraction
+  int bits, shift, fraction;
 
-  // 2^bits exp((x - m) / T), rounded to nearest: exp2 of a whole part and a
-  // polynomial (Taylor, to 2^-42 of the value) of what is left, |f| <= 1/2.
-  __device__ __forceinline__ uint64_t weight(float x) const {
-    const double d = x == m ? 0.0 : (double)x - (double)m;
-    const double t = __builtin_fmax(d * per, -128.0);   // NaN (inf / inf) too
+  static constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: a sum's low word is its whole part, rounded
+  static constexpr int kBias = 26;                       // 2^kBias is added to e, so that it is positive
+
+  __device__ __forceinline__ RowScale(float most, float least, float temperature, const SampleArgs& a) {
+    m = above(most);
+    per = 1.4426950408889634 / (double)temperature;
+    bits = a.bits;
+    shift = a.shift;
+    fraction = a.fraction;
+    const double far = __builtin_fmin((double)temperature * ((bits + 12) * 0.6931471805599453), m - above(least));
+    inv = far > 0.0 ? __builtin_fmin((kSmBins - 1) / far, 1e300) : 0.0;
+    wide = inv > 0.0 ? per / inv : 0.0;
+    const double w = wide * 0.6931471805599453, unit = __builtin_ldexp(1.0, fraction);
+    c1 = -w * unit;
+    c2 = w * w * (unit / 2);
+    c3 = -w * w * w * (unit / 6);
+    c4 = w * w * w * w * (unit / 24);
+    m = alike(m), per = alike(per), inv = alike(inv), wide = alike(wide);
+    c1 = alike(c1), c2 = alike(c2), c3 = alike(c3), c4 = alike(c4);
+  }
+  static __device__ __forceinline__ double above(float x) { return __builtin_fmin((double)x, 0x1p200); }
+
+  // 2^bits 2^t, t <= 0, rounded to nearest: a whole part and a polynomial
+  // (Taylor, to 2^-42 of the value) of what is left, |f| <= 1/2.
+  __device__ __forceinline__ uint64_t power(double t) const {
+    t = __builtin_fmax(t, -128.0);
     const double n = __builtin_rint(t), f = t - n;
     double p = 7.054911620801121e-09;                   // ln2^k / k!, k = 10 ... 0
     p = __builtin_fma(p, f, 1.0178086009239696e-07);
@@ -96,14 +136,43 @@ struct RowScale {
     p = __builtin_fma(p, f, 2.402265069591007e-01);
     p = __builtin_fma(p, f, 6.931471805599453e-01);
     p = __builtin_fma(p, f, 1.0);
-    const double w = __builtin_ldexp(p, (int)n + bits);
-    return (uint64_t)__double_as_longlong(w + 4503599627370496.0) & ((1ull << 52) - 1);   // + 2^52: the units' place is the last bit
+    return whole(__builtin_ldexp(p, (int)n + bits));
   }
-  // Bin 0 holds the largest; a larger logit is never in a later bin.
+  static __device__ __forceinline__ uint64_t whole(double v) {   // below 2^52, rounded
+    return (uint64_t)__double_as_longlong(v + 4503599627370496.0) & ((1ull << 52) - 1);
+  }
+  __device__ __forceinline__ uint64_t weight(float x) const { return power((above(x) - m) * per); }
+
+  // Bin 0 holds the largest; a larger logit is never in a later bin.  `at` is
+  // its place, in bins, and `middle` the bin's.
+  __device__ __forceinline__ uint32_t bin(float x, double& at, double& middle) const {
+    at = __builtin_fmin((m - above(x)) * inv, (double)(kSmBins - 1));
+    const double y = at + kMagic;
+    middle = y - kMagic;
+    return (uint32_t)__double_as_longlong(y);
+  }
   __device__ __forceinline__ uint32_t bin(float x) const {
-    const float d = x == m ? 0.0f : __builtin_fminf(m - x, 3.4e38f);
-    const uint32_t b = (uint32_t)(d * inv);
-    return b < kSmBins ? b : kSmBins - 1;
+    double at, middle;
+    return bin(x, at, middle);
+  }
+  // What a token adds to its bin's word, without weight and with.
+  __device__ __forceinline__ uint64_t one() const { return 1ull << shift; }
+  __device__ __forceinline__ uint64_t one(double at, double middle) const {
+    const double d = at - middle;
+    double e = __builtin_fma(c4, d, c3);
+    e = __builtin_fma(e, d, c2);
+    e = __builtin_fma(e, d, c1);
+    const uint32_t low = (uint32_t)__double_as_longlong(__builtin_fma(e, d, kMagic)) + (1u << kBias);
+    return one() + low;
+  }
+  // A word's count and, of tokens around the middle of bin b, their weight.
+  __device__ __forceinline__ uint32_t count_of(uint64_t word) const { return (uint32_t)(word >> shift); }
+  __device__ __forceinline__ uint64_t mass_of(uint64_t word, uint32_t b) const {
+    const double count = (double)count_of(word);
+    const double e = (double)(word & (one() - 1)) - count * (double)(1 << kBias);
+    const double all = __builtin_fma(e, __builtin_ldexp(1.0, -fraction), count);
+    const double w = (double)power(-(double)b * wide);
+    return (uint64_t)(all * w);
   }
 };
 
@@ -251,23 +320,9 @@ struct Logits {
   // Every token once, for what takes long: f(logit, token).
   template <typename F>
   __device__ __forceinline__ void walk(const F& f) const {
-    uint4 r[kBatch];
-    int64_t v = v0 + threadIdx.x;
-    const auto fetch = [&](int64_t from) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) r[i] = KEEP ? kept[i] : load(from + i * kSmThreads);
-    };
-    fetch(v);
-#pragma unroll 1
-    for (; v < v1; v += kBatch * kSmThreads) {
-#pragma unroll 1
-      for (int i = 0; i < kBatch; ++i) {
-        one_by_one(r[0], first_token((int)(v + i * kSmThreads)), f);
-#pragma unroll
-        for (int j = 0; j + 1 < kBatch; ++j) r[j] = r[j + 1];
-      }
-      if constexpr (KEEP == 0) fetch(v + kBatch * kSmThreads);
-    }
+    loads([&](const uint4& r, int v) __attribute__((always_inline)) {
+      if (v < v1) one_by_one(r, first_token(v), f);
+    });
     ends(f);
   }
 };
@@ -299,37 +354,31 @@ __device__ __forceinline__ uint64_t of_lane(uint64_t v, int l) {
   return (uint64_t)of_lane((uint32_t)(v >> 32), l) << 32 | of_lane((uint32_t)v, l);
 }
 
-// A value that all threads have alike, taken into scalar registers.
-__device__ __forceinline__ uint32_t alike(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int32_t alike(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ uint64_t alike(uint64_t v) {
-  return (uint64_t)alike((uint32_t)(v >> 32)) << 32 | alike((uint32_t)v);
-}
-__device__ __forceinline__ float alike(float v) { return __uint_as_float(alike(__float_as_uint(v))); }
-
-// Sums up to and with each thread's; the total in `total`.
+// Sums up to and with each lane's, of its row of 16.
 template <typename V>
-__device__ __forceinline__ V block_prefix(V v, V* waves, V& total) {
-  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+__device__ __forceinline__ V row_prefix(V v) {
   v += lanes_below<1>(v);
   v += lanes_below<2>(v);
   v += lanes_below<4>(v);
   v += lanes_below<8>(v);
+  return v;
+}
+
+// Sums up to and with each thread's; the total in `total`.
+template <typename V>
+__device__ __forceinline__ V block_prefix(V v, V* waves, V& total) {
+  static_assert(kSmWaves == 16, "a row of lanes adds up the waves");
+  const int lane = threadIdx.x & (kWave - 1), w = alike((int)threadIdx.x / kWave);
+  v = row_prefix(v);
   const V a = of_lane(v, 15), b = a + of_lane(v, 31), c = b + of_lane(v, 47), all = c + of_lane(v, 63);
   const int row = lane >> 4;
   v += row == 0 ? 0 : row == 1 ? a : row == 2 ? b : c;
   __syncthreads();   // the last sums have been read
   if (lane == 0) waves[w] = all;
   __syncthreads();
-  V before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kSmWaves; ++i) {
-    const V o = waves[i];
-    if (i < w) before += o;
-    total += o;
-  }
-  return v + before;
+  const V upto = row_prefix(waves[lane & 15]);
+  total = of_lane(upto, 15);
+  return v + (w > 0 ? of_lane(upto, w - 1) : 0);
 }
 
 // The place in the row's order that is looked for: the smallest n with n >=
@@ -385,38 +434,32 @@ struct Row {
     return least_key([&](uint32_t k) { return scale.bin(unordered(k)) <= b; });
   }
 
-  // Counts, and weights if they are wanted, by `where` (a bin, or none for
-  // kSmBins and above) of the tokens, up to and with each bin.
+  // The words of tokens in `where(logit, bin)` (none: kSmBins and above).
   template <typename Where>
-  __device__ void histogram(int at, bool weights, const Where& where) {
-    fill(at, weights, where);
-    sum_up(at);
-  }
-  template <typename Where>
-  __device__ void fill(int at, bool weights, const Where& where) {
+  __device__ __forceinline__ void fill(int at, bool weights, const Where& where) {
     const int tid = threadIdx.x;
     __syncthreads();
-    s.count[at][tid] = 0;
     s.mass[at][tid] = 0;
     __syncthreads();
     logits.walk([&](float x, int) __attribute__((always_inline)) {
       if (!(x > -__builtin_inff())) return;
-      const uint32_t b = where(x);
+      double place, middle;
+      const uint32_t b = where(x, scale.bin(x, place, middle));
       if (b >= kSmBins) return;
-      atomicAdd(&s.count[at][b], 1u);
-      if (weights) {
-        const uint64_t q = scale.weight(x);
-        if (q) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[at][b]), (unsigned long long)q);
-      }
+      const uint64_t word = weights ? scale.one(place, middle) : scale.one();
+      atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[at][b]), (unsigned long long)word);
     });
     __syncthreads();
   }
-  __device__ void sum_up(int at) {
+  // Words into counts and weights up to and with each bin.  The tokens are
+  // those of bin `only`, or each of the bin that its place names.
+  __device__ __forceinline__ void sum_up(int at, bool weights, uint32_t only = kSmBins) {
     const int tid = threadIdx.x;
+    const uint64_t word = s.mass[at][tid];
     uint32_t all;
     uint64_t all_mass;
-    const uint32_t n = block_prefix(s.count[at][tid], s.wave_count, all);
-    const uint64_t m = block_prefix(s.mass[at][tid], s.wave_mass, all_mass);
+    const uint32_t n = block_prefix(scale.count_of(word), s.wave_count, all);
+    const uint64_t m = weights ? block_prefix(scale.mass_of(word, only < kSmBins ? only : tid), s.wave_mass, all_mass) : 0;
     s.count[at][tid] = n;
     s.mass[at][tid] = m;
     __syncthreads();
@@ -487,16 +530,16 @@ struct Row {
   }
 
   // Values that no logit of bin b is below, or above: the bin's edges with
-  // room for the roundings of a distance and its product.
+  // room for the roundings of a place.
   __device__ __forceinline__ float floor_of(uint32_t b) const {
-    if (b + 1 >= kSmBins || !(scale.inv > 0.0f) || !(scale.m < __builtin_inff())) return -3.4028234e38f;
-    const float d = (float)(b + 1) / scale.inv;
-    return __builtin_fmaxf(scale.m - d - (__builtin_fabsf(scale.m) + d) * 0x1p-20f, -3.4028234e38f);
+    if (b + 1 >= kSmBins || !(scale.inv > 0.0) || scale.m > 1e50) return -3.4028234e38f;
+    const double d = ((double)b + 0.5) / scale.inv, x = scale.m - d - (__builtin_fabs(scale.m) + d) * 0x1p-20;
+    return x > -3.4e38 ? (float)x : -3.4028234e38f;
   }
   __device__ __forceinline__ float ceiling_of(uint32_t b) const {
-    if (b == 0 || !(scale.inv > 0.0f) || !(scale.m < __builtin_inff())) return scale.m;
-    const float d = (float)b / scale.inv;
-    return __builtin_fminf(scale.m - d + (__builtin_fabsf(scale.m) + d) * 0x1p-20f, scale.m);
+    if (b == 0 || !(scale.inv > 0.0) || scale.m > 1e50) return unordered(top);
+    const double d = ((double)b - 0.5) / scale.inv, x = scale.m - d + (__builtin_fabs(scale.m) + d) * 0x1p-20;
+    return __builtin_fminf(x < 3.4e38 ? (float)x : __builtin_inff(), unordered(top));
   }
 
   // The tokens of these bits and bins (no more than the list holds) into the
@@ -524,11 +567,12 @@ struct Row {
       if (at < kQueue) queue[at] = v;
     });
     __syncthreads();
-    if (s.queued <= kQueue) {
+    constexpr bool kRoom = KEEP > 0 && KEEP * kSmThreads <= kQueue;   // for all of a row
+    if (kRoom || s.queued <= kQueue) {
       logits.ends(take);
 #pragma unroll 1
       for (int e = tid; e < s.queued; e += kSmThreads) logits.one_by_one(logits.load(queue[e]), logits.first_token(queue[e]), take);
-    } else {   // more that may than room to note it
+    } else if constexpr (!kRoom) {   // more that may than room to note it
       logits.walk(take);
     }
     __syncthreads();
@@ -643,10 +687,11 @@ struct Row {
     while (n > kSmCap && from < to) {   // too many: by their bits
       int shift = 0;
       while ((to - from) >> shift >= kSmBins) ++shift;
-      histogram(1, true, [&](float x) {
+      fill(1, true, [&](float x, uint32_t in) __attribute__((always_inline)) {
         const uint32_t k = ordered(x);
-        return k < from || k > to ? kSmBins : (to - k) >> shift;
+        return in != first || k < from || k > to ? kSmBins : (to - k) >> shift;
       });
+      sum_up(1, true, first);
       b = by == By::kKey ? (to - (uint32_t)goal) >> shift : bin_of(1, by, goal, n0, m0);
       const uint32_t nb = b ? alike(s.count[1][b - 1]) : 0;
       n = alike(s.count[1][b]) - nb;
@@ -660,7 +705,8 @@ struct Row {
       return in_list(by, goal);
     }
     const uint64_t q = scale.weight(unordered(to));   // n tokens of one value
-    const uint32_t r = by == By::kCount ? (uint32_t)goal - n0 : by == By::kKey ? n : (uint32_t)((goal - m0 + q - 1) / q);
+    const uint64_t by_mass = q ? (goal - m0 + q - 1) / q : n;
+    const uint32_t r = by == By::kCount ? (uint32_t)goal - n0 : by == By::kKey || by_mass > n ? n : by_mass ? (uint32_t)by_mass : 1;
     return Place{n0 + r, m0 + r * q, to, nth_equal(to, r)};
   }
 };
@@ -680,12 +726,6 @@ struct Settings {
       low = 0.0f;
     }
     few = k > 0 && k <= kSmCap / 2;
-  }
-  // Bins reach to where weights are zero, or as far as the row does.
-  __device__ __forceinline__ RowScale scale(float most, float least, int bits) const {
-    const float far = __builtin_fminf(temperature * (float)((bits + 1) * 0.6931472), most - least);
-    return RowScale{most, 1.4426950408889634 / (double)temperature,
-                    far > 0.0f ? __builtin_fminf(kSmBins / far, 3.0e38f) : 0.0f, bits};
   }
 };
 
@@ -745,10 +785,9 @@ __global__ __launch_bounds__(kSmThreads) void k_sample_bins(SampleArgs a) {
   if (range.x == -__builtin_inff()) return;
   const Logits<T, 0> logits(a, t, seg);
   const Settings set(a, t);
-  Row<T, 0> row{a, t, s, logits, set.scale(range.x, range.y, a.bits), ordered(range.x)};
-  row.fill(0, !set.few, [&](float x) __attribute__((always_inline)) { return row.scale.bin(x); });
-  a.counts[(size_t)blockIdx.x * kSmBins + tid] = s.count[0][tid];
-  if (!set.few) a.masses[(size_t)blockIdx.x * kSmBins + tid] = s.mass[0][tid];
+  Row<T, 0> row{a, t, s, logits, RowScale(range.x, range.y, set.temperature, a), ordered(range.x)};
+  row.fill(0, !set.few, [](float, uint32_t b) { return b; });
+  a.words[(size_t)blockIdx.x * kSmBins + tid] = s.mass[0][tid];
 }
 
 // The choice.  PIECES: the pieces' histograms are there.
@@ -768,37 +807,38 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
     return;
   }
   const Settings set(a, t);
-  Row<T, KEEP> row{a, t, s, logits, set.scale(most, least, a.bits), ordered(most)};
+  Row<T, KEEP> row{a, t, s, logits, RowScale(most, least, set.temperature, a), ordered(most)};
+  bool weights = !set.few;
+  uint32_t live = 0;
   if constexpr (PIECES) {
-    uint32_t counts[kSmPieces], count = 0;
-    uint64_t masses[kSmPieces], mass = 0;
+    uint64_t words[kSmPieces], word = 0;
 #pragma unroll
-    for (int i = 0; i < kSmPieces; ++i) {   // all of them on their way at once
-      const size_t at = ((size_t)t * a.segs + (i < a.segs ? i : 0)) * kSmBins + tid;
-      counts[i] = a.counts[at];
-      masses[i] = set.few ? 0 : a.masses[at];
-    }
+    for (int i = 0; i < kSmPieces; ++i)   // all of them on their way at once
+      words[i] = a.words[((size_t)t * a.segs + (i < a.segs ? i : 0)) * kSmBins + tid];
 #pragma unroll
-    for (int i = 0; i < kSmPieces; ++i) {
-      count += i < a.segs ? counts[i] : 0;
-      mass += i < a.segs ? masses[i] : 0;
-    }
-    s.count[0][tid] = count;
-    s.mass[0][tid] = mass;
+    for (int i = 0; i < kSmPieces; ++i) word += i < a.segs ? words[i] : 0;
+    s.mass[0][tid] = word;
     __syncthreads();
-    row.sum_up(0);
   } else {
-    row.histogram(0, !set.few, [&](float x) __attribute__((always_inline)) { return row.scale.bin(x); });
+    row.fill(0, weights, [](float, uint32_t b) { return b; });
+  }
+#pragma unroll 1
+  for (;;) {
+    row.sum_up(0, weights);
+    live = alike(s.count[0][kSmBins - 1]);
+    if (weights) break;
+    // more equal ones than the list holds: weights after all
+    const uint32_t want = set.k < live ? (uint32_t)set.k : live;
+    if (alike(s.count[0][row.bin_of(0, By::kCount, want, 0, 0)]) <= kSmCap) break;
+    weights = true;
+    row.fill(0, true, [](float, uint32_t b) { return b; });
   }
   const int64_t k = set.k;
-  const uint32_t live = alike(s.count[0][kSmBins - 1]);
-  if (set.few) {   // more equal ones than the list holds: weights after all
-    const uint32_t want = k < live ? (uint32_t)k : live;
-    if (alike(s.count[0][row.bin_of(0, By::kCount, want, 0, 0)]) > kSmCap)
-      row.histogram(0, true, [&](float x) __attribute__((always_inline)) { return row.scale.bin(x); });
-  }
   // The places that cut the order, then the one that is drawn, by one copy of
-  // the search.
+  // the search.  (What long functions need is taken before: the compiler would
+  // keep their constants in registers throughout.)
+  double bound = 0.0;
+  if (set.low > 0.0f) bound = log((double)set.low) * (double)set.temperature;
   Place cut{live, alike(s.mass[0][kSmBins - 1]), ordered(least), -1}, drawn = cut;
 #pragma unroll 1
   for (int step = 0; step < 4; ++step) {
@@ -811,10 +851,9 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
       const double at = __builtin_ceil((double)set.p * (double)cut.mass);
       goal = at < 1.0 ? 1 : at >= (double)cut.mass ? cut.mass : (uint64_t)at;
     } else if (step == 2 && set.low > 0.0f) {
-      const double bound = log((double)set.low);   // the least bits that pass
       const uint32_t key = row.least_key([&](uint32_t key) __attribute__((always_inline)) {
         const float x = unordered(key);
-        return x == most || ((double)x - (double)most) / (double)set.temperature >= bound;
+        return x == most || (double)x - (double)most >= bound;
       });
       by = By::kKey;
       goal = cut.key < key ? key : 0;
@@ -832,7 +871,7 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
     if (a.kept) a.kept[t] = (int32_t)cut.n;
     if (a.logprob) {
       const float x = unordered(drawn.key);
-      const double d = x == most ? 0.0 : ((double)x - (double)most) / (double)set.temperature;
+      const double d = (RowScale::above(x) - row.scale.m) / (double)set.temperature;
       a.logprob[t] = (float)(d - (log((double)cut.mass) - a.bits * 0.6931471805599453));
     }
   }
@@ -868,7 +907,7 @@ int sample_segments(int64_t tokens, int64_t vocab) { return (int)pieces_of(token
 
 int64_t sample_workspace_bytes(int64_t tokens, int64_t vocab) {
   const int64_t segs = pieces_of(tokens, vocab);
-  return segs == 1 ? 0 : tokens * segs * (int64_t)(sizeof(float2) + kSmBins * (sizeof(uint64_t) + sizeof(uint32_t)));
+  return segs == 1 ? 0 : tokens * segs * (int64_t)(sizeof(float2) + kSmBins * sizeof(uint64_t));
 }
 
 hipError_t launch_sample(const SampleCall& c, hipStream_t stream) {
@@ -876,12 +915,12 @@ hipError_t launch_sample(const SampleCall& c, hipStream_t stream) {
   while (((int64_t)1 << log) < c.vocab) ++log;
   const int segs = (int)pieces_of(c.tokens, c.vocab);
   SampleArgs a{c.logits, c.uniforms, c.temperature, c.top_k, c.top_p, c.min_p, c.ids, c.logprob, c.kept,
-               c.stride, c.tokens, c.vocab, log > 12 ? 62 - log : 50, segs, 0, nullptr, nullptr, nullptr};
+               c.stride, c.tokens, c.vocab, log > 12 ? 62 - log : 50, log > 18 ? 63 - log : 45,
+               log > 18 ? 67 - 2 * log : 31, segs, 0, nullptr, nullptr};
   if (segs > 1) {
     a.per = (int32_t)(((c.vocab + 7) / segs + 8) & ~7);   // a piece starts at a multiple of 16 bytes
-    a.masses = static_cast<uint64_t*>(c.workspace);
-    a.ranges = reinterpret_cast<float2*>(a.masses + (size_t)c.tokens * segs * kSmBins);
-    a.counts = reinterpret_cast<uint32_t*>(a.ranges + (size_t)c.tokens * segs);
+    a.words = static_cast<uint64_t*>(c.workspace);
+    a.ranges = reinterpret_cast<float2*>(a.words + (size_t)c.tokens * segs * kSmBins);
   }
   return c.f32 ? sample_launch<float>(a, stream) : sample_launch<uint16_t>(a, stream);
 }
