@@ -786,7 +786,7 @@ FP8W_API fp8w_status fp8w_linear(const uint16_t* x, int64_t x_stride, int64_t m,
 namespace {
 
 bool sample_shape_ok(int64_t tokens, int64_t vocab) {
-  return tokens >= 0 && tokens <= kMaxDim && vocab >= 1 && vocab <= kMaxDim - 63;
+  return tokens >= 0 && tokens <= kMaxDim && vocab >= 1 && vocab <= fp8w::kMaxSampleVocab;
 }
 
 }  // namespace

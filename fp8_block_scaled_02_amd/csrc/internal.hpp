@@ -225,6 +225,8 @@ struct SampleCall {
   int64_t stride;
   int32_t tokens, vocab, f32;
 };
+// A histogram's word holds a count and a sum of fractions: 19 bits of these are left.
+constexpr int64_t kMaxSampleVocab = 1 << 24;
 int sample_segments(int64_t tokens, int64_t vocab);
 int64_t sample_workspace_bytes(int64_t tokens, int64_t vocab);
 hipError_t launch_sample(const SampleCall& c, hipStream_t stream);

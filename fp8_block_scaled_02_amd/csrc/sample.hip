@@ -13,9 +13,10 @@
 //
 // Weights are whole numbers, 2^S w rounded (S = 62 - ceil(log2 vocab), at most
 // 50), from fp64 exponentials: their sums are the same in any order, so that
-// atomics may add them up, and a choice between two tokens changes with the
-// 2^-45 of a weight's rounding alone.  fp32 would turn over one of some
-// thousand choices among 10^5 tokens.  (fp64 multiply-adds run at the rate of fp32's.)
+// atomics may add them up.  Those of a whole bin are known to 2^-31 of their sum
+// (2^-19 for 2^24 tokens), as RowScale says.  fp32 sums would turn over one
+// choice of some thousand among 10^5 tokens.  (fp64 multiply-adds run at the
+// rate of fp32's.)
 //
 // A row is taken in passes: its largest and smallest logit; a histogram of the
 // distance from the largest, counts and weights; and the tokens of the bins
@@ -23,10 +24,10 @@
 // has room for are divided again by the values' bits, down to a single value,
 // whose tokens differ by their place alone.
 //
-// With rows enough one workgroup does all of it, and keeps a row of up to 64
-// KB of its registers' 128 there from pass to pass (longer ones come out of
-// the caches again).  With fewer the first two passes are launches of their
-// own over pieces of rows, and a third workgroup adds the pieces' histograms.
+// With rows enough one workgroup does all of it, and finds the row in the
+// caches again from pass to pass.  With fewer the first two passes are
+// launches of their own over pieces of rows, and a third adds the pieces'
+// histograms.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -36,11 +37,11 @@
 namespace fp8w {
 namespace {
 
-constexpr int kSmThreads = 1024;
-constexpr int kSmWaves = kSmThreads / kWave;
-constexpr int kSmBins = kSmThreads;   // a thread a bin
+constexpr int kSmThreads = 512;       // of a workgroup that has a row, or a piece of one, to itself
+constexpr int kSmMany = 1024;         // of one that takes up a row from its pieces
+constexpr int kSmBins = 1024;
 constexpr int kSmCap = 2048;          // tokens of a sorted list
-constexpr int kSmSmall = 256;         // of one that is ranked by counting, four threads a token
+constexpr int kSmSmall = 256;         // of one that is ranked by counting
 constexpr int kSmPieces = 16;         // of a row, at most
 constexpr uint32_t kFirstLive = 0x00800000u;   // the ordered bits of the lowest value; -inf is one below
 
@@ -87,19 +88,24 @@ struct SampleArgs {
 // reach to where weights are zero, or as far as the row does.
 //
 // The histogram adds, for each token, one to its bin's count and to the same
-// word the weight relative to that of the bin's middle, less one: |e| < 2^-5,
-// as a whole number of 2^-fraction, so that a bin's weight is that of its
-// middle times (count + sum of e).  An exponential for every token would take
-// twice as long, a second atomic as well.
+// word the weight relative to that of the bin's middle, less one: |e| < 2^-5
+// (a bin is no wider than 62/1023 powers of two), as a whole number of
+// 2^-fraction, so that a bin's weight is that of its middle times (count + sum
+// of e).  Half a unit's rounding and the term left out, |ln2 wide/2|^5 / 120 <
+// 2^-34, make 2^-31 of a weight for up to 2^18 tokens, whose counts leave 31
+// bits of fraction; above, both give up a bit for each doubling.  The sum of e +
+// 2^-5 stays below 2^(fraction - 4) times the count, and so below 2^shift.  An
+// exponential for every token would take twice as long, a second atomic as well.
 struct RowScale {
   double m;            // the largest logit (2^200 for infinity)
   double per;          // log2 e / T
-  double inv, wide;    // bins for each unit of distance; log2 of a bin's weights' ratio
+  double inv, unit;    // bins for each unit of distance, and the distance of one
+  double wide;         // log2 of a bin's weights' ratio
   double c1, c2, c3, c4;   // e of a place in the bin, times 2^fraction
   int bits, shift, fraction;
+  uint32_t bias;           // added to e, so that it is positive: 2^-5
 
   static constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: a sum's low word is its whole part, rounded
-  static constexpr int kBias = 26;                       // 2^kBias is added to e, so that it is positive
 
   __device__ __forceinline__ RowScale(float most, float least, float temperature, const SampleArgs& a) {
     m = above(most);
@@ -107,15 +113,17 @@ struct RowScale {
     bits = a.bits;
     shift = a.shift;
     fraction = a.fraction;
+    bias = 1u << (fraction - 5);
     const double far = __builtin_fmin((double)temperature * ((bits + 12) * 0.6931471805599453), m - above(least));
     inv = far > 0.0 ? __builtin_fmin((kSmBins - 1) / far, 1e300) : 0.0;
-    wide = inv > 0.0 ? per / inv : 0.0;
-    const double w = wide * 0.6931471805599453, unit = __builtin_ldexp(1.0, fraction);
-    c1 = -w * unit;
-    c2 = w * w * (unit / 2);
-    c3 = -w * w * w * (unit / 6);
-    c4 = w * w * w * w * (unit / 24);
-    m = alike(m), per = alike(per), inv = alike(inv), wide = alike(wide);
+    unit = inv > 0.0 ? 1.0 / inv : 0.0;
+    wide = per * unit;
+    const double w = wide * 0.6931471805599453, one = __builtin_ldexp(1.0, fraction);
+    c1 = -w * one;
+    c2 = w * w * (one / 2);
+    c3 = -w * w * w * (one / 6);
+    c4 = w * w * w * w * (one / 24);
+    m = alike(m), per = alike(per), inv = alike(inv), unit = alike(unit), wide = alike(wide);
     c1 = alike(c1), c2 = alike(c2), c3 = alike(c3), c4 = alike(c4);
   }
   static __device__ __forceinline__ double above(float x) { return __builtin_fmin((double)x, 0x1p200); }
@@ -162,40 +170,39 @@ struct RowScale {
     double e = __builtin_fma(c4, d, c3);
     e = __builtin_fma(e, d, c2);
     e = __builtin_fma(e, d, c1);
-    const uint32_t low = (uint32_t)__double_as_longlong(__builtin_fma(e, d, kMagic)) + (1u << kBias);
+    const uint32_t low = (uint32_t)__double_as_longlong(__builtin_fma(e, d, kMagic)) + bias;
     return one() + low;
   }
   // A word's count and, of tokens around the middle of bin b, their weight.
   __device__ __forceinline__ uint32_t count_of(uint64_t word) const { return (uint32_t)(word >> shift); }
   __device__ __forceinline__ uint64_t mass_of(uint64_t word, uint32_t b) const {
     const double count = (double)count_of(word);
-    const double e = (double)(word & (one() - 1)) - count * (double)(1 << kBias);
+    const double e = (double)(word & (one() - 1)) - count * (double)bias;
     const double all = __builtin_fma(e, __builtin_ldexp(1.0, -fraction), count);
     const double w = (double)power(-(double)b * wide);
     return (uint64_t)(all * w);
   }
 };
 
-// A row's logits, or those of one piece of it, as the workgroup's threads read
-// them: 16 bytes at a time, KEEP of them a thread loaded once and kept, or (0)
-// all of them at each pass.
+// A row's logits, or those of one piece of it, as a workgroup of N threads
+// reads them, 16 bytes at a time.  (Rows of up to 64 KB kept in registers from
+// pass to pass were no faster than the caches: 56.4 us for 512 x 32000 both.)
 //
 // A pass's code runs but once or a few times a wave, so its time is that of
 // fetching it: what is done for each value is written out for two values of a
 // load, with the registers moved on under it, not for each of eight (32 copies
 // of the exponential, and a place of the order looked for in five copies,
 // took 50 us where the row had 5000 tokens).
-template <typename T, int KEEP>
+template <typename T, int N>
 struct Logits {
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   static constexpr int kVec = 16 / sizeof(T);
-  static constexpr int kBatch = KEEP ? KEEP : 4;   // loads that leave at once
+  static constexpr int kBatch = 4;   // loads that leave at once
   // Places are counted from the 16-byte boundary at or below the row's start;
   // only 16 bytes that lie in the row are loaded whole.
   const char* base;
   int skew;
   int64_t v0, v1, end, tail;   // whole 16 bytes, and the values behind them
-  uint4 kept[KEEP ? KEEP : 1];
 
   __device__ __forceinline__ Logits(const SampleArgs& a, int t, int seg) {
     const char* row = static_cast<const char*>(a.logits) + (size_t)t * a.stride * sizeof(T);
@@ -215,10 +222,6 @@ struct Logits {
         v0 = lo > v0 ? lo : v0;
         skew |= 0x40000000;   // nor its start
       }
-    }
-    if constexpr (KEEP > 0) {
-#pragma unroll
-      for (int i = 0; i < KEEP; ++i) kept[i] = load(v0 + threadIdx.x + i * kSmThreads);
     }
   }
   // Nothing to see in what is not there: NaN.
@@ -258,12 +261,12 @@ struct Logits {
   __device__ __forceinline__ void loads(const G& g) const {
     const int tid = threadIdx.x;
 #pragma unroll 1
-    for (int64_t v = v0 + tid; v < v1; v += kBatch * kSmThreads) {
+    for (int64_t v = v0 + tid; v < v1; v += kBatch * N) {
       uint4 r[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) r[i] = KEEP ? kept[i] : load(v + i * kSmThreads);
+      for (int i = 0; i < kBatch; ++i) r[i] = load(v + i * N);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) g(r[i], (int)(v + i * kSmThreads));
+      for (int i = 0; i < kBatch; ++i) g(r[i], (int)(v + i * N));
     }
   }
   __device__ __forceinline__ int first_token(int v) const { return v * kVec - (skew & 0xFF); }
@@ -327,17 +330,36 @@ struct Logits {
   }
 };
 
+// The words of the tokens by `where(logit, bin)` (none: kSmBins and above).
+template <typename T, int N, typename Where>
+__device__ __forceinline__ void fill(const Logits<T, N>& logits, const RowScale& scale, uint64_t* words, bool weights,
+                                     const Where& where) {
+  __syncthreads();
+  for (int b = threadIdx.x; b < kSmBins; b += N) words[b] = 0;
+  __syncthreads();
+  logits.walk([&](float x, int) __attribute__((always_inline)) {
+    if (!(x > -__builtin_inff())) return;
+    double place, middle;
+    const uint32_t b = where(x, scale.bin(x, place, middle));
+    if (b >= kSmBins) return;
+    const uint64_t word = weights ? scale.one(place, middle) : scale.one();
+    atomicAdd(reinterpret_cast<unsigned long long*>(&words[b]), (unsigned long long)word);
+  });
+  __syncthreads();
+}
+
+template <int N>
 struct Shared {
   uint64_t list[kSmCap];        // ordered bits, then the token's complement
   uint64_t list_mass[kSmCap];   // weights of the list up to and with each
   uint64_t mass[2][kSmBins];    // of the whole row's bins, of one bin's parts
   uint32_t count[2][kSmBins];
-  int rank[4][kSmSmall];
-  uint64_t wave_mass[kSmWaves];
-  uint32_t wave_count[kSmWaves];
-  float wave_max[kSmWaves], wave_min[kSmWaves];
+  int rank[N / kSmSmall][kSmSmall];
+  uint64_t wave_mass[N / kWave];
+  uint32_t wave_count[N / kWave];
+  float2 wave_range[N / kWave];
   int length, queued;
-  uint32_t found;
+  uint32_t found[2];
 };
 
 // A value from the lane n places below in its row of 16 (0 from none).
@@ -365,9 +387,10 @@ __device__ __forceinline__ V row_prefix(V v) {
 }
 
 // Sums up to and with each thread's; the total in `total`.
-template <typename V>
+template <int N, typename V>
 __device__ __forceinline__ V block_prefix(V v, V* waves, V& total) {
-  static_assert(kSmWaves == 16, "a row of lanes adds up the waves");
+  constexpr int kWaves = N / kWave;
+  static_assert(kWaves <= 16, "a row of lanes adds up the waves");
   const int lane = threadIdx.x & (kWave - 1), w = alike((int)threadIdx.x / kWave);
   v = row_prefix(v);
   const V a = of_lane(v, 15), b = a + of_lane(v, 31), c = b + of_lane(v, 47), all = c + of_lane(v, 63);
@@ -376,8 +399,8 @@ __device__ __forceinline__ V block_prefix(V v, V* waves, V& total) {
   __syncthreads();   // the last sums have been read
   if (lane == 0) waves[w] = all;
   __syncthreads();
-  const V upto = row_prefix(waves[lane & 15]);
-  total = of_lane(upto, 15);
+  const V upto = row_prefix(waves[lane & (kWaves - 1)]);
+  total = of_lane(upto, kWaves - 1);
   return v + (w > 0 ? of_lane(upto, w - 1) : 0);
 }
 
@@ -394,12 +417,13 @@ struct Place {
 };
 
 // One workgroup's view of its row.
-template <typename T, int KEEP>
+template <typename T, int N>
 struct Row {
+  static constexpr int kPer = kSmBins / N;   // neighbouring bins of a thread
   const SampleArgs& a;
   const int t;
-  Shared& s;
-  const Logits<T, KEEP>& logits;
+  Shared<N>& s;
+  const Logits<T, N>& logits;
   RowScale scale;
   uint32_t top;             // ordered bits of the largest
   // what s.list holds: the tokens of these bits and these bins, and what
@@ -434,66 +458,71 @@ struct Row {
     return least_key([&](uint32_t k) { return scale.bin(unordered(k)) <= b; });
   }
 
-  // The words of tokens in `where(logit, bin)` (none: kSmBins and above).
-  template <typename Where>
-  __device__ __forceinline__ void fill(int at, bool weights, const Where& where) {
-    const int tid = threadIdx.x;
-    __syncthreads();
-    s.mass[at][tid] = 0;
-    __syncthreads();
-    logits.walk([&](float x, int) __attribute__((always_inline)) {
-      if (!(x > -__builtin_inff())) return;
-      double place, middle;
-      const uint32_t b = where(x, scale.bin(x, place, middle));
-      if (b >= kSmBins) return;
-      const uint64_t word = weights ? scale.one(place, middle) : scale.one();
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[at][b]), (unsigned long long)word);
-    });
-    __syncthreads();
-  }
   // Words into counts and weights up to and with each bin.  The tokens are
   // those of bin `only`, or each of the bin that its place names.
   __device__ __forceinline__ void sum_up(int at, bool weights, uint32_t only = kSmBins) {
     const int tid = threadIdx.x;
-    const uint64_t word = s.mass[at][tid];
-    uint32_t all;
-    uint64_t all_mass;
-    const uint32_t n = block_prefix(scale.count_of(word), s.wave_count, all);
-    const uint64_t m = weights ? block_prefix(scale.mass_of(word, only < kSmBins ? only : tid), s.wave_mass, all_mass) : 0;
-    s.count[at][tid] = n;
-    s.mass[at][tid] = m;
+    uint32_t n[kPer], all, count = 0;
+    uint64_t m[kPer], all_mass, mass = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int b = tid * kPer + j;
+      const uint64_t word = s.mass[at][b];
+      count += n[j] = scale.count_of(word);
+      mass += m[j] = weights ? scale.mass_of(word, only < kSmBins ? only : b) : 0;
+    }
+    count = block_prefix<N>(count, s.wave_count, all);
+    mass = weights ? block_prefix<N>(mass, s.wave_mass, all_mass) : 0;
+#pragma unroll
+    for (int j = kPer - 1; j >= 0; --j) {
+      const int b = tid * kPer + j;
+      s.count[at][b] = count;
+      s.mass[at][b] = mass;
+      count -= n[j];
+      mass -= m[j];
+    }
     __syncthreads();
   }
 
-  // The first bin that reaches the goal, with `n0` and `m0` before them all.
-  __device__ uint32_t bin_of(int at, By by, uint64_t goal, uint32_t n0, uint64_t m0) {
-    const int tid = threadIdx.x;
-    const uint64_t upto = by == By::kCount ? n0 + s.count[at][tid] : m0 + s.mass[at][tid];
-    const uint64_t less = tid == 0 ? (by == By::kCount ? n0 : m0) : by == By::kCount ? n0 + s.count[at][tid - 1] : m0 + s.mass[at][tid - 1];
-    if (tid == 0) s.found = kSmBins - 1;
+  // One of the words by which a thread tells the others what it found: in
+  // turn, so that a barrier lies between the last look at it and its next use.
+  int turn = 0;
+  __device__ __forceinline__ uint32_t& answer() { return s.found[turn ^= 1]; }
+
+  // The first bin that reaches the goal, which one does, with `n0` and `m0`
+  // before them all.
+  __device__ __forceinline__ uint32_t bin_of(int at, By by, uint64_t goal, uint32_t n0, uint64_t m0) {
+    const int first = threadIdx.x * kPer;
+    uint32_t& found = answer();
+    const auto upto = [&](int b) { return b < 0 ? (by == By::kCount ? n0 : m0) : by == By::kCount ? n0 + s.count[at][b] : m0 + s.mass[at][b]; };
+    uint64_t less = upto(first - 1);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint64_t now = upto(first + j);
+      if ((less < goal && now >= goal) || (first + j == kSmBins - 1 && now < goal)) found = first + j;
+      less = now;
+    }
     __syncthreads();
-    if (less < goal && upto >= goal) s.found = tid;
-    __syncthreads();
-    const uint32_t b = alike(s.found);
-    __syncthreads();
-    return b;
+    return alike(found);
   }
 
   // The list in order, larger first: each key's place is the number of larger
-  // ones, counted by four threads.
-  __device__ void rank_list(int n) {
+  // ones, counted by a few threads.
+  __device__ __forceinline__ void rank_list(int n) {
+    constexpr int kParts = N / kSmSmall;
     const int tid = threadIdx.x, e = tid % kSmSmall, part = tid / kSmSmall;
-    static_assert(kSmThreads == 4 * kSmSmall, "four threads a token");
     const uint64_t key = e < n ? s.list[e] : 0;
-    const int per = (n + 3) / 4, last = min((part + 1) * per, n);
+    const int per = (n + kParts - 1) / kParts, last = min((part + 1) * per, n);
     int rank = 0;
-    if (e < n) {
-#pragma unroll 4
-      for (int j = part * per; j < last; ++j) rank += s.list[j] > key ? 1 : 0;
-    }
+#pragma unroll 8
+    for (int j = part * per; j < last; ++j) rank += s.list[j] > key ? 1 : 0;
     s.rank[part][e] = rank;
     __syncthreads();
-    if (part == 0 && e < n) s.list[s.rank[0][e] + s.rank[1][e] + s.rank[2][e] + s.rank[3][e]] = key;
+    if (part == 0 && e < n) {
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) rank += s.rank[i][e];
+      s.list[rank] = key;
+    }
     __syncthreads();
   }
 
@@ -503,15 +532,17 @@ struct Row {
     const int tid = threadIdx.x;
     int size = 2 * kSmSmall;
     while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kSmThreads) s.list[i] = 0;
+    for (int i = n + tid; i < size; i += N) s.list[i] = 0;
     __syncthreads();
     const auto step = [&](int k, int j) {
-      if (tid >= size / 2) return;
-      const int i = 2 * tid - (tid & (j - 1));   // bit j clear
-      const uint64_t x = s.list[i], y = s.list[i + j];
-      if ((x < y) == ((i & k) == 0)) {
-        s.list[i] = y;
-        s.list[i + j] = x;
+#pragma unroll 1
+      for (int p = tid; p < size / 2; p += N) {
+        const int i = 2 * p - (p & (j - 1));   // bit j clear
+        const uint64_t x = s.list[i], y = s.list[i + j];
+        if ((x < y) == ((i & k) == 0)) {
+          s.list[i] = y;
+          s.list[i + j] = x;
+        }
       }
     };
     for (int k = 2; k <= size; k *= 2) {
@@ -533,12 +564,12 @@ struct Row {
   // room for the roundings of a place.
   __device__ __forceinline__ float floor_of(uint32_t b) const {
     if (b + 1 >= kSmBins || !(scale.inv > 0.0) || scale.m > 1e50) return -3.4028234e38f;
-    const double d = ((double)b + 0.5) / scale.inv, x = scale.m - d - (__builtin_fabs(scale.m) + d) * 0x1p-20;
+    const double d = ((double)b + 0.5) * scale.unit, x = scale.m - d - (__builtin_fabs(scale.m) + d) * 0x1p-20;
     return x > -3.4e38 ? (float)x : -3.4028234e38f;
   }
   __device__ __forceinline__ float ceiling_of(uint32_t b) const {
     if (b == 0 || !(scale.inv > 0.0) || scale.m > 1e50) return unordered(top);
-    const double d = ((double)b - 0.5) / scale.inv, x = scale.m - d + (__builtin_fabs(scale.m) + d) * 0x1p-20;
+    const double d = ((double)b - 0.5) * scale.unit, x = scale.m - d + (__builtin_fabs(scale.m) + d) * 0x1p-20;
     return __builtin_fminf(x < 3.4e38 ? (float)x : __builtin_inff(), unordered(top));
   }
 
@@ -552,7 +583,7 @@ struct Row {
     __syncthreads();
     if (tid == 0) s.length = s.queued = 0;
     __syncthreads();
-    const typename Logits<T, KEEP>::Band band(alike(__builtin_fmaxf(unordered(from), floor_of(b1))),
+    const typename Logits<T, N>::Band band(alike(__builtin_fmaxf(unordered(from), floor_of(b1))),
                                               alike(__builtin_fminf(unordered(to), ceiling_of(b0))));
     const auto take = [&](float x, int id) __attribute__((always_inline)) {
       if (!(x >= band.lo && x <= band.hi)) return;   // NaN and -inf too
@@ -567,12 +598,11 @@ struct Row {
       if (at < kQueue) queue[at] = v;
     });
     __syncthreads();
-    constexpr bool kRoom = KEEP > 0 && KEEP * kSmThreads <= kQueue;   // for all of a row
-    if (kRoom || s.queued <= kQueue) {
+    if (s.queued <= kQueue) {
       logits.ends(take);
 #pragma unroll 1
-      for (int e = tid; e < s.queued; e += kSmThreads) logits.one_by_one(logits.load(queue[e]), logits.first_token(queue[e]), take);
-    } else if constexpr (!kRoom) {   // more that may than room to note it
+      for (int e = tid; e < s.queued; e += N) logits.one_by_one(logits.load(queue[e]), logits.first_token(queue[e]), take);
+    } else {   // more that may than room to note it
       logits.walk(take);
     }
     __syncthreads();
@@ -581,13 +611,20 @@ struct Row {
       rank_list(n);
     else
       sort_list(n);
-    const int i0 = 2 * tid, i1 = 2 * tid + 1;
-    const uint64_t q0 = i0 < n ? scale.weight(unordered((uint32_t)(s.list[i0] >> 32))) : 0;
-    const uint64_t q1 = i1 < n ? scale.weight(unordered((uint32_t)(s.list[i1] >> 32))) : 0;
-    uint64_t all;
-    const uint64_t upto = block_prefix(q0 + q1, s.wave_mass, all);
-    if (i0 < n) s.list_mass[i0] = m0 + upto - q1;
-    if (i1 < n) s.list_mass[i1] = m0 + upto;
+    // weights up to and with each token: a thread takes some neighbours
+    constexpr int kSome = kSmCap / N;
+    const int some = n <= N ? 1 : kSome, first = tid * some;
+    uint64_t mine = 0, all;
+#pragma unroll 1
+    for (int j = 0; j < some; ++j)
+      if (first + j < n) {
+        mine += scale.weight(unordered((uint32_t)(s.list[first + j] >> 32)));
+        s.list_mass[first + j] = mine;
+      }
+    const uint64_t less = m0 + block_prefix<N>(mine, s.wave_mass, all) - mine;
+#pragma unroll 1
+    for (int j = 0; j < some; ++j)
+      if (first + j < n) s.list_mass[first + j] += less;
     __syncthreads();
     lo = from;
     hi = to;
@@ -610,22 +647,29 @@ struct Row {
     }
   }
 
-  // The goal's place within the list.
-  __device__ Place in_list(By by, uint64_t goal) {
+  // The goal's place within the list (its last token's, where sums that were
+  // rounded otherwise fall short of the goal).
+  __device__ __forceinline__ Place in_list(By by, uint64_t goal) {
     const int tid = threadIdx.x;
-    if (tid == 0) s.found = by == By::kKey ? 0 : length;
-    __syncthreads();
-    for (uint32_t i = tid; i < length; i += kSmThreads) {
-      if (by == By::kKey) {
-        const bool here = (s.list[i] >> 32) >= goal, next = i + 1 < length && (s.list[i + 1] >> 32) >= goal;
-        if (here && !next) s.found = i + 1;
-      } else if (by == By::kMass) {
-        if (s.list_mass[i] >= goal && (i == 0 || s.list_mass[i - 1] < goal)) s.found = i + 1;
+    uint32_t n = (uint32_t)goal - before;
+    if (by != By::kCount) {
+      uint32_t& found = answer();
+      if (tid == 0 && length == 0) found = 0;
+#pragma unroll 1
+      for (uint32_t i = tid; i < length; i += N) {
+        const bool last = i + 1 == length;
+        if (by == By::kKey) {
+          const bool here = (s.list[i] >> 32) >= goal;
+          if (here && (last || (s.list[i + 1] >> 32) < goal)) found = i + 1;
+          if (i == 0 && !here) found = 0;
+        } else {
+          const bool reached = s.list_mass[i] >= goal;
+          if ((reached || last) && (i == 0 || s.list_mass[i - 1] < goal)) found = i + 1;
+        }
       }
+      __syncthreads();
+      n = alike(found);
     }
-    __syncthreads();
-    const uint32_t n = by == By::kCount ? (uint32_t)goal - before : alike(s.found);
-    __syncthreads();
     if (n == 0) return Place{before, before_mass, top, -1};
     const uint64_t e = alike(s.list[n - 1]);
     return Place{before + n, alike(s.list_mass[n - 1]), (uint32_t)(e >> 32), (int32_t)~(uint32_t)e};
@@ -634,7 +678,7 @@ struct Row {
   // The n-th token, by place in the row, of those with these bits.
   __device__ int32_t nth_equal(uint32_t key, uint32_t n) {
     const int tid = threadIdx.x;
-    const int per = (a.vocab + kSmThreads - 1) / kSmThreads;
+    const int per = (a.vocab + N - 1) / N;
     const int64_t first = (int64_t)tid * per, last = min(first + per, (int64_t)a.vocab);
     const char* row = static_cast<const char*>(a.logits) + (size_t)t * a.stride * sizeof(T);
     const auto is = [&](int64_t i) {
@@ -647,20 +691,17 @@ struct Row {
     };
     uint32_t mine = 0, all;
     for (int64_t i = first; i < last; ++i) mine += is(i) ? 1 : 0;
-    const uint32_t upto = block_prefix(mine, s.wave_count, all);
-    if (tid == 0) s.found = 0;
-    __syncthreads();
+    const uint32_t upto = block_prefix<N>(mine, s.wave_count, all);
+    uint32_t& found = answer();
     if (mine && upto - mine < n && upto >= n) {
       uint32_t left = n - (upto - mine);
       int64_t i = first;
       for (; i < last; ++i)
         if (is(i) && --left == 0) break;
-      s.found = (uint32_t)i;
+      found = (uint32_t)i;
     }
     __syncthreads();
-    const int32_t id = alike((int32_t)s.found);
-    __syncthreads();
-    return id;
+    return (int32_t)alike(found);
   }
 
   // The goal's place, which the row has.  The histogram holds weights if
@@ -687,7 +728,7 @@ struct Row {
     while (n > kSmCap && from < to) {   // too many: by their bits
       int shift = 0;
       while ((to - from) >> shift >= kSmBins) ++shift;
-      fill(1, true, [&](float x, uint32_t in) __attribute__((always_inline)) {
+      fill(logits, scale, s.mass[1], true, [&](float x, uint32_t in) __attribute__((always_inline)) {
         const uint32_t k = ordered(x);
         return in != first || k < from || k > to ? kSmBins : (to - k) >> shift;
       });
@@ -730,8 +771,8 @@ struct Settings {
 };
 
 // The largest and smallest live logit, in every thread.
-template <typename T, int KEEP>
-__device__ __forceinline__ float2 range_of(const Logits<T, KEEP>& logits, Shared& s) {
+template <typename T, int N>
+__device__ __forceinline__ float2 range_of(const Logits<T, N>& logits, float2* waves) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   float most = -__builtin_inff(), least = __builtin_inff();
   const auto take = [&](float x) __attribute__((always_inline)) {
@@ -745,15 +786,12 @@ __device__ __forceinline__ float2 range_of(const Logits<T, KEEP>& logits, Shared
     most = __builtin_fmaxf(most, __shfl_xor(most, off));
     least = __builtin_fminf(least, __shfl_xor(least, off));
   }
-  if (lane == 0) {
-    s.wave_max[tid / kWave] = most;
-    s.wave_min[tid / kWave] = least;
-  }
+  if (lane == 0) waves[tid / kWave] = make_float2(most, least);
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kSmWaves; ++w) {
-    most = __builtin_fmaxf(most, s.wave_max[w]);
-    least = __builtin_fminf(least, s.wave_min[w]);
+  for (int w = 0; w < N / kWave; ++w) {
+    most = __builtin_fmaxf(most, waves[w].x);
+    least = __builtin_fminf(least, waves[w].y);
   }
   return make_float2(alike(most), alike(least));
 }
@@ -770,33 +808,37 @@ __device__ __forceinline__ float2 joined_range(const SampleArgs& a, int t) {
 
 template <typename T>
 __global__ __launch_bounds__(kSmThreads) void k_sample_range(SampleArgs a) {
-  __shared__ Shared s;
+  __shared__ float2 waves[kSmThreads / kWave];
   const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs;
-  const Logits<T, 0> logits(a, t, seg);
-  const float2 r = range_of(logits, s);
+  const Logits<T, kSmThreads> logits(a, t, seg);
+  const float2 r = range_of(logits, waves);
   if (threadIdx.x == 0) a.ranges[blockIdx.x] = r;
 }
 
 template <typename T>
 __global__ __launch_bounds__(kSmThreads) void k_sample_bins(SampleArgs a) {
-  __shared__ Shared s;
-  const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs, tid = threadIdx.x;
+  __shared__ uint64_t words[kSmBins];
+  const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs;
   const float2 range = joined_range(a, t);
   if (range.x == -__builtin_inff()) return;
-  const Logits<T, 0> logits(a, t, seg);
+  const Logits<T, kSmThreads> logits(a, t, seg);
   const Settings set(a, t);
-  Row<T, 0> row{a, t, s, logits, RowScale(range.x, range.y, set.temperature, a), ordered(range.x)};
-  row.fill(0, !set.few, [](float, uint32_t b) { return b; });
-  a.words[(size_t)blockIdx.x * kSmBins + tid] = s.mass[0][tid];
+  const RowScale scale(range.x, range.y, set.temperature, a);
+  fill(logits, scale, words, !set.few, [](float, uint32_t b) { return b; });
+  for (int b = threadIdx.x; b < kSmBins; b += kSmThreads) a.words[(size_t)blockIdx.x * kSmBins + b] = words[b];
 }
 
-// The choice.  PIECES: the pieces' histograms are there.
-template <typename T, int KEEP, bool PIECES>
-__global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
-  __shared__ Shared s;
+// The choice.  PIECES: the pieces' histograms are there, and the rows are few.
+// Whole rows are taken by two workgroups a CU, of which one computes while the
+// other waits (1024 x 32000 fp32 93 us, 118 with one of twice the threads);
+// few rows by one of many threads (64 x 151936 40 us, 46 with half of them).
+template <typename T, int N, bool PIECES>
+__global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
+  constexpr int kPer = kSmBins / N;
+  __shared__ Shared<N> s;
   const int t = blockIdx.x, tid = threadIdx.x;
-  const Logits<T, KEEP> logits(a, t, -1);
-  const float2 range = PIECES ? joined_range(a, t) : range_of(logits, s);
+  const Logits<T, N> logits(a, t, -1);
+  const float2 range = PIECES ? joined_range(a, t) : range_of(logits, s.wave_range);
   const float most = range.x, least = range.y;
   if (most == -__builtin_inff()) {   // masked throughout
     if (tid == 0) {
@@ -807,20 +849,24 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
     return;
   }
   const Settings set(a, t);
-  Row<T, KEEP> row{a, t, s, logits, RowScale(most, least, set.temperature, a), ordered(most)};
+  Row<T, N> row{a, t, s, logits, RowScale(most, least, set.temperature, a), ordered(most)};
   bool weights = !set.few;
   uint32_t live = 0;
   if constexpr (PIECES) {
-    uint64_t words[kSmPieces], word = 0;
 #pragma unroll
-    for (int i = 0; i < kSmPieces; ++i)   // all of them on their way at once
-      words[i] = a.words[((size_t)t * a.segs + (i < a.segs ? i : 0)) * kSmBins + tid];
+    for (int j = 0; j < kPer; ++j) {
+      const int b = tid + j * N;
+      uint64_t words[kSmPieces], word = 0;
 #pragma unroll
-    for (int i = 0; i < kSmPieces; ++i) word += i < a.segs ? words[i] : 0;
-    s.mass[0][tid] = word;
+      for (int i = 0; i < kSmPieces; ++i)   // all of them on their way at once
+        words[i] = a.words[((size_t)t * a.segs + (i < a.segs ? i : 0)) * kSmBins + b];
+#pragma unroll
+      for (int i = 0; i < kSmPieces; ++i) word += i < a.segs ? words[i] : 0;
+      s.mass[0][b] = word;
+    }
     __syncthreads();
   } else {
-    row.fill(0, weights, [](float, uint32_t b) { return b; });
+    fill(logits, row.scale, s.mass[0], weights, [](float, uint32_t b) { return b; });
   }
 #pragma unroll 1
   for (;;) {
@@ -831,7 +877,7 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
     const uint32_t want = set.k < live ? (uint32_t)set.k : live;
     if (alike(s.count[0][row.bin_of(0, By::kCount, want, 0, 0)]) <= kSmCap) break;
     weights = true;
-    row.fill(0, true, [](float, uint32_t b) { return b; });
+    fill(logits, row.scale, s.mass[0], true, [](float, uint32_t b) { return b; });
   }
   const int64_t k = set.k;
   // The places that cut the order, then the one that is drawn, by one copy of
@@ -877,26 +923,26 @@ __global__ __launch_bounds__(kSmThreads) void k_sample(SampleArgs a) {
   }
 }
 
-// Pieces of a row: two workgroups a CU for the whole call, and no less than
-// one pass of the workgroup's threads over 16 bytes each.
+// Pieces of a row: four workgroups a CU for the whole call, where rows are few
+// and long.  Three launches take longer than they save on rows of 32000 (1 row
+// 22.3 us in pieces, 21.2 whole; 256 rows 42.6 and 33.0) and save on 65536 (1
+// row 23.2 and 31.4); more than a row a CU is work enough (256 x 151936: 122 us
+// in pieces, 131 whole; 500 x 151936: 188 and 145).
 int64_t pieces_of(int64_t tokens, int64_t vocab) {
-  int64_t segs = 512 / (tokens > 0 ? tokens : 1);
+  if (tokens >= 350 || vocab < 49152) return 1;
+  int64_t segs = 1024 / (tokens > 0 ? tokens : 1);
   if (segs > kSmPieces) segs = kSmPieces;
-  if (segs > vocab / 8192) segs = vocab / 8192;
-  return segs < 2 ? 1 : segs;
+  return segs > vocab / 8192 ? vocab / 8192 : segs;
 }
 
 template <typename T>
 hipError_t sample_launch(const SampleArgs& a, hipStream_t stream) {
-  constexpr int kVec = 16 / sizeof(T);
   if (a.segs > 1) {
     k_sample_range<T><<<a.tokens * a.segs, kSmThreads, 0, stream>>>(a);
     k_sample_bins<T><<<a.tokens * a.segs, kSmThreads, 0, stream>>>(a);
-    k_sample<T, 0, true><<<a.tokens, kSmThreads, 0, stream>>>(a);
-  } else if (a.vocab <= 4 * kSmThreads * kVec) {
-    k_sample<T, 4, false><<<a.tokens, kSmThreads, 0, stream>>>(a);
+    k_sample<T, kSmMany, true><<<a.tokens, kSmMany, 0, stream>>>(a);
   } else {
-    k_sample<T, 0, false><<<a.tokens, kSmThreads, 0, stream>>>(a);
+    k_sample<T, kSmThreads, false><<<a.tokens, kSmThreads, 0, stream>>>(a);
   }
   return hipGetLastError();
 }

@@ -725,12 +725,13 @@ fp8w_status fp8w_logprobs(const void* logits, fp8w_dtype dtype, int64_t stride, 
  * (log probability 0, one kept).  Masked tokens (-inf, NaN) are never drawn nor
  * counted; where +inf stands, only such tokens have weight.  A row masked
  * throughout gives token -1, log probability -inf and none kept.
- * Weights are fixed-point numbers of at least 31 bits below the largest (44
- * for 2^18 tokens) out of fp64 exponentials, so that the choice does not
- * depend on the order of sums, and hardly on their rounding.
+ * Weights are fixed-point numbers of 38 to 50 bits below the largest out of
+ * fp64 exponentials, and sums of many are within 2^-31 of themselves (2^-19
+ * for 2^24 tokens), so that the choice does not depend on the order of sums,
+ * and hardly on their rounding.
  * workspace: fp8w_sample_workspace_bytes(tokens, vocab) bytes, 16-byte
- * aligned (0 where there are enough rows to fill the chip).  tokens may be 0.
- * Requires 1 <= vocab <= 2^31 - 64, stride >= vocab.
+ * aligned (0 where rows are short, or enough to fill the chip).  tokens may be
+ * 0.  Requires 1 <= vocab <= 2^24, stride >= vocab.
  * Errors: NULL, SHAPE (also: workspace too small), UNSUPPORTED (dtype),
  * ALIGN, OVERLAP, HIP. */
 int64_t fp8w_sample_workspace_bytes(int64_t tokens, int64_t vocab);

@@ -120,8 +120,16 @@ def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=Non
 
 def sample_tolerance(logprob, vocab: int):
     """A log probability is rounded once to fp32; the sum behind it is of at
-    most `vocab` weights off by half a unit each, and at least 1."""
-    return 2.0 ** -24 * np.abs(np.where(np.isfinite(logprob), logprob, 0)) + vocab * 2.0 ** -(weight_bits(vocab) + 1) + 2.0 ** -40
+    most `vocab` weights off by half a unit each, and at least 1.
+
+    Where whole bins enter that sum, each weight is 1 + e times its bin's middle:
+    e rounded to half of 2^-f (f = 31, two less for each doubling beyond 2^18
+    tokens), with (0.021)^5 / 120 < 2^-34.7 left out of its series, 2^-41 of the
+    middle's, and all of it at most e^0.021 of the weight: 1.03 (2^-(f+1) +
+    2^-34.7 + 2^-41) < 2^-f of the sum, and as much of its logarithm."""
+    f = 31 - 2 * max(0, math.ceil(math.log2(vocab)) - 18)
+    return (2.0 ** -24 * np.abs(np.where(np.isfinite(logprob), logprob, 0)) + vocab * 2.0 ** -(weight_bits(vocab) + 1)
+            + 2.0 ** -f + 2.0 ** -40)
 
 
 def route_grouped(logits, top_k: int, groups: int, top_groups: int, by: str = "max", score: str = "softmax", bias=None,

@@ -225,7 +225,7 @@ def test_sample_refusals(L):
     for name in ("logits", "u", "ids"):
         assert call(**{name: None}) == F.ERR_NULL, name
     assert call(dtype=2) == F.ERR_UNSUPPORTED
-    for bad in (dict(t=-1), dict(v=0), dict(stride=99), dict(v=(1 << 31) - 1, stride=(1 << 31) - 1), dict(stride=1 << 31),
+    for bad in (dict(t=-1), dict(v=0), dict(stride=99), dict(v=(1 << 24) + 1, stride=1 << 25), dict(stride=1 << 31),
                 dict(t=1 << 30, u=1 << 50, ids=1 << 51, lp=1 << 52, kept=1 << 53, ws=1 << 54)):
         assert call(**bad) == F.ERR_SHAPE, bad
     for bad in (dict(logits=A + 1), dict(logits=A + 2, dtype=1), dict(u=B + 2), dict(temp=I + 1), dict(k=I + 2), dict(p=I + 3),

@@ -204,6 +204,63 @@ def test_lm_head_rows(F):
         _check(F, x, **k)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("i", range(len(FILTERS)))
+def test_long_rows(F, i, dtype):
+    """Rows of which pieces are taken at once."""
+    _check(F, _logits(3, 70001, dtype), **FILTERS[i])
+
+
+@pytest.mark.parametrize("pad", [1, 3, 8])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_long_rows_unaligned_and_masked(F, pad, dtype):
+    wide = _logits(5, 60000 + pad, dtype)
+    wide[0, 30000:] = -np.inf
+    wide[1] = -np.inf
+    wide[2] = -np.inf
+    wide[2, [pad, 59999]] = 1.0
+    wide[3, ::3] = float("nan")
+    for k in FILTERS[::2]:
+        _check(F, wide[:, pad:], **k)
+        _check(F, wide[:, :60000], **k)
+
+
+@pytest.mark.parametrize("t", [20, 349, 350])
+def test_long_rows_with_settings_of_their_own(F, t):
+    rng = np.random.default_rng(t)
+
+    def among(*v):
+        return np.array(v)[rng.integers(0, len(v), t)]
+    _check(F, _logits(t, 49152), temperature=among(0.0, 0.3, 1.0, 1.7), top_k=among(0, 1, 30, 700, 1500, 10**6),
+           top_p=among(1.0, 0.95, 0.5, 0.01), min_p=among(0.0, 0.0, 0.02, 0.3))
+
+
+@pytest.mark.parametrize("v", [262144, 262145, 300000, 600000, 1 << 21])
+def test_more_tokens_than_a_count_of_18_bits(F, v):
+    """All in one bin, all equal, and spread: a bin's sums stay within their part of its word."""
+    x = torch.zeros(4, v, device=dev())
+    x[1] = torch.randn(v, generator=torch.Generator(device="cuda").manual_seed(v), device=dev()) * 1e-4
+    x[1, 5], x[1, 6] = 1.0, -60.0                          # bins of a wide range, one of which has nearly all
+    x[2] = -30.0
+    x[2, -1] = 0.0
+    x[3] = _logits(1, v, F32)[0]
+    for k in (dict(), dict(top_p=0.6), dict(top_k=v // 2), dict(min_p=0.3), dict(top_k=40, top_p=0.9)):
+        _check(F, x, u=np.array([0.3, 0.6, 0.999, 0.42], np.float32), **k)
+
+
+def test_rows_beyond_4_gib(F):
+    """The last row starts past 2^32 bytes."""
+    stride = (1 << 30) + 64
+    try:
+        wide = torch.empty(2 * stride + 60000, dtype=BF16, device=dev())
+    except torch.OutOfMemoryError:
+        pytest.skip("needs 4 GiB")
+    x = torch.as_strided(wide, (3, 60000), (stride, 1))
+    x.copy_(_logits(3, 60000))
+    _check(F, x, top_p=0.9)
+    _check(F, x[:, :7001], top_k=30)
+
+
 def test_shares_follow_the_probabilities(F):
     """20000 evenly spaced numbers give every token its share of them, off by one at most."""
     x = _logits(1, 40, F32, scale=1.0)
@@ -215,8 +272,9 @@ def test_shares_follow_the_probabilities(F):
     assert (share - p).abs().max() <= 1.01 / n
 
 
-def test_repeatable_on_another_stream_and_in_a_graph(F):
-    x, u = _logits(5, 40000), torch.rand(5, device=dev())
+@pytest.mark.parametrize("v", [40000, 70000])
+def test_repeatable_on_another_stream_and_in_a_graph(F, v):
+    x, u = _logits(5, v), torch.rand(5, device=dev())
     k = dict(temperature=torch.full((5,), 0.8, device=dev()), top_p=torch.full((5,), 0.9, device=dev()))
     want = [v.clone() for v in F.fp8w_sample(x, u, **k)]
     side = torch.cuda.Stream()
@@ -225,13 +283,13 @@ def test_repeatable_on_another_stream_and_in_a_graph(F):
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     buf = [torch.empty_like(v) for v in want]
-    ws = torch.empty(max(F.lib().fp8w_sample_workspace_bytes(5, 40000), 16), dtype=torch.uint8, device=dev())
+    ws = torch.empty(max(F.lib().fp8w_sample_workspace_bytes(5, v), 16), dtype=torch.uint8, device=dev())
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
         F.fp8w_sample(x, u, **k, tokens=buf[0], logprob=buf[1], kept=buf[2], workspace=ws)
     for i in range(4):
-        x.copy_(_logits(5, 40000, seed=i + 1))
+        x.copy_(_logits(5, v, seed=i + 1))
         u.copy_(torch.rand(5, device=dev()))
         for b in buf:
             b.fill_(-7)
