@@ -31,7 +31,8 @@ __device__ __forceinline__ void store_one(const LinearCall& c, int i, int n, flo
     st_global<uint16_t>(c.y, at * 2, (uint16_t)f32_to_bf16_rne(v));
 }
 
-// The simple kernel: one wave takes 16 weight rows (gated: 16 of each half)
+// MX weights of up to three groups a row, of which the others read four
+// exponents at a time: one wave takes 16 weight rows (gated: 16 of each half)
 // against 16 rows of x, operands straight from memory.
 template <bool GATED>
 __global__ __launch_bounds__(256) void k_linear_simple(LinearCall c, int n_groups) {
@@ -43,42 +44,29 @@ __global__ __launch_bounds__(256) void k_linear_simple(LinearCall c, int n_group
   const int i = lane & 15, g = lane >> 4;
   const int row = min(m0 + i, c.m - 1);
   f32x4 acc[2] = {};
-  const int nkb = (c.k + 127) / 128, ng = (c.k + 31) / 32;
-  for (int kb = 0; kb < nkb; ++kb) {
-    f32x4 part[2] = {};
-    for (int h = 0; h < 2; ++h) {
-      const int col = kb * 128 + h * 64 + 16 * g;
-      const bool in = col < c.k;
-      uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
-      if (in) {
-        b0 = ld_global_u4(c.x, ((size_t)row * c.x_stride + col) * 2);
-        b1 = ld_global_u4(c.x, ((size_t)row * c.x_stride + col) * 2 + 16);
-      }
-#pragma unroll
-      for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-        const int n = min(n0 + i, n_out - 1) + q * n_out;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        float s = 1.0f;
-        if (in) {
-          w = ld_global_u4(c.codes, (size_t)n * c.k + col);
-          if (c.format == kFmtMx) s = mx_scale(ld_global<uint8_t>(c.scales, (size_t)n * ng + col / 32));
-        }
-        bf16x8 a0, a1;
-        a_operands<true>(w, s, a0, a1);
-        part[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, b0), part[q], 0, 0, 0);
-        part[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, b1), part[q], 0, 0, 0);
-      }
+  const int ng = (c.k + 31) / 32;
+  for (int first = 0; first < c.k; first += 64) {
+    const int col = first + 16 * g;
+    const bool in = col < c.k;   // all lanes take part in a product, those past k with zeros
+    uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+    if (in) {
+      b0 = ld_global_u4(c.x, ((size_t)row * c.x_stride + col) * 2);
+      b1 = ld_global_u4(c.x, ((size_t)row * c.x_stride + col) * 2 + 16);
     }
 #pragma unroll
-    for (int q = 0; q < (GATED ? 2 : 1); ++q)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int n = min(n0 + 4 * g + v, n_out - 1) + q * n_out;
-        float s = 1.0f;
-        if (c.format == kFmtBlock) s = ld_global<float>(c.scales, ((size_t)(n / 128) * nkb + kb) * 4);
-        if (c.format == kFmtBlockBf16) s = bf16_lo(ld_global<uint16_t>(c.scales, ((size_t)(n / 128) * nkb + kb) * 2));
-        acc[q][v] = __builtin_fmaf(s, part[q][v], acc[q][v]);
+    for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+      const int n = min(n0 + i, n_out - 1) + q * n_out;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      float s = 1.0f;
+      if (in) {
+        w = ld_global_u4(c.codes, (size_t)n * c.k + col);
+        s = mx_scale(ld_global<uint8_t>(c.scales, (size_t)n * ng + col / 32));
       }
+      bf16x8 a0, a1;
+      a_operands<true>(w, s, a0, a1);
+      acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, b0), acc[q], 0, 0, 0);
+      acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, b1), acc[q], 0, 0, 0);
+    }
   }
   if (m0 + i >= c.m) return;
 #pragma unroll
@@ -87,13 +75,7 @@ __global__ __launch_bounds__(256) void k_linear_simple(LinearCall c, int n_group
     if (n >= n_out) continue;
     float r[2];
 #pragma unroll
-    for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-      const int nq = n + q * n_out;
-      float s = 1.0f;
-      if (c.format == kFmtRow) s = ld_global<float>(c.scales, (size_t)nq * 4);
-      if (c.format == kFmtTensor) s = ld_global<float>(c.scales, 0);
-      r[q] = __builtin_fmaf(s, acc[q][v], bias_of(c, nq));
-    }
+    for (int q = 0; q < (GATED ? 2 : 1); ++q) r[q] = acc[q][v] + bias_of(c, n + q * n_out);
     store_one(c, m0 + i, n, GATED ? gated(c.act, r[0], r[1]) : c.act == kActGelu ? gelu(r[0]) : activated(c.act, r[0]));
   }
 }
@@ -204,10 +186,14 @@ __device__ __forceinline__ void settle(float (&v)[16]) {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32_unaligned __attribute__((aligned(1)));
 
+// A wave's number among the four that share a tile's columns.
+__device__ __forceinline__ int wave_of_four() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave % 4); }
+
 // Where a workgroup works: a tile of x's rows and of outputs, and a slice of
 // k's 128-column blocks.
 struct LinearTile {
   int m0, count, group, kb0, kb1;
+  int turn;   // how far into its columns it starts: XCDs do not all read the same ones
 };
 
 // How the tiles of a call are laid out.  Workgroups go round the 8 XCDs in
@@ -226,6 +212,7 @@ struct LinearGrid {
     t.group = (int)(pair - split * (uint32_t)groups);
     t.kb0 = (int)((int64_t)nkb * split / splits);
     t.kb1 = (int)((int64_t)nkb * (split + 1) / splits);
+    t.turn = (int)(blockIdx.x & 7);
     return true;
   }
 };
@@ -254,7 +241,7 @@ template <int FMT, bool GATED, int MT, int TW, typename Acc>
 __device__ __forceinline__ void finish_tile(const LinearCall& c, const LinearTile& at, Acc (&acc)[TW][MT], unsigned char* wl) {
   using Rows = WaveRows<GATED, TW>;
   constexpr int kCols = Rows::kCols, kUnits = kCols / 4;   // 16-byte units of a row of results
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_of_four();
   const int i = lane & 31, hh = lane >> 5;
   const Rows w(c, at.group, wave);
   if (FMT == kFmtRow || FMT == kFmtTensor || c.bias) {
@@ -366,33 +353,54 @@ constexpr int64_t slice_bytes() { return (int64_t)TW * MT * 4 * 4096; }
 //   * Weights: a wave's rows of a 128-column block are its own 4 * TW KB.  At
 //     the start of a block it takes them into registers in the A layout and
 //     asks for the next block at once: a block's time to arrive.
-//   * x: 64 columns of the rows for all four waves, three buffers, asked for
-//     two steps ahead; one barrier a step.
+//   * x: half of the rows (of 32: half of the columns) of the block for all
+//     four waves, three buffers, asked for two steps ahead; one barrier a step.
 // The waits name how many younger loads may still be on their way; a wait
 // for everything would put the memory's latency into every step.
 //
 // A lane's 16 bytes of codes are two MFMA steps of 8 columns each, so step
-// (p, s) takes columns 32p + 16(l/32) + 8s of the step, for weights and x
-// alike.  LDS rows are 128 bytes, their 16-byte units XOR-swizzled by row / 2,
-// so that any 16 consecutive rows fall into 16 different bank groups.
+// (p, s) takes columns 32p + 16(l/32) + 8s of the block, for weights and x
+// alike.  LDS rows are 128 or 256 bytes, their 16-byte units XOR-swizzled by
+// row / 2 or the row, so that any 16 consecutive rows fall into 16 different
+// bank groups.
 //
-// A block scale multiplies its sums every 64 columns (a full block's sums
-// would need as many registers as the accumulators); MX scales multiply the
-// codes as they become bf16 (exact); row and tensor scales the results.
-template <int FMT, bool GATED, int MT, int TW>
+// A block scale multiplies a block's sums of 32 rows at a time (sums of all
+// rows would need as many registers as the accumulators; steps of 64 columns
+// for all rows, twice the multiplications, took LEFT_US).  MX scales multiply
+// the codes as they become bf16 (exact); row and tensor scales the results.
+template <int FMT, bool GATED, int MT, int TW, int KW, bool BORDER>
 __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile& at, float* partial, unsigned char* ws,
-                                           unsigned char* xs0, unsigned char* xs1, unsigned char* xs2) {
+                                           unsigned char* xs0, unsigned char* xs1, unsigned char* xs2,
+                                           unsigned char* sums) {
   constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
   constexpr bool kMx = FMT == kFmtMx;
   using Rows = WaveRows<GATED, TW>;
   constexpr int kRows = Rows::kRows;
   constexpr int kXLoads = MT;          // x loads of a wave and step (1 KB each)
   constexpr int kWLoads = 4 * TW;      // weight loads of a wave and block
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  constexpr bool kTall = MT == 2 && KW == 1;   // a step is half of the rows, else half of the columns
+  constexpr int kStepQ = kTall ? MT / 2 : MT, kStepU = kTall ? 8 : 4;   // rows / 32, columns / 16
+  constexpr int kUnits = 2 * kStepU, kPerLoad = kWave / kUnits;        // 16 bytes of a row, rows of a load
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_of_four();
   const int i = lane & 31, hh = lane >> 5;
-  const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32, kb1 = at.kb1;
+  const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32;
   const Rows w(c, at.group, wave);
   const int n_out = w.n_out;
+  // Of KW groups of four waves each takes a part of the columns, as many blocks
+  // as the others (their barriers are the workgroup's); what is past the slice
+  // becomes past k, where all is zeros.
+  const int part = KW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / 256);
+  const int blocks = (at.kb1 - at.kb0 + KW - 1) / KW, first_block = at.kb0 + part * blocks;
+  int turned = at.turn % blocks;
+  const auto block_now = [&]() {
+    const int b = first_block + turned;
+    return KW == 1 || b < at.kb1 ? b : nkb;
+  };
+  int kb = block_now();   // the block in hand
+  const auto next_block = [&]() {
+    turned = turned + 1 < blocks ? turned + 1 : 0;
+    return block_now();
+  };
   unsigned char* wl = ws + wave * kRows * 128;
 
   // Load j of a wave's weights brings rows 8j + l/8; LDS place l%8 of a row
@@ -408,58 +416,72 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
   int wcol = 16 * wu;
   const auto load_w = [&](int kb, int j) __attribute__((always_inline)) {
     asm volatile("" : "+v"(wrow), "+v"(wcol)::"memory");
-    const int c0 = kb * 128 + (wcol ^ (j & 1) * 64);
+    const uint32_t c0 = (uint32_t)kb * 128 + (uint32_t)(wcol ^ (j & 1) * 64);
     const int row = min(w.out_row(8 * j), n_out - 1);
     const uint32_t within = (uint32_t)min(n_out - 1 - row, 7) * (uint32_t)k;
-    stage16(c.codes + (size_t)(row + w.half(8 * j)) * k + (min(wrow, within) + (uint32_t)(c0 < k ? c0 : 0)), wl + j * 1024);
+    stage16(c.codes + (size_t)(row + w.half(8 * j)) * k + (min(wrow, within) + (c0 < (uint32_t)k ? c0 : 0)), wl + j * 1024);
     asm volatile("" ::: "memory");
   };
   const auto request_w = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j) load_w(kb, j);
   };
-  // x rows a wave stages: 8 (MT * wave + j) + l/8, the same places (row / 2 % 8
-  // = 4 (row / 8 % 2) + l/16)
-  uint32_t xrow[kXLoads];
-#pragma unroll
-  for (int j = 0; j < kXLoads; ++j) xrow[j] = (uint32_t)(at.m0 + min(8 * (kXLoads * wave + j) + (lane >> 3), at.count - 1));
-  int xcol = 8 * (wu ^ (kXLoads * wave & 1) * 4);
-  const auto load_x = [&](int step, int j, unsigned char* to) __attribute__((always_inline)) {
-    asm volatile("" : "+v"(xcol), "+v"(xrow[j])::"memory");
-    const int c0 = step * 64 + (xcol ^ (j & 1) * 32);
+  // x rows a wave stages: kPerLoad (MT * wave + j) + l / kUnits of the step's,
+  // place l % kUnits with unit (l % kUnits) ^ row % 16 (of 8: row / 2 % 8 = 4
+  // (row / 8 % 2) + l / 16)
+  const int xrow = kPerLoad * kXLoads * wave + lane / kUnits;
+  int xcol = kTall ? 8 * ((lane & 15) ^ (lane >> 4) ^ (kXLoads * wave & 3) * 4) : 8 * (wu ^ (kXLoads * wave & 1) * 4);
+  const auto load_x = [&](int kb, int h, int j, unsigned char* to) __attribute__((always_inline)) {
+    int from_row = xrow;
+    asm volatile("" : "+v"(xcol), "+v"(from_row)::"memory");
+    const uint32_t c0 = (uint32_t)kb * 128 + (kTall ? 0 : 64 * h) + (uint32_t)(xcol ^ (j & (kTall ? 3 : 1)) * 32);
+    const uint32_t row = (uint32_t)(at.m0 + min(from_row + kPerLoad * j + (kTall ? 16 * MT * h : 0), at.count - 1));
     // An offset from x either way: chosen between two addresses the MX tile
     // spilled.
     const uint64_t x = reinterpret_cast<uint64_t>(c.x), none = reinterpret_cast<uint64_t>(&kNoColumns) - x;
-    const uint64_t from = (uint64_t)xrow[j] * (2 * (uint32_t)c.x_stride) + (uint32_t)(2 * c0);
-    stage16(reinterpret_cast<const void*>(x + (c0 < k ? from : none)), to + (kXLoads * wave + j) * 1024);
+    const uint64_t from = (uint64_t)row * (2 * (uint32_t)c.x_stride) + 2 * (uint64_t)c0;
+    stage16(reinterpret_cast<const void*>(x + (c0 < (uint32_t)k ? from : none)), to + (kXLoads * wave + j) * 1024);
     asm volatile("" ::: "memory");
   };
-  const auto request_x = [&](int step, unsigned char* to) __attribute__((always_inline)) {
+  const auto request_x = [&](int kb, int h, unsigned char* to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < kXLoads; ++j) load_x(step, j, to);
+    for (int j = 0; j < kXLoads; ++j) load_x(kb, h, j, to);
   };
 
   // scales of the next block: a float a run of rows that lie in one scale
-  // block (a half's, or a 32-row tile; scalar loads), or the four MX exponents
-  // of the lane's row in each tile
+  // block (a half's, or a 32-row tile; scalar loads), or two where the second
+  // half's blocks begin anywhere (BORDER); or the four MX exponents of the
+  // lane's row in each tile
+  static_assert(!BORDER || (kBlock && GATED && TW == 1), "runs of 16 rows");
   constexpr int kScales = kMx ? TW : GATED ? 2 : TW;
   const auto scale_of = [](int t, int v) { return GATED && TW == 1 ? v >> 3 : t; };   // of sum v of tile t
   const char* sp[kScales];
-  float sc[kScales];
+  float sc[kScales], after[BORDER ? kScales : 1];
+  int border[BORDER ? kScales : 1], down[BORDER ? kScales : 1];
   uint32_t ex[kScales];
 #pragma unroll
   for (int t = 0; t < kScales; ++t) {
     const int first = t * (kRows / kScales);
     const char* scales = static_cast<const char*>(c.scales);
+    if constexpr (BORDER) {
+      const int row = min(w.out_row(first), n_out - 1) + w.half(first);
+      border[t] = 128 - row % 128;
+      down[t] = row / 128 < (c.n - 1) / 128 ? nkb : 0;
+    }
     if (kBlock) sp[t] = scales + (size_t)((min(w.out_row(first), n_out - 1) + w.half(first)) / 128) * nkb * (FMT == kFmtBlock ? 4 : 2);
     if (kMx) sp[t] = scales + (size_t)(min(w.out_row(32 * t + i), n_out - 1) + w.half(32 * t + i)) * ng;
   }
-  const auto request_s = [&](int kb) __attribute__((always_inline)) {
+  const auto request_s = [&](int b) __attribute__((always_inline)) {
+    const int kb = KW == 1 ? b : min(b, nkb - 1);
 #pragma unroll
     for (int t = 0; t < kScales; ++t) {
-      if (FMT == kFmtBlock) sc[t] = reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(sp[t]))[kb];
-      if (FMT == kFmtBlockBf16)
-        sc[t] = bf16_lo(reinterpret_cast<const __attribute__((address_space(4))) uint16_t*>(reinterpret_cast<uintptr_t>(sp[t]))[kb]);
+      const auto scale = [&](int at) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(sp[t]);
+        return FMT == kFmtBlock ? reinterpret_cast<const __attribute__((address_space(4))) float*>(p)[at]
+                                : bf16_lo(reinterpret_cast<const __attribute__((address_space(4))) uint16_t*>(p)[at]);
+      };
+      if (kBlock) sc[t] = scale(kb);
+      if constexpr (BORDER) after[t] = scale(kb + down[t]);
       // four bytes that end with the row's last, where the block has fewer
       if (kMx) ex[t] = ld_global<u32_unaligned>(sp[t], (size_t)min(4 * kb, ng - 4));
     }
@@ -476,48 +498,62 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
       for (int v = 0; v < 16; ++v) acc[t][q][v] = 0.0f;
 
   uint4 wr[TW][4];                 // tile, 32-column pair of the block
-  float s[kScales];
+  bf16x8 a[TW][kStepU];            // the same as operands
+  float s[kScales], s_after[BORDER ? kScales : 1];
   uint32_t e[TW];
-  const auto take_w = [&](int kb) __attribute__((always_inline)) {
+  const auto scale_now = [&](int t, int v) {   // of sum v of tile t
+    const int run = scale_of(t, v);
+    if constexpr (BORDER) return 8 * (v >> 2 & 1) + 4 * hh + (v & 3) < border[run] ? s[run] : s_after[run];
+    return s[run];
+  };
+  const auto take_w = [&](int kb, int next) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < TW; ++t)
 #pragma unroll
       for (int p = 0; p < 4; ++p)
         wr[t][p] = *reinterpret_cast<const uint4*>(&wl[(32 * t + i) * 128 + 16 * ((2 * p + hh) ^ (i >> 1 & 7))]);
-    if (kb * 128 + 128 > k) {
-      const int from = kb * 128 + 16 * (lane_fresh() >> 5);
+    if ((uint32_t)kb * 128 + 128 > (uint32_t)k) {
+      const uint32_t from = (uint32_t)kb * 128 + 16 * (lane_fresh() >> 5);
 #pragma unroll
       for (int p = 0; p < 4; ++p)
 #pragma unroll
         for (int t = 0; t < TW; ++t)
-          if (from + 32 * p >= k) wr[t][p] = make_uint4(0, 0, 0, 0);
+          if (from + 32 * p >= (uint32_t)k) wr[t][p] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int t = 0; t < kScales; ++t) {
       if (kBlock) s[t] = sc[t];
-      if (kMx) e[t] = ex[t] >> 8 * (4 * kb - min(4 * kb, ng - 4));
+      if constexpr (BORDER) s_after[t] = after[t];
+      if (kMx) e[t] = ex[t] >> (8 * (4 * kb - min(4 * kb, ng - 4)) & 31);
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0): the codes are in registers
-    request_s(kb + 1 < kb1 ? kb + 1 : at.kb0);    // the last block asks for one nobody takes
+    request_s(next);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // 64 columns.  Scaled sums are settled after every 32 rows: left alone the
+  // A step.  Scaled sums are settled after every 32 rows: left alone the
   // compiler starts all products first, each with sums of its own, and spills.
   const auto step = [&](int h, const unsigned char* xb, const auto& load) __attribute__((always_inline)) {
-    const auto read_b = [&](int q, int u) __attribute__((always_inline)) {
-      return *reinterpret_cast<const bf16x8*>(&xb[(32 * q + i) * 128 + 16 * ((4 * (u >> 1) + 2 * hh + (u & 1)) ^ (i >> 1 & 7))]);
+    const auto read_b = [&](int n) __attribute__((always_inline)) {
+      const int q = n / kStepU, u = n % kStepU;
+      return *reinterpret_cast<const bf16x8*>(
+          &xb[(32 * q + i) * 16 * kUnits + 16 * ((4 * (u >> 1) + 2 * hh + (u & 1)) ^ (kTall ? i & 15 : i >> 1 & 7))]);
     };
-    bf16x8 a[TW][4], b[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) b[u] = read_b(0, u);
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
+    const auto operands = [&](int p, int from) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < TW; ++t)
-        a_operands<kMx>(wr[t][2 * h + p], kMx ? mx_scale((uint8_t)(e[t] >> 8 * (2 * h + p))) : 1.0f, a[t][2 * p], a[t][2 * p + 1]);
+        a_operands<kMx>(wr[t][from], kMx ? mx_scale((uint8_t)(e[t] >> 8 * from)) : 1.0f, a[t][2 * p], a[t][2 * p + 1]);
+    };
+    bf16x8 b[4];
 #pragma unroll
-    for (int q = 0; q < MT; ++q) {
+    for (int u = 0; u < 4; ++u) b[u] = read_b(u);
+    if (!kTall || h == 0) {
+#pragma unroll
+      for (int p = 0; p < kStepU / 2; ++p) operands(p, kTall ? p : 2 * h + p);
+    }
+#pragma unroll
+    for (int q = 0; q < kStepQ; ++q) {
+      const int rows = kTall ? h * kStepQ + q : q;
       f32x16 part[TW];
 #pragma unroll
       for (int t = 0; t < TW; ++t) {
@@ -525,36 +561,36 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
 #pragma unroll
           for (int v = 0; v < 16; ++v) part[t][v] = 0.0f;
         } else {
-          part[t] = acc[t][q];
+          part[t] = acc[t][rows];
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kStepU; ++u) {
+        const int n = q * kStepU + u;
 #pragma unroll
-        for (int t = 0; t < TW; ++t) part[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[t][u], b[u], part[t], 0, 0, 0);
-        // the operand's register is free: the next 32 rows' into it, three
-        // products ahead of their use
-        if (q + 1 < MT) b[u] = read_b(q + 1, u);
-        if (TW == 2) load(4 * q + u);
-        if (q + 1 < MT || u < 3) __builtin_amdgcn_sched_barrier(0);
+        for (int t = 0; t < TW; ++t) part[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[t][u], b[u & 3], part[t], 0, 0, 0);
+        // the operand's register is free: what is four products on into it
+        if (n + 4 < kStepQ * kStepU) b[u & 3] = read_b(n + 4);
+        if (TW == 2) load(n);
+        if (n + 1 < kStepQ * kStepU) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int t = 0; t < TW; ++t) {
         if constexpr (kBlock) {
 #pragma unroll
-          for (int v = 0; v < 16; ++v) acc[t][q][v] = __builtin_fmaf(s[scale_of(t, v)], part[t][v], acc[t][q][v]);
-          settle(acc[t][q]);
+          for (int v = 0; v < 16; ++v) acc[t][rows][v] = __builtin_fmaf(scale_now(t, v), part[t][v], acc[t][rows][v]);
+          settle(acc[t][rows]);
         } else {
-          acc[t][q] = part[t];
+          acc[t][rows] = part[t];
         }
       }
     }
   };
-  // A block of 128 columns: x steps 2kb and 2kb + 1 are in x0 and x1, and
+  // A block of 128 columns: its two steps' x are in x0 and x1, and
   // the two after them go to x2 and x0.
-  const auto block = [&](int kb, unsigned char* x0, unsigned char* x1, unsigned char* x2) __attribute__((always_inline)) {
-    take_w(kb);
-    const int next = kb + 1 < kb1 ? kb + 1 : at.kb0;
+  const auto block = [&](unsigned char* x0, unsigned char* x1, unsigned char* x2) __attribute__((always_inline)) {
+    const int next = next_block();   // the last block asks for one nobody takes
+    take_w(kb, next);
     const auto first = [&](int n) __attribute__((always_inline)) {   // 4 MT places for 8 + MT loads
       const int to = (n + 1) * (kWLoads + kXLoads) / (4 * MT);
 #pragma unroll
@@ -562,40 +598,62 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
         if (j < kWLoads)
           load_w(next, j);
         else
-          load_x(2 * next, j - kWLoads, x2);
+          load_x(next, 0, j - kWLoads, x2);
       }
     };
     const auto second = [&](int n) __attribute__((always_inline)) {
-      if (n % 4 == 0) load_x(2 * next + 1, n / 4, x0);
+      if (n % 4 == 0) load_x(next, 1, n / 4, x0);
     };
     if (TW == 1) {
       request_w(next);
-      request_x(2 * next, x2);
+      request_x(next, 0, x2);
       __builtin_amdgcn_sched_barrier(0);
     }
     step(0, x0, first);
     land_and_meet<kWLoads + kXLoads>();           // younger than x1's: weights and x2's
-    if (TW == 1) request_x(2 * next + 1, x0);
+    if (TW == 1) request_x(next, 1, x0);
     step(1, x1, second);
     land_and_meet<kXLoads>();                     // the weights and x2's have landed
+    kb = next;
   };
 
-  request_s(at.kb0);
-  request_w(at.kb0);
-  request_x(2 * at.kb0, xs0);
-  request_x(2 * at.kb0 + 1, xs1);
+  request_s(kb);
+  request_w(kb);
+  request_x(kb, 0, xs0);
+  request_x(kb, 1, xs1);
   land_and_meet<kXLoads>();
-  int kb = at.kb0;
+  int left = blocks;
 #pragma unroll 1
-  for (; kb + 2 < kb1; kb += 3) {
-    block(kb, xs0, xs1, xs2);
-    block(kb + 1, xs2, xs0, xs1);
-    block(kb + 2, xs1, xs2, xs0);
+  for (; left > 2; left -= 3) {
+    block(xs0, xs1, xs2);
+    block(xs2, xs0, xs1);
+    block(xs1, xs2, xs0);
   }
-  if (kb < kb1) block(kb, xs0, xs1, xs2);
-  if (kb + 1 < kb1) block(kb + 1, xs2, xs0, xs1);
+  if (left > 0) block(xs0, xs1, xs2);
+  if (left > 1) block(xs2, xs0, xs1);
   vm_wait_all();   // nothing may land in LDS that is no longer ours
 
+  if constexpr (KW > 1) {   // the groups' sums meet in the first's registers, in their order
+    static_assert((KW - 1) * MT <= KW, "they have the weights' LDS");
+    __syncthreads();
+    if (part > 0)
+      each_sum<MT, TW>(acc, [&](int off, auto* from, int a) {
+        *reinterpret_cast<f32x4*>(sums + (part - 1) * slice_bytes<MT, TW>() + off + (threadIdx.x & 255) * 16) =
+            f32x4{(*from)[a], (*from)[a + 1], (*from)[a + 2], (*from)[a + 3]};
+      });
+    __syncthreads();
+    if (part == 0) {
+#pragma unroll
+      for (int p = 0; p < KW - 1; ++p)
+        each_sum<MT, TW>(acc, [&](int off, auto* to, int a) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(sums + p * slice_bytes<MT, TW>() + off + threadIdx.x * 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) (*to)[a + e] += v[e];
+        });
+    }
+    __syncthreads();   // the tile's end writes over them
+    if (part > 0) return;
+  }
   if (partial) {
     each_sum<MT, TW>(acc, [&](int off, auto* sums, int a) {
       st_global<f32x4>(partial, (size_t)off + threadIdx.x * 16, f32x4{(*sums)[a], (*sums)[a + 1], (*sums)[a + 2], (*sums)[a + 3]});
@@ -605,20 +663,22 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
   finish_tile<FMT, GATED, MT, TW>(c, at, acc, wl);
 }
 
-template <int FMT, bool GATED, int MT, int TW>
-__global__ __launch_bounds__(256, TW == 2 ? 2 : 4) void k_linear_tile(LinearCall c, LinearGrid grid) {
+template <int FMT, bool GATED, int MT, int TW, int KW, bool BORDER>
+__global__ __launch_bounds__(256 * KW, TW == 2 || BORDER ? 2 : 4) void k_linear_tile(LinearCall c, LinearGrid grid) {
   // separate arrays: the compiler then knows that reads of one need not wait
   // for what is on its way into another
-  __shared__ __attribute__((aligned(16))) unsigned char ws[4 * 32 * TW * 128];
-  __shared__ __attribute__((aligned(16))) unsigned char xs0[32 * MT * 128];
-  __shared__ __attribute__((aligned(16))) unsigned char xs1[32 * MT * 128];
-  __shared__ __attribute__((aligned(16))) unsigned char xs2[32 * MT * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char ws[KW * 4 * 32 * TW * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs0[KW * 32 * MT * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs1[KW * 32 * MT * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char xs2[KW * 32 * MT * 128];
+  const int part = KW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / 256);
   LinearTile at;
   int64_t id;
   if (!grid.at(32 * MT, c.m, (c.k + 127) / 128, at, id)) return;
   float* partial = grid.splits == 1 ? nullptr
                                     : reinterpret_cast<float*>(static_cast<char*>(c.workspace) + id * slice_bytes<MT, TW>());
-  linear_run<FMT, GATED, MT, TW>(c, at, partial, ws, xs0, xs1, xs2);
+  linear_run<FMT, GATED, MT, TW, KW, BORDER>(c, at, partial, ws + part * 4 * 32 * TW * 128, xs0 + part * 32 * MT * 128,
+                                     xs1 + part * 32 * MT * 128, xs2 + part * 32 * MT * 128, ws);
 }
 
 // The slices' sums added, in their order, and the tile's end.
@@ -854,52 +914,90 @@ __global__ __launch_bounds__(256) void k_linear_rows(LinearCall c, int splits) {
 bool is_gated(int act) { return act == kActSwiglu || act == kActGeglu; }
 
 constexpr int kStreamRows = 16;   // x's rows that the streaming kernel takes
-constexpr int kStreamTiles = 2, kStreamWaves = 4;
-constexpr int kMaxSplits = 64;
-
+constexpr int kFill = 256;        // workgroups: one a CU
 
 // The kernel of a call, by its sizes.
 struct LinearPlan {
-  enum Kind { kSimple, kStream, kSkinny, kNarrow, kWide } kind;
+  enum Kind { kSimple, kStream, kTile } kind;
   int height, width;   // x's rows and outputs of a tile
+  int nt;              // the streaming kernel's
+  int mt, tw, kw;      // the tiled kernel's
+  bool border;
   LinearGrid grid;
   int64_t slice;       // workspace of one tile and slice
 };
 
+// Times are of weights that come from HBM, in us.
+//
+// Up to 16 rows of x the streaming kernel: 16 nt weight rows a workgroup, four
+// waves that share k (nt = 1: eight).
+//   nt = 1 where 32 rows a workgroup left CUs without one, and k is short:
+//     1 x 4096 x 4096 6.4, 7.6 with nt = 2; 1 x 6144 x 4096 8.2 with either.
+//     Long k is cut in slices instead, and x read half as often:
+//     16 x 4096 x 12288 15.2, 17.8 with nt = 1.
+//   nt = 4 where there are workgroups enough all the same, and the reads of x
+//     weigh: 8 x 151936 x 2048 54, 60 with nt = 2; 16 x 16384 x 4096 18 and 21;
+//     but 1 x 24576 x 4096 23 and 21.
+// Above, the tiled kernel of 128 weight rows (mt = 4: 256) by 32 mt rows of x.
+//   Up to 512 rows mt = 2: 300 x 24576 x 4096 88, 124 with mt = 4; 512 x 6144
+//     x 4096 44 and 52; 512 x 4096 x 12288 69 and 65; 1000 x 6144 x 4096 68 and
+//     60.  mt = 4 also needs halves of whole 32 rows.
+//   mt = 1 up to 32 rows, and where its tiles fill the CUs once and twice as
+//     high ones did not: 128 x 6144 x 4096 17.7, 21 with mt = 2 and two slices.
+//   While there is no more than a tile a CU, eight waves share its k: 203 x
+//     6144 x 4096 25, 29 with four, 30 with four and two slices; 64 x 24576 x
+//     4096 30 and 34; 512 x 6144 x 4096 (384 tiles) 44 with either.
+// Fewer tiles than CUs are cut in slices of k, of eight blocks (streaming: 32)
+// at least, and a second launch adds these up: 64 x 4096 x 12288 with eight
+// slices 24.6, four 28; 32 x 4096 x 12288 with eight 20.5, one 35.  More than
+// one workgroup a CU does not pay: 1777 x 4096 x 12288 (224 tiles) 170, with
+// two slices 178.
 LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, int format, int act) {
   const bool gate = is_gated(act), block = format == kFmtBlock || format == kFmtBlockBf16;
   const int outputs = gate ? 1 : 2;   // of two weight rows
   const int64_t n_out = gate ? n / 2 : n, nkb = (k + 127) / 128;
-  const int64_t split = gate && block ? n_out : 0;   // where the second half's scale blocks start
-  LinearPlan p{LinearPlan::kSimple, 16, 64, {1, 1, 1}, 0};
-  int64_t fill = 1;    // workgroups that fill the chip
-  int64_t least = 4;   // blocks of a slice
+  const int64_t second = gate && block ? n_out : 0;   // where the second half's scale blocks start
+  LinearPlan p{LinearPlan::kSimple, 16, 64, 0, 0, 0, 1, false, {1, 1, 1}, 0};
+  int64_t least = 8;   // blocks of a slice
+  const int64_t groups = (n_out + 64 * outputs - 1) / (64 * outputs);
   if (format == kFmtMx && k <= 96) {
     // rows of fewer than four exponents, which the others read at a time
   } else if (m <= kStreamRows) {
-    p = {LinearPlan::kStream, kStreamRows, 8 * kStreamTiles * outputs, {1, 1, 1}, 0}, fill = 256, least = 32;
-  } else if (split % 32 == 0) {
-    if (m <= 32)
-      p = {LinearPlan::kSkinny, 32, 64 * outputs, {1, 1, 1}, slice_bytes<1, 1>()}, fill = 1024;
-    else if (m <= 256)
-      p = {LinearPlan::kNarrow, 64, 64 * outputs, {1, 1, 1}, slice_bytes<2, 1>()}, fill = 1024;
-    else
-      p = {LinearPlan::kWide, 128, 128 * outputs, {1, 1, 1}, slice_bytes<4, 2>()}, fill = 512;
+    p.kind = LinearPlan::kStream;
+    p.nt = n >= 65536 || (m > 8 && n >= 64 * kFill) ? 4 : n <= 16 * kFill && nkb < 64 && !gate ? 1 : 2;
+    p.height = kStreamRows;
+    p.width = 8 * p.nt * outputs;
+    least = 32;
+  } else {
+    p.kind = LinearPlan::kTile;
+    const int64_t flat = (m + 31) / 32 * groups;
+    p.mt = m <= 32 || (flat > 128 && flat <= kFill) ? 1 : m <= 512 || second % 32 != 0 ? 2 : 4;
+    p.tw = p.mt == 4 ? 2 : 1;
+    p.kw = p.mt < 4 && (m + 32 * p.mt - 1) / (32 * p.mt) * groups <= kFill ? 2 : 1;
+    p.border = second % 16 != 0;
+    p.height = 32 * p.mt;
+    p.width = 64 * p.tw * outputs;
+    p.slice = (int64_t)p.mt * p.tw * 4 * 4096;
   }
   p.grid.tiles_m = (int)((m + p.height - 1) / p.height);
   p.grid.groups = (int)((n_out + p.width - 1) / p.width);
-  const int64_t tiles = (int64_t)p.grid.tiles_m * p.grid.groups;
-  int64_t splits = fill / tiles;
+  if (p.kind == LinearPlan::kSimple) return p;
+  int64_t splits = kFill / ((int64_t)p.grid.tiles_m * p.grid.groups);
   if (splits > nkb / least) splits = nkb / least;
-  if (splits > kMaxSplits) splits = kMaxSplits;
   p.grid.splits = splits < 1 ? 1 : (int)splits;
   return p;
 }
 
 template <int FMT, bool GATED>
 hipError_t launch_stream(const LinearCall& c, const LinearPlan& p, hipStream_t stream) {
-  k_linear_stream<FMT, GATED, kStreamTiles, 1, kStreamWaves, 2>
-      <<<dim3(p.grid.groups, p.grid.splits), kStreamWaves * kWave, 0, stream>>>(c);
+  const dim3 grid(p.grid.groups, p.grid.splits);
+  if (p.nt == 4) {
+    k_linear_stream<FMT, GATED, 4, 1, 4, 2><<<grid, 4 * kWave, 0, stream>>>(c);
+  } else if (p.nt == 2) {
+    k_linear_stream<FMT, GATED, 2, 1, 4, 2><<<grid, 4 * kWave, 0, stream>>>(c);
+  } else if constexpr (!GATED) {
+    k_linear_stream<FMT, GATED, 1, 1, 8, 2><<<grid, 8 * kWave, 0, stream>>>(c);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.grid.splits == 1) return e;
   const int64_t quads = (int64_t)c.m * (((GATED ? c.n / 2 : c.n) + 3) / 4);
@@ -907,24 +1005,30 @@ hipError_t launch_stream(const LinearCall& c, const LinearPlan& p, hipStream_t s
   return hipGetLastError();
 }
 
-template <int FMT, bool GATED>
-hipError_t launch_plan(const LinearCall& c, const LinearPlan& p, hipStream_t stream) {
-  if (p.kind == LinearPlan::kStream) return launch_stream<FMT, GATED>(c, p, stream);
+template <int FMT, bool GATED, int MT, int TW, int KW>
+hipError_t launch_tile(const LinearCall& c, const LinearPlan& p, hipStream_t stream) {
   const int64_t tiles = (int64_t)p.grid.tiles_m * p.grid.groups;
   const unsigned blocks = (unsigned)((tiles * p.grid.splits + 7) / 8 * 8), joins = (unsigned)((tiles + 7) / 8 * 8);
-  switch (p.kind) {
-    case LinearPlan::kSkinny: k_linear_tile<FMT, GATED, 1, 1><<<blocks, 256, 0, stream>>>(c, p.grid); break;
-    case LinearPlan::kNarrow: k_linear_tile<FMT, GATED, 2, 1><<<blocks, 256, 0, stream>>>(c, p.grid); break;
-    default: k_linear_tile<FMT, GATED, 4, 2><<<blocks, 256, 0, stream>>>(c, p.grid); break;
+  if constexpr (GATED && TW == 1 && (FMT == kFmtBlock || FMT == kFmtBlockBf16)) {
+    if (p.border)
+      k_linear_tile<FMT, GATED, MT, TW, KW, true><<<blocks, 256 * KW, 0, stream>>>(c, p.grid);
+    else
+      k_linear_tile<FMT, GATED, MT, TW, KW, false><<<blocks, 256 * KW, 0, stream>>>(c, p.grid);
+  } else {
+    k_linear_tile<FMT, GATED, MT, TW, KW, false><<<blocks, 256 * KW, 0, stream>>>(c, p.grid);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.grid.splits == 1) return e;
-  switch (p.kind) {
-    case LinearPlan::kSkinny: k_linear_join<FMT, GATED, 1, 1><<<joins, 256, 0, stream>>>(c, p.grid); break;
-    case LinearPlan::kNarrow: k_linear_join<FMT, GATED, 2, 1><<<joins, 256, 0, stream>>>(c, p.grid); break;
-    default: k_linear_join<FMT, GATED, 4, 2><<<joins, 256, 0, stream>>>(c, p.grid); break;
-  }
+  k_linear_join<FMT, GATED, MT, TW><<<joins, 256, 0, stream>>>(c, p.grid);
   return hipGetLastError();
+}
+
+template <int FMT, bool GATED>
+hipError_t launch_plan(const LinearCall& c, const LinearPlan& p, hipStream_t stream) {
+  if (p.kind == LinearPlan::kStream) return launch_stream<FMT, GATED>(c, p, stream);
+  if (p.mt == 4) return launch_tile<FMT, GATED, 4, 2, 1>(c, p, stream);
+  if (p.mt == 2) return p.kw == 2 ? launch_tile<FMT, GATED, 2, 1, 2>(c, p, stream) : launch_tile<FMT, GATED, 2, 1, 1>(c, p, stream);
+  return p.kw == 2 ? launch_tile<FMT, GATED, 1, 1, 2>(c, p, stream) : launch_tile<FMT, GATED, 1, 1, 1>(c, p, stream);
 }
 
 template <int FMT>
