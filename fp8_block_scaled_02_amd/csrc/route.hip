@@ -141,6 +141,35 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t at) {
   return bf16_lo(ld_global<uint16_t>(p, (size_t)at * 2));
 }
 
+// The experts' scores in fp64 (softmax: not yet divided by their sum).  Of few
+// experts a lane by one copy of the exponential, with the registers moved on
+// under it: a lone token's time is that of fetching the code.
+template <int R>
+__device__ __forceinline__ void scores(const RouteArgs& a, const float (&x)[R], float top, double (&score)[R]) {
+  const auto of = [&](float v) {
+    const double e = exp(a.score == 0 ? (double)v - (double)top : -(double)v);
+    return a.score == 0 ? e : 1.0 / (1.0 + e);
+  };
+  if constexpr (R > 4) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) score[r] = of(x[r]);
+    return;
+  }
+  float v[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) v[r] = x[r];
+#pragma unroll 1
+  for (int n = 0; n < R; ++n) {
+    const double s = of(v[0]);
+#pragma unroll
+    for (int r = 0; r + 1 < R; ++r) {
+      v[r] = v[r + 1];
+      score[r] = score[r + 1];
+    }
+    score[R - 1] = s;
+  }
+}
+
 // Shuts the groups that are not among the token's best: their experts' keys
 // become -inf.  2^log_lanes neighbouring lanes hold a group's experts (lanes
 // past the last group hold none), so a group's two best keys meet in steps of
@@ -152,23 +181,34 @@ __device__ __forceinline__ void shut_groups(const RouteArgs& a, const float (&x)
   const int lane = threadIdx.x & (L - 1), mine = lane >> a.log_lanes;
   const double ninf = -(double)__builtin_inff();
   double first = ninf, second = ninf;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    double k = (double)key[r];
-    if (sizeof(Key) == 4 && a.top2 && x[r] > -__builtin_inff())
-      k = a.score == 0 ? exp((double)x[r] - (double)top) : 1.0 / (1.0 + exp(-(double)x[r]));
-    second = pick_max(second, first < k ? first : k);
-    first = pick_max(first, k);
-  }
-  for (int off = 1; off < 1 << a.log_lanes; off <<= 1) {
-    const double f = __shfl_xor(first, off), s = __shfl_xor(second, off);
+  const auto meet = [&](double f, double s) {
     second = pick_max(pick_max(second, s), first < f ? first : f);
     first = pick_max(first, f);
+  };
+  if (sizeof(Key) == 4 && a.top2) {
+    double score[R];
+    scores<R>(a, x, top, score);
+#pragma unroll
+    for (int r = 0; r < R; ++r) meet(x[r] > -__builtin_inff() ? score[r] : ninf, ninf);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) meet((double)key[r], ninf);
   }
+  // Lanes that have met hold the same, so that a mirrored row or half of one
+  // brings the other half's.
+  if (a.log_lanes > 0) meet(dpp_mov<0xB1>(first), dpp_mov<0xB1>(second));
+  if (a.log_lanes > 1) meet(dpp_mov<0x4E>(first), dpp_mov<0x4E>(second));
+  if (a.log_lanes > 2) meet(dpp_mov<0x141>(first), dpp_mov<0x141>(second));
+  if (a.log_lanes > 3) meet(dpp_mov<0x140>(first), dpp_mov<0x140>(second));
+  for (int off = 16; off < 1 << a.log_lanes; off <<= 1) meet(__shfl_xor(first, off), __shfl_xor(second, off));
   const double rating = a.top2 && second > ninf ? first + second : first;
   int better = 0;
   for (int g = 0; g < a.groups; ++g) {
-    const double other = __shfl(rating, g << a.log_lanes, L);
+    double other;
+    if constexpr (L == kWave)
+      other = lane_value(rating, g << a.log_lanes);
+    else
+      other = __shfl(rating, g << a.log_lanes, L);
     better += other > rating || (other == rating && g < mine) ? 1 : 0;
   }
   if (better >= a.top_groups) {
@@ -193,13 +233,14 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_i
     const int in = (r << a.log_lanes) + (lane & ((1 << a.log_lanes) - 1));
     return part < a.groups && in < size ? part * size + in : kRouteMaxE;
   };
-  float x[R];
+  float x[R], bias[kBias ? R : 1];
   Key key[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int e = expert(r);
     const float v = load_logit<T>(a.logits, (int64_t)t * a.stride + (e < a.experts ? e : 0));
     x[r] = v == v && e < a.experts ? v : ninf;
+    if constexpr (kBias) bias[r] = ld_global<float>(a.bias, (size_t)(e < a.experts ? e : 0) * 4);
   }
   float top = x[0];
 #pragma unroll
@@ -212,17 +253,18 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int& my_i
     z = group_total<L>(z);
   }
   if constexpr (kBias) {
-    double zd = 0.0;
+    scores<R>(a, x, top, key);
+    if (a.score == 0) {
+      double zd = 0.0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      key[r] = a.score == 0 ? exp((double)x[r] - (double)top) : 1.0 / (1.0 + exp(-(double)x[r]));
-      zd += x[r] > ninf ? key[r] : 0.0;
+      for (int r = 0; r < R; ++r) zd += x[r] > ninf ? key[r] : 0.0;
+      zd = group_total<L>(zd);
+#pragma unroll
+      for (int r = 0; r < R; ++r) key[r] = key[r] / zd;
     }
-    zd = a.score == 0 ? group_total<L>(zd) : 1.0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int e = expert(r);
-      const double k = key[r] / zd + (double)ld_global<float>(a.bias, (size_t)(e < a.experts ? e : 0) * 4);
+      const double k = key[r] + (double)bias[r];
       key[r] = x[r] > ninf && k == k ? k : (double)ninf;
     }
   } else {
