@@ -289,6 +289,16 @@ __device__ __forceinline__ void finish_tile(const LinearCall& c, const LinearTil
       }
       asm volatile("" ::: "memory");
     }
+    if (!vec) {   // rows that start anywhere: an output a lane
+      const int col = lane % kCols, n = w.n0 + col;
+#pragma unroll 4
+      for (int r = lane / kCols; r < min(32, at.count - 32 * q); r += kWave / kCols) {
+        const float v = *reinterpret_cast<const float*>(wl + r * 4 * kCols + 16 * ((col >> 2) ^ (r & (kUnits - 1))) + 4 * (col & 3));
+        if (n < w.n_out) store_one(c, at.m0 + 32 * q + r, n, v);
+      }
+      asm volatile("" ::: "memory");
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < kCols / 16; ++j) {   // 8 outputs a lane
       constexpr int kLanes = kCols / 8;      // lanes of a row
@@ -303,7 +313,7 @@ __device__ __forceinline__ void finish_tile(const LinearCall& c, const LinearTil
         o[e] = v0[e];
         o[4 + e] = v1[e];
       }
-      if (!vec || n + 8 > w.n_out) {
+      if (n + 8 > w.n_out) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (n + e < w.n_out) store_one(c, row, n + e, o[e]);
@@ -939,9 +949,10 @@ struct LinearPlan {
 //     weigh: 8 x 151936 x 2048 54, 60 with nt = 2; 16 x 16384 x 4096 18 and 21;
 //     but 1 x 24576 x 4096 23 and 21.
 // Above, the tiled kernel of 128 weight rows (mt = 4: 256) by 32 mt rows of x.
-//   Up to 512 rows mt = 2: 300 x 24576 x 4096 88, 124 with mt = 4; 512 x 6144
-//     x 4096 44 and 52; 512 x 4096 x 12288 69 and 65; 1000 x 6144 x 4096 68 and
-//     60.  mt = 4 also needs halves of whole 32 rows.
+//   mt = 2 up to 512 rows (300 x 24576 x 4096 88, 124 with mt = 4; 512 x 6144
+//     x 4096 44 and 52; 512 x 4096 x 12288 69 and 65), and above while tiles of
+//     mt = 4 were fewer than 160 (1000 x 4096 x 4096 46 and 61; 1000 x 6144 x
+//     4096, which has 192, 68 and 60).  mt = 4 also needs halves of whole 32 rows.
 //   mt = 1 up to 32 rows, and where its tiles fill the CUs once and twice as
 //     high ones did not: 128 x 6144 x 4096 17.7, 21 with mt = 2 and two slices.
 //   While there is no more than a tile a CU, eight waves share its k: 203 x
@@ -971,7 +982,8 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, int format, int act) {
   } else {
     p.kind = LinearPlan::kTile;
     const int64_t flat = (m + 31) / 32 * groups;
-    p.mt = m <= 32 || (flat > 128 && flat <= kFill) ? 1 : m <= 512 || second % 32 != 0 ? 2 : 4;
+    const int64_t wide = (m + 127) / 128 * ((groups + 1) / 2);
+    p.mt = m <= 32 || (flat > 128 && flat <= kFill) ? 1 : m <= 512 || wide < 160 || second % 32 != 0 ? 2 : 4;
     p.tw = p.mt == 4 ? 2 : 1;
     p.kw = p.mt < 4 && (m + 32 * p.mt - 1) / (32 * p.mt) * groups <= kFill ? 2 : 1;
     p.border = second % 16 != 0;
