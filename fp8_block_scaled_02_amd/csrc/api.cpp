@@ -755,7 +755,7 @@ FP8W_API fp8w_status fp8w_linear(const uint16_t* x, int64_t x_stride, int64_t m,
     return FP8W_ERR_UNSUPPORTED;
   if (!linear_shape_ok(m, n, k, act)) return FP8W_ERR_SHAPE;
   const int64_t n_out = act_gated(act) ? n / 2 : n;
-  if (x_stride < k || x_stride > kMaxDim || y_stride < n_out || y_stride > kMaxDim ||
+  if (x_stride < k || x_stride > (1 << 28) || y_stride < n_out || y_stride > kMaxDim ||
       (residual && (residual_stride < n_out || residual_stride > kMaxDim)))
     return FP8W_ERR_SHAPE;
   if (k % 16 != 0 || x_stride % 8 != 0 || !aligned(x, 16) || !aligned(codes, 16) ||

@@ -163,6 +163,16 @@ __device__ __forceinline__ void stage16(const void* from, unsigned char* to) {
                                    (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
+// Block scale `at` (uniform), by a scalar load: there are none of two bytes, and
+// a vector load would be waited for with all that left before it.
+template <int FMT>
+__device__ __forceinline__ float scalar_scale(const char* scales, int at) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(scales) + (size_t)at * (FMT == kFmtBlock ? 4 : 2);
+  if constexpr (FMT == kFmtBlock) return *reinterpret_cast<const __attribute__((address_space(4))) float*>(p);
+  const uint32_t both = *reinterpret_cast<const __attribute__((address_space(4))) uint32_t*>(p & ~(uintptr_t)3);
+  return __uint_as_float(p & 2 ? both & 0xFFFF0000u : both << 16);
+}
+
 // What x holds past its columns.
 __device__ const uint4 kNoColumns = {0, 0, 0, 0};
 
@@ -380,8 +390,7 @@ constexpr int64_t slice_bytes() { return (int64_t)TW * MT * 4 * 4096; }
 // the codes as they become bf16 (exact); row and tensor scales the results.
 template <int FMT, bool GATED, int MT, int TW, int KW, bool BORDER>
 __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile& at, float* partial, unsigned char* ws,
-                                           unsigned char* xs0, unsigned char* xs1, unsigned char* xs2,
-                                           unsigned char* sums) {
+                                           unsigned char* xs0, unsigned char* xs1, unsigned char* xs2) {
   constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
   constexpr bool kMx = FMT == kFmtMx;
   using Rows = WaveRows<GATED, TW>;
@@ -401,7 +410,7 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
   // becomes past k, where all is zeros.
   const int part = KW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / 256);
   const int blocks = (at.kb1 - at.kb0 + KW - 1) / KW, first_block = at.kb0 + part * blocks;
-  int turned = at.turn % blocks;
+  int turned = at.turn % blocks, here = turned;
   const auto block_now = [&]() {
     const int b = first_block + turned;
     return KW == 1 || b < at.kb1 ? b : nkb;
@@ -411,13 +420,15 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
     turned = turned + 1 < blocks ? turned + 1 : 0;
     return block_now();
   };
-  unsigned char* wl = ws + wave * kRows * 128;
+  // (By the wave's number in the workgroup: as a part's four waves' the compiler
+  // takes what is on its way to x's LDS to be on its way here.)
+  unsigned char* wl = ws + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * kRows * 128;
 
   // Load j of a wave's weights brings rows 8j + l/8; LDS place l%8 of a row
   // holds its unit (l%8) ^ (row / 2 % 8), so j odd the unit of j even ^ 4.
-  // Rows past the end are the last one, columns past it the first ones (zeroed
-  // by take_w; x has zeros there, so that no infinity of a column that is read
-  // in their place meets them).  No branches: a load that two paths share is
+  // Rows past the end are the last one, columns past it the last ones (zeroed
+  // by take_w, and in x by no_columns, so that no infinity of a column that is
+  // read in their place meets them).  No branches: a load that two paths share is
   // one the compiler takes to write any of the arrays.  Offsets pass through
   // an empty asm statement where they are used: the addresses of all loads
   // would otherwise be kept in registers throughout.
@@ -429,7 +440,7 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
     const uint32_t c0 = (uint32_t)kb * 128 + (uint32_t)(wcol ^ (j & 1) * 64);
     const int row = min(w.out_row(8 * j), n_out - 1);
     const uint32_t within = (uint32_t)min(n_out - 1 - row, 7) * (uint32_t)k;
-    stage16(c.codes + (size_t)(row + w.half(8 * j)) * k + (min(wrow, within) + (c0 < (uint32_t)k ? c0 : 0)), wl + j * 1024);
+    stage16(c.codes + (size_t)(row + w.half(8 * j)) * k + (min(wrow, within) + min(c0, (uint32_t)k - 16)), wl + j * 1024);
     asm volatile("" ::: "memory");
   };
   const auto request_w = [&](int kb) __attribute__((always_inline)) {
@@ -438,19 +449,17 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
   };
   // x rows a wave stages: kPerLoad (MT * wave + j) + l / kUnits of the step's,
   // place l % kUnits with unit (l % kUnits) ^ row % 16 (of 8: row / 2 % 8 = 4
-  // (row / 8 % 2) + l / 16)
-  const int xrow = kPerLoad * kXLoads * wave + lane / kUnits;
+  // (row / 8 % 2) + l / 16).  Offsets within a load's rows have 32 bits.
+  const uint32_t x_row = 2 * (uint32_t)c.x_stride;
+  uint32_t xrow = (uint32_t)(lane / kUnits) * x_row;
   int xcol = kTall ? 8 * ((lane & 15) ^ (lane >> 4) ^ (kXLoads * wave & 3) * 4) : 8 * (wu ^ (kXLoads * wave & 1) * 4);
   const auto load_x = [&](int kb, int h, int j, unsigned char* to) __attribute__((always_inline)) {
-    int from_row = xrow;
-    asm volatile("" : "+v"(xcol), "+v"(from_row)::"memory");
+    asm volatile("" : "+v"(xcol), "+v"(xrow)::"memory");
     const uint32_t c0 = (uint32_t)kb * 128 + (kTall ? 0 : 64 * h) + (uint32_t)(xcol ^ (j & (kTall ? 3 : 1)) * 32);
-    const uint32_t row = (uint32_t)(at.m0 + min(from_row + kPerLoad * j + (kTall ? 16 * MT * h : 0), at.count - 1));
-    // An offset from x either way: chosen between two addresses the MX tile
-    // spilled.
-    const uint64_t x = reinterpret_cast<uint64_t>(c.x), none = reinterpret_cast<uint64_t>(&kNoColumns) - x;
-    const uint64_t from = (uint64_t)row * (2 * (uint32_t)c.x_stride) + 2 * (uint64_t)c0;
-    stage16(reinterpret_cast<const void*>(x + (c0 < (uint32_t)k ? from : none)), to + (kXLoads * wave + j) * 1024);
+    const int row = min(kPerLoad * (kXLoads * wave + j) + (kTall ? 16 * MT * h : 0), at.count - 1);
+    const uint32_t within = (uint32_t)min(at.count - 1 - row, kPerLoad - 1) * x_row;
+    stage16(reinterpret_cast<const char*>(c.x) + (size_t)(at.m0 + row) * x_row + (min(xrow, within) + 2 * min(c0, (uint32_t)k - 8)),
+            to + (kXLoads * wave + j) * 1024);
     asm volatile("" ::: "memory");
   };
   const auto request_x = [&](int kb, int h, unsigned char* to) __attribute__((always_inline)) {
@@ -486,9 +495,7 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
 #pragma unroll
     for (int t = 0; t < kScales; ++t) {
       const auto scale = [&](int at) {
-        const uintptr_t p = reinterpret_cast<uintptr_t>(sp[t]);
-        return FMT == kFmtBlock ? reinterpret_cast<const __attribute__((address_space(4))) float*>(p)[at]
-                                : bf16_lo(reinterpret_cast<const __attribute__((address_space(4))) uint16_t*>(p)[at]);
+        return scalar_scale<FMT>(sp[t], at);
       };
       if (kBlock) sc[t] = scale(kb);
       if constexpr (BORDER) after[t] = scale(kb + down[t]);
@@ -532,7 +539,7 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
     }
 #pragma unroll
     for (int t = 0; t < kScales; ++t) {
-      if (kBlock) s[t] = sc[t];
+      if (kBlock) s[t] = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sc[t])));   // stays scalar
       if constexpr (BORDER) s_after[t] = after[t];
       if (kMx) e[t] = ex[t] >> (8 * (4 * kb - min(4 * kb, ng - 4)) & 31);
     }
@@ -596,9 +603,28 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
       }
     }
   };
+  // Where a block of any of the groups reaches past k (the last one, or one past
+  // the slice), x's columns there become zeros once they have landed.
+  const auto no_columns = [&](int h, unsigned char* xb) __attribute__((always_inline)) {
+    bool any = false;
+#pragma unroll
+    for (int p = 0; p < KW; ++p) {
+      const int b = at.kb0 + p * blocks + here;
+      any |= b >= at.kb1 || (uint32_t)b * 128 + 128 > (uint32_t)k;
+    }
+    if (__builtin_expect(!any, 1)) return;
+    const int from = (int)min((uint32_t)k - min((uint32_t)kb * 128, (uint32_t)k), 128u) - (kTall ? 0 : 64 * h);   // columns there are
+#pragma unroll 1
+    for (int u = wave * kWave + lane_fresh(); u < 256 * MT; u += 256) {
+      const int row = u / kUnits, unit = u % kUnits ^ (kTall ? row & 15 : row >> 1 & 7);
+      if (8 * unit >= from) *reinterpret_cast<uint4*>(xb + 16 * u) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+  };
   // A block of 128 columns: its two steps' x are in x0 and x1, and
   // the two after them go to x2 and x0.
   const auto block = [&](unsigned char* x0, unsigned char* x1, unsigned char* x2) __attribute__((always_inline)) {
+    here = turned;
     const int next = next_block();   // the last block asks for one nobody takes
     take_w(kb, next);
     const auto first = [&](int n) __attribute__((always_inline)) {   // 4 MT places for 8 + MT loads
@@ -619,9 +645,11 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
       request_x(next, 0, x2);
       __builtin_amdgcn_sched_barrier(0);
     }
+    no_columns(0, x0);
     step(0, x0, first);
     land_and_meet<kWLoads + kXLoads>();           // younger than x1's: weights and x2's
     if (TW == 1) request_x(next, 1, x0);
+    no_columns(1, x1);
     step(1, x1, second);
     land_and_meet<kXLoads>();                     // the weights and x2's have landed
     kb = next;
@@ -648,7 +676,7 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
     __syncthreads();
     if (part > 0)
       each_sum<MT, TW>(acc, [&](int off, auto* from, int a) {
-        *reinterpret_cast<f32x4*>(sums + (part - 1) * slice_bytes<MT, TW>() + off + (threadIdx.x & 255) * 16) =
+        *reinterpret_cast<f32x4*>(ws + (part - 1) * slice_bytes<MT, TW>() + off + (threadIdx.x & 255) * 16) =
             f32x4{(*from)[a], (*from)[a + 1], (*from)[a + 2], (*from)[a + 3]};
       });
     __syncthreads();
@@ -656,7 +684,7 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
 #pragma unroll
       for (int p = 0; p < KW - 1; ++p)
         each_sum<MT, TW>(acc, [&](int off, auto* to, int a) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(sums + p * slice_bytes<MT, TW>() + off + threadIdx.x * 16);
+          const f32x4 v = *reinterpret_cast<const f32x4*>(ws + p * slice_bytes<MT, TW>() + off + threadIdx.x * 16);
 #pragma unroll
           for (int e = 0; e < 4; ++e) (*to)[a + e] += v[e];
         });
@@ -687,8 +715,8 @@ __global__ __launch_bounds__(256 * KW, TW == 2 || BORDER ? 2 : 4) void k_linear_
   if (!grid.at(32 * MT, c.m, (c.k + 127) / 128, at, id)) return;
   float* partial = grid.splits == 1 ? nullptr
                                     : reinterpret_cast<float*>(static_cast<char*>(c.workspace) + id * slice_bytes<MT, TW>());
-  linear_run<FMT, GATED, MT, TW, KW, BORDER>(c, at, partial, ws + part * 4 * 32 * TW * 128, xs0 + part * 32 * MT * 128,
-                                     xs1 + part * 32 * MT * 128, xs2 + part * 32 * MT * 128, ws);
+  linear_run<FMT, GATED, MT, TW, KW, BORDER>(c, at, partial, ws, xs0 + part * 32 * MT * 128,
+                                     xs1 + part * 32 * MT * 128, xs2 + part * 32 * MT * 128);
 }
 
 // The slices' sums added, in their order, and the tile's end.
@@ -801,9 +829,7 @@ __global__ __launch_bounds__(NW * kWave) void k_linear_stream(LinearCall c) {
     for (int t = 0; t < NT; ++t) {
       if (kBlock) {
         const auto scale = [&](int down) {
-          const char* p = sp[t] + (size_t)(down * nkb + kb) * (FMT == kFmtBlock ? 4 : 2);
-          return FMT == kFmtBlock ? *reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(p))
-                                  : bf16_lo(*reinterpret_cast<const __attribute__((address_space(4))) uint16_t*>(reinterpret_cast<uintptr_t>(p)));
+          return scalar_scale<FMT>(sp[t], down * nkb + kb);
         };
         slot.s[t][0] = scale(0);
         if (GATED) slot.s[t][1] = scale(two && (min(out_row(t), n_out - 1) + half(t)) / 128 < last_block ? 1 : 0);

@@ -653,7 +653,8 @@ fp8w_status fp8w_combine_experts(const uint16_t* y, int64_t slot_rows, const flo
  * alone, as the formula has it; gates and values beyond fp32's range pass as
  * the formula's limit.
  * Requires 0 <= m <= 2^30 (0: no launch), 1 <= n <= 2^28 (gated: even),
- * 16 <= k <= 2^28, k % 16 == 0, strides >= the columns and <= 2^31 - 1.
+ * 16 <= k <= 2^28, k % 16 == 0, strides >= the columns and <= 2^31 - 1 (x's
+ * <= 2^28).
  * Errors: NULL, SHAPE (also: workspace too small), UNSUPPORTED (format, act,
  * dtype), ALIGN, OVERLAP, HIP. */
 int64_t fp8w_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, fp8w_format format, fp8w_act act);

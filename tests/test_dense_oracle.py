@@ -184,7 +184,7 @@ def test_linear_refusals(L):
     for bad in (dict(fmt=5), dict(fmt=-1), dict(act=7), dict(act=-1), dict(bd=2), dict(yd=2)):
         assert call(**bad) == F.ERR_UNSUPPORTED, bad
     for bad in (dict(m=-1), dict(n=0), dict(k=0), dict(n=33, act=1), dict(n=33, act=6, res=None), dict(xs=56), dict(ys=31),
-                dict(rs=31), dict(xs=1 << 31), dict(ys=1 << 31), dict(rs=1 << 31), dict(m=(1 << 30) + 1),
+                dict(rs=31), dict(xs=1 << 31), dict(xs=(1 << 28) + 8), dict(ys=1 << 31), dict(rs=1 << 31), dict(m=(1 << 30) + 1),
                 dict(n=(1 << 28) + 1, ys=1 << 29, rs=1 << 29), dict(k=(1 << 28) + 16, xs=1 << 29),
                 dict(m=1 << 30, n=1 << 28, ys=1 << 28, res=None, x=1 << 62, y=1 << 61)):
         assert call(**bad) == F.ERR_SHAPE, bad

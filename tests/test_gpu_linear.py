@@ -162,6 +162,44 @@ def test_infinities_reach_their_row_alone(F, m):
     assert torch.equal(got[rest], want[rest]) and torch.isnan(got[m // 2]).all()
 
 
+@pytest.mark.parametrize("k", [16, 208, 336, 400, 1040])
+@pytest.mark.parametrize("m", [1, 20, 100, 300, 600])
+@pytest.mark.parametrize("fmt", ["block", "mx"])
+def test_infinities_in_any_column(F, fmt, m, k):
+    """A column that is read in the place of one past the end may hold an infinity: it adds nothing twice."""
+    codes, scales, _, sd = _weight(48, k, fmt)
+    codes[:] = 0x38 | codes & 0x80                                    # 1.0 or -1.0
+    cd = to_dev(codes)
+    for col in (0, k - 16, k - 8, k - 1):
+        xb = W.activation(2, m, k)
+        xb[m // 2, col] = 0x7F80
+        got = F.fp8w_linear(to_dev_bf16(xb), cd, sd, fmt).float().cpu().numpy()
+        assert np.array_equal(got[m // 2], np.where(codes[:, col] < 0x80, np.inf, -np.inf)), col
+        assert np.isfinite(np.delete(got, m // 2, 0)).all()
+
+
+def test_rows_beyond_4_gib(F):
+    """x, residual and y of rows far apart: the last begins past 2^32 bytes."""
+    m, k, n, pitch = 18, 256, 96, (1 << 27) + 8
+    codes, scales, cd, sd = _weight(n, k, "block")
+    xb = W.activation(3, m, k)
+    try:
+        wide = torch.empty((m - 1) * pitch + k + n, dtype=BF16, device=dev())
+    except torch.OutOfMemoryError:
+        pytest.skip("needs 5 GiB")
+    x, y = torch.as_strided(wide, (m, k), (pitch, 1)), torch.as_strided(wide, (m, n), (pitch, 1), k)
+    r = torch.randn(m, n, generator=torch.Generator(device="cuda").manual_seed(1), device=dev()).to(BF16)
+    x.copy_(to_dev_bf16(xb))
+    y.copy_(r)
+    want = F.fp8w_linear(x.contiguous(), cd, sd, residual=r)
+    x2, y2 = x.contiguous(), torch.empty(m, n, dtype=BF16, device=dev())
+    got = F.fp8w_linear(x, cd, sd, residual=r, y=y2)
+    assert torch.equal(got, want)
+    far = torch.as_strided(wide, (m, n), (pitch, 1), k)
+    assert torch.equal(F.fp8w_linear(x2, cd, sd, residual=far, y=far), want)
+    assert torch.equal(x, x2)
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu", "swiglu", "geglu"])
 @pytest.mark.parametrize("m", [1, 40])
 def test_activations_far_out(F, act, m):
