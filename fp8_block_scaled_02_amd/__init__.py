@@ -287,9 +287,10 @@ def _format_id(fmt: str) -> int:
 
 
 def _check_scales(torch, fmt, scales, n, k, what):
-    _require(scales, (_scale_dtype(torch, fmt),), "scales", len(scale_shape(fmt, n, k)))
-    if tuple(scales.shape) != scale_shape(fmt, n, k):
-        raise ValueError(f"{what}: {fmt} scales must be {scale_shape(fmt, n, k)}, got {tuple(scales.shape)}")
+    want = scale_shape(fmt, n, k)
+    _require(scales, (_scale_dtype(torch, fmt),), "scales", len(want))
+    if scales.shape != want:
+        raise ValueError(f"{what}: {fmt} scales must be {want}, got {tuple(scales.shape)}")
 
 
 # --------------------------------------------------------------- quantize --
@@ -806,7 +807,7 @@ def _buffer(t, shape, dtype, device, what: str):
 
 def _on_current_device(*tensors) -> None:
     """Calls go to the current device: tensors of another one are refused."""
-    current = _torch().cuda.current_device()
+    current = _torch()._C._cuda_getDevice()   # there are GPU tensors: no first use to wait for
     for t in tensors:
         if t is not None and t.get_device() != current:
             raise ValueError(f"tensors must be on the current device (cuda:{current}), got {t.device}")
@@ -992,20 +993,22 @@ LINEAR_ACT_IDS = {"none": 0, "swiglu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, 
 
 def _rows_of(t, dtypes, shape, what: str) -> int:
     """The row stride of a matrix whose rows are contiguous, after a check."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{what}: must be a GPU tensor (libfp8w has no CPU path)")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{what}: expected shape {shape or '[rows, columns]'}, got {tuple(t.shape)}")
-    rows, cols = t.shape
-    stride = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or stride < cols:
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
+        raise ValueError(f"{what}: expected shape {shape or '[rows, columns]'}, got {tuple(size)}")
+    rows, cols = size
+    down, along = t.stride()
+    if rows <= 1:
+        down = cols
+    if (cols > 1 and along != 1) or down < cols:
         raise ValueError(f"{what}: rows must be contiguous and must not overlap")
-    return stride
+    return down
 
 
 def fp8w_linear(x, codes, scales, fmt: str = "block", bias=None, act: str = "none", residual=None, y=None,
@@ -1018,15 +1021,16 @@ def fp8w_linear(x, codes, scales, fmt: str = "block", bias=None, act: str = "non
     residual itself."""
     torch = _torch()
     bf16 = _bf16_like(torch)
+    outputs = (*bf16, torch.float32)
     x_stride = _rows_of(x, bf16, None, "x")
     _require(codes, (torch.uint8,), "codes", 2)
     if act not in LINEAR_ACT_IDS:
         raise ValueError(f"unknown act {act!r}")
     fid, aid = _format_id(fmt), LINEAR_ACT_IDS[act]
     m, k = x.shape
-    n = codes.shape[0]
-    if codes.shape[1] != k:
-        raise ValueError(f"fp8w_linear: x has {k} columns, the weights {codes.shape[1]}")
+    n, columns = codes.shape
+    if columns != k:
+        raise ValueError(f"fp8w_linear: x has {k} columns, the weights {columns}")
     _check_scales(torch, fmt, scales, n, k, "fp8w_linear")
     gated = act in ("swiglu", "geglu")
     if gated and n % 2:
@@ -1034,7 +1038,7 @@ def fp8w_linear(x, codes, scales, fmt: str = "block", bias=None, act: str = "non
     shape = (m, n // 2 if gated else n)
     bias_dtype = 0
     if bias is not None:
-        _require(bias, (*bf16, torch.float32), "bias", 1)
+        _require(bias, outputs, "bias", 1)
         if bias.shape[0] != n:
             raise ValueError(f"bias: expected shape {(n,)}, got {tuple(bias.shape)}")
         bias_dtype = 1 if bias.dtype is torch.float32 else 0
@@ -1043,7 +1047,7 @@ def fp8w_linear(x, codes, scales, fmt: str = "block", bias=None, act: str = "non
         y = torch.empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=x.device)
     elif out_dtype is not None and y.dtype is not out_dtype:
         raise TypeError(f"y: dtype {y.dtype} is not out_dtype {out_dtype}")
-    y_stride = _rows_of(y, (*bf16, torch.float32), shape, "y")
+    y_stride = _rows_of(y, outputs, shape, "y")
     _on_current_device(x, codes, scales, bias, residual, y, workspace)
     if workspace is not None:
         need = _workspace_bytes(workspace)
