@@ -373,8 +373,9 @@ constexpr int64_t slice_bytes() { return (int64_t)TW * MT * 4 * 4096; }
 //   * Weights: a wave's rows of a 128-column block are its own 4 * TW KB.  At
 //     the start of a block it takes them into registers in the A layout and
 //     asks for the next block at once: a block's time to arrive.
-//   * x: half of the rows (of 32: half of the columns) of the block for all
-//     four waves, three buffers, asked for two steps ahead; one barrier a step.
+//   * x: half of the columns of the block (64-row tiles of four waves: half of
+//     the rows) for all four waves, three buffers, asked for two steps ahead;
+//     one barrier a step.
 // The waits name how many younger loads may still be on their way; a wait
 // for everything would put the memory's latency into every step.
 //
@@ -384,10 +385,20 @@ constexpr int64_t slice_bytes() { return (int64_t)TW * MT * 4 * 4096; }
 // row / 2 or the row, so that any 16 consecutive rows fall into 16 different
 // bank groups.
 //
-// A block scale multiplies a block's sums of 32 rows at a time (sums of all
-// rows would need as many registers as the accumulators; steps of 64 columns
-// for all rows, twice the multiplications, took LEFT_US).  MX scales multiply
-// the codes as they become bf16 (exact); row and tensor scales the results.
+// A block scale multiplies a step's sums of 32 rows at a time (sums of all rows
+// would need as many registers as the accumulators).  With half of the rows a
+// step that is once for 128 columns instead of twice: 512 x 6144 x 4096 44 us,
+// 46 otherwise; 128-row tiles have no registers for it (a block's operands are
+// 64 of them), and spilled 300.  MX scales multiply the codes as they become
+// bf16 (exact); row and tensor scales the results.
+//
+// Measured: 2048 x 24576 x 4096 gated 409 us with block scales (1010 TFLOP/s),
+// 335 with row scales (1230; the library's bf16 product of dequantized weights
+// 320); 1777 x 4096 x 12288 row scales 172 (1040; 158).  There a wave's
+// products of a block take 2048 clocks, and its VALU 2000 (block) or 900 (row):
+// what is missing is their overlap at two waves a SIMD.  203 x 6144 x 4096 MX
+// 26 us: 192 tiles' 16 rounds of loads, products and barriers, 1.6 us each.
+// 32 x 24576 x 4096 gated 25.6 us: HBM, 3.9 TB/s.
 template <int FMT, bool GATED, int MT, int TW, int KW, bool BORDER>
 __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile& at, float* partial, unsigned char* ws,
                                            unsigned char* xs0, unsigned char* xs1, unsigned char* xs2) {
@@ -758,6 +769,12 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearCall c, LinearGrid gr
 // to wait for one block alone: blocks past a wave's last one are zeros.
 // (Weights straight to LDS: the compiler then waits for every load before it
 // uses one of x's.)
+//
+// Bound by HBM and, where weights are few, by launch, first loads and the join:
+// 1 x 6144 x 4096 8.2 us (3.1 TB/s; a bare read of as much 5.7), 16 x 4096 x
+// 12288 13.9 and 2 for the second launch, 8 x 151936 x 2048 52.6 (5.9 TB/s).
+// Non-temporal loads and workgroups that start at different columns are worth
+// a quarter: a bare read of 24576 x 4096 took 21.9 us without, 16.9 with both.
 template <int FMT, bool GATED, int NT, int MT, int NW, int D>
 __global__ __launch_bounds__(NW * kWave) void k_linear_stream(LinearCall c) {
   constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
