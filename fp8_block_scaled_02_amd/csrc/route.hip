@@ -190,7 +190,10 @@ __device__ __forceinline__ void shut_groups(const RouteArgs& a, const float (&x)
     double score[R];
     scores<R>(a, x, top, score);
 #pragma unroll
-    for (int r = 0; r < R; ++r) meet(x[r] > -__builtin_inff() ? score[r] : ninf, ninf);
+    for (int r = 0; r < R; ++r) {
+      const double s = a.score == 0 && x[r] == top ? 1.0 : score[r];   // infinities next to each other have no difference
+      meet(x[r] > -__builtin_inff() ? s : ninf, ninf);
+    }
   } else {
 #pragma unroll
     for (int r = 0; r < R; ++r) meet((double)key[r], ninf);

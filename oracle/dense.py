@@ -145,7 +145,9 @@ def route_grouped(logits, top_k: int, groups: int, top_groups: int, by: str = "m
             continue
         safe = np.where(live, x[r], 0.0)
         if score == "softmax":
-            p = np.where(live, np.exp(np.minimum(safe - safe[live].max(), 0.0)), 0.0)
+            top = safe[live].max()
+            with np.errstate(invalid="ignore"):
+                p = np.where(live, np.exp(np.where(safe == top, 0.0, np.minimum(safe - top, 0.0))), 0.0)
             p = p / p.sum()
         else:
             p = np.where(live, _sigmoid(safe), 0.0)

@@ -143,3 +143,19 @@ def test_repeatable_on_another_stream_and_in_a_graph(F):
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(buf, F.fp8w_route_experts(x, 4, **kw))), i
+
+
+@pytest.mark.parametrize("by", ["max", "top2"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("t", [3, 40])
+def test_an_infinite_logit_opens_its_group(F, by, score, t):
+    """The choice is defined, the weights are not."""
+    x = _logits(t, 64)
+    x[0, 41], x[1, 3] = np.inf, np.inf
+    x[1, 60:62] = np.inf
+    r = F.fp8w_route_experts(x, 4, score, groups=8, top_groups=2, group_score=by)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        ids = D.route_grouped(x.double().cpu().numpy(), 4, 8, 2, by, score)[0]
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    assert 41 in ids[0]
