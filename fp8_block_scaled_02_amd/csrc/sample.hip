@@ -801,12 +801,17 @@ __device__ __forceinline__ float2 range_of(const Logits<T, N>& logits, float2* w
   return make_float2(alike(most), alike(least));
 }
 
-// The same of a row whose pieces' are known.
-__device__ __forceinline__ float2 joined_range(const SampleArgs& a, int t) {
-  float2 r = a.ranges[(size_t)t * a.segs];
-  for (int i = 1; i < a.segs; ++i) {
-    const float2 o = a.ranges[(size_t)t * a.segs + i];
-    r = make_float2(__builtin_fmaxf(r.x, o.x), __builtin_fminf(r.y, o.y));
+// The same of a row whose pieces' are known: a lane asks for one of them, and
+// they meet once something else is on its way too.
+__device__ __forceinline__ float2 piece_range(const SampleArgs& a, int t) {
+  const int lane = threadIdx.x & (kSmPieces - 1);
+  return a.ranges[(size_t)t * a.segs + (lane < a.segs ? lane : 0)];
+}
+__device__ __forceinline__ float2 joined_range(float2 r) {
+#pragma unroll
+  for (int off = 1; off < kSmPieces; off <<= 1) {
+    r.x = __builtin_fmaxf(r.x, __shfl_xor(r.x, off));
+    r.y = __builtin_fminf(r.y, __shfl_xor(r.y, off));
   }
   return make_float2(alike(r.x), alike(r.y));
 }
@@ -824,10 +829,11 @@ template <typename T>
 __global__ __launch_bounds__(kSmThreads) void k_sample_bins(SampleArgs a) {
   __shared__ uint64_t words[kSmBins];
   const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs;
-  const float2 range = joined_range(a, t);
-  if (range.x == -__builtin_inff()) return;
-  const Logits<T, kSmThreads> logits(a, t, seg);
+  const float2 piece = piece_range(a, t);
   const Settings set(a, t);
+  const Logits<T, kSmThreads> logits(a, t, seg);
+  const float2 range = joined_range(piece);
+  if (range.x == -__builtin_inff()) return;
   const RowScale scale(range.x, range.y, set.temperature, a);
   fill(logits, scale, words, !set.few, [](float, uint32_t b) { return b; });
   for (int b = threadIdx.x; b < kSmBins; b += kSmThreads) a.words[(size_t)blockIdx.x * kSmBins + b] = words[b];
@@ -843,7 +849,23 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
   __shared__ Shared<N> s;
   const int t = blockIdx.x, tid = threadIdx.x;
   const Logits<T, N> logits(a, t, -1);
-  const float2 range = PIECES ? joined_range(a, t) : range_of(logits, s.wave_range);
+  // All that is known beforehand is asked for at once: each is a way to memory.
+  float2 range;
+  uint64_t words[PIECES ? kPer : 1][kSmPieces];
+  if constexpr (PIECES) {
+    range = piece_range(a, t);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+      for (int i = 0; i < kSmPieces; ++i)
+        words[j][i] = a.words[((size_t)t * a.segs + (i < a.segs ? i : 0)) * kSmBins + tid + j * N];
+  }
+  const Settings set(a, t);
+  const float u = a.uniforms[t];
+  if constexpr (PIECES)
+    range = joined_range(range);
+  else
+    range = range_of(logits, s.wave_range);
   const float most = range.x, least = range.y;
   if (most == -__builtin_inff()) {   // masked throughout
     if (tid == 0) {
@@ -853,21 +875,16 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
     }
     return;
   }
-  const Settings set(a, t);
   Row<T, N> row{a, t, s, logits, RowScale(most, least, set.temperature, a), ordered(most)};
   bool weights = !set.few;
   uint32_t live = 0;
   if constexpr (PIECES) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int b = tid + j * N;
-      uint64_t words[kSmPieces], word = 0;
+      uint64_t word = 0;
 #pragma unroll
-      for (int i = 0; i < kSmPieces; ++i)   // all of them on their way at once
-        words[i] = a.words[((size_t)t * a.segs + (i < a.segs ? i : 0)) * kSmBins + b];
-#pragma unroll
-      for (int i = 0; i < kSmPieces; ++i) word += i < a.segs ? words[i] : 0;
-      s.mass[0][b] = word;
+      for (int i = 0; i < kSmPieces; ++i) word += i < a.segs ? words[j][i] : 0;
+      s.mass[0][tid + j * N] = word;
     }
     __syncthreads();
   } else {
@@ -909,7 +926,7 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
       by = By::kKey;
       goal = cut.key < key ? key : 0;
     } else if (step == 3) {
-      const double at = __builtin_floor((double)a.uniforms[t] * (double)cut.mass);
+      const double at = __builtin_floor((double)u * (double)cut.mass);
       const uint64_t below = !(at > 0.0) ? 0 : at >= (double)cut.mass ? cut.mass - 1 : (uint64_t)at;
       goal = (below < cut.mass ? below : cut.mass - 1) + 1;
     }
