@@ -1000,7 +1000,9 @@ struct LinearPlan {
 //     high ones did not: 128 x 6144 x 4096 17.7, 21 with mt = 2 and two slices.
 //   While there is no more than a tile a CU, eight waves share its k: 203 x
 //     6144 x 4096 25, 29 with four, 30 with four and two slices; 64 x 24576 x
-//     4096 30 and 34; 512 x 6144 x 4096 (384 tiles) 44 with either.
+//     4096 30 and 34; 512 x 6144 x 4096 (384 tiles) 44 with either.  With mt = 1
+//     and 96 tiles or more sixteen waves: 32 x 24576 x 4096 25.9, 27.3 with
+//     eight, 32 x 12288 x 4096 20 and 21; 17 x 6144 x 4096 (48) 14.4 and 13.9.
 // Fewer tiles than CUs are cut in slices of k, of eight blocks (streaming: 32)
 // at least, and a second launch adds these up: 64 x 4096 x 12288 with eight
 // slices 24.6, four 28; 32 x 4096 x 12288 with eight 20.5, one 35.  More than
@@ -1028,7 +1030,8 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, int format, int act) {
     const int64_t wide = (m + 127) / 128 * ((groups + 1) / 2);
     p.mt = m <= 32 || (flat > 128 && flat <= kFill) ? 1 : m <= 512 || wide < 160 || second % 32 != 0 ? 2 : 4;
     p.tw = p.mt == 4 ? 2 : 1;
-    p.kw = p.mt < 4 && (m + 32 * p.mt - 1) / (32 * p.mt) * groups <= kFill ? 2 : 1;
+    const int64_t tiles = (m + 32 * p.mt - 1) / (32 * p.mt) * groups;
+    p.kw = p.mt == 4 || tiles > kFill ? 1 : p.mt == 1 && tiles >= 96 ? 4 : 2;
     p.border = second % 16 != 0;
     p.height = 32 * p.mt;
     p.width = 64 * p.tw * outputs;
@@ -1083,6 +1086,7 @@ hipError_t launch_plan(const LinearCall& c, const LinearPlan& p, hipStream_t str
   if (p.kind == LinearPlan::kStream) return launch_stream<FMT, GATED>(c, p, stream);
   if (p.mt == 4) return launch_tile<FMT, GATED, 4, 2, 1>(c, p, stream);
   if (p.mt == 2) return p.kw == 2 ? launch_tile<FMT, GATED, 2, 1, 2>(c, p, stream) : launch_tile<FMT, GATED, 2, 1, 1>(c, p, stream);
+  if (p.kw == 4) return launch_tile<FMT, GATED, 1, 1, 4>(c, p, stream);
   return p.kw == 2 ? launch_tile<FMT, GATED, 1, 1, 2>(c, p, stream) : launch_tile<FMT, GATED, 1, 1, 1>(c, p, stream);
 }
 

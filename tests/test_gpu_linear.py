@@ -103,7 +103,7 @@ def test_gated_halves(F, fmt, half, m):
 
 
 @pytest.mark.parametrize("fmt", ["block", "block_bf16", "mx"])
-@pytest.mark.parametrize("m,half,k", [(20, 16500, 80), (20, 70, 1040), (100, 2001, 272), (100, 3001, 144), (270, 130, 2064),
+@pytest.mark.parametrize("m,half,k", [(20, 16500, 80), (20, 70, 1040), (100, 2001, 272), (100, 3001, 144), (30, 6801, 400), (30, 6816, 656), (270, 130, 2064),
                                       (270, 7001, 144), (600, 100, 400), (600, 1111, 272), (600, 1120, 272), (520, 64, 4112)])
 def test_gated_halves_of_many_sizes(F, fmt, m, half, k):
     """Every tiling, with halves that start at the end of a scale block, of 32 or 16 rows, and anywhere."""
@@ -112,7 +112,7 @@ def test_gated_halves_of_many_sizes(F, fmt, m, half, k):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("m,n,k", [(2, 300, 144), (1, 3000, 400), (3, 65600, 48), (12, 16400, 144), (16, 130, 8208), (20, 33000, 80),
-                                   (100, 6100, 272), (70, 500, 2064), (150, 400, 1296), (500, 8400, 144), (513, 300, 656), (700, 200, 3104)])
+                                   (100, 6100, 272), (25, 12400, 592), (33, 7000, 1552), (70, 500, 2064), (150, 400, 1296), (500, 8400, 144), (513, 300, 656), (700, 200, 3104)])
 def test_sizes_of_every_kernel(F, fmt, m, n, k):
     _check(F, m, n, k, fmt, "silu", F32, True)
 
