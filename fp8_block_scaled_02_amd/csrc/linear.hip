@@ -376,6 +376,10 @@ constexpr int64_t slice_bytes() { return (int64_t)TW * MT * 4 * 4096; }
 //   * x: half of the columns of the block (64-row tiles of four waves: half of
 //     the rows) for all four waves, three buffers, asked for two steps ahead;
 //     one barrier a step.
+// Eight waves (a CU has one such workgroup) have room for two blocks of each,
+// weights two blocks ahead and one barrier a block: 203 x 6144 x 4096 MX 26.9
+// us, 28.9 without on the same card; 64 x 24576 x 4096 29.0 and 32.5; 512 x 4096
+// x 12288 64 and 69.5; with few rounds it gives nothing (384 x 4096 x 4096 25.7).
 // The waits name how many younger loads may still be on their way; a wait
 // for everything would put the memory's latency into every step.
 //
@@ -401,13 +405,15 @@ constexpr int64_t slice_bytes() { return (int64_t)TW * MT * 4 * 4096; }
 // 32 x 24576 x 4096 gated 25.6 us: HBM, 3.9 TB/s.
 template <int FMT, bool GATED, int MT, int TW, int KW, bool BORDER>
 __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile& at, float* partial, unsigned char* ws,
-                                           unsigned char* xs0, unsigned char* xs1, unsigned char* xs2) {
+                                           unsigned char* xs0, unsigned char* xs1, unsigned char* xs2,
+                                           unsigned char* xs3, unsigned char* ws1) {
   constexpr bool kBlock = FMT == kFmtBlock || FMT == kFmtBlockBf16;
   constexpr bool kMx = FMT == kFmtMx;
   using Rows = WaveRows<GATED, TW>;
   constexpr int kRows = Rows::kRows;
   constexpr int kXLoads = MT;          // x loads of a wave and step (1 KB each)
   constexpr int kWLoads = 4 * TW;      // weight loads of a wave and block
+  constexpr bool kDeep = KW == 2;      // two blocks of weights and of x at a time
   constexpr bool kTall = MT == 2 && KW == 1;   // a step is half of the rows, else half of the columns
   constexpr int kStepQ = kTall ? MT / 2 : MT, kStepU = kTall ? 8 : 4;   // rows / 32, columns / 16
   constexpr int kUnits = 2 * kStepU, kPerLoad = kWave / kUnits;        // 16 bytes of a row, rows of a load
@@ -433,7 +439,8 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
   };
   // (By the wave's number in the workgroup: as a part's four waves' the compiler
   // takes what is on its way to x's LDS to be on its way here.)
-  unsigned char* wl = ws + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * kRows * 128;
+  unsigned char* const wl = ws + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * kRows * 128;
+  unsigned char* const wl1 = ws1 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * kRows * 128;   // (kDeep)
 
   // Load j of a wave's weights brings rows 8j + l/8; LDS place l%8 of a row
   // holds its unit (l%8) ^ (row / 2 % 8), so j odd the unit of j even ^ 4.
@@ -446,17 +453,17 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
   const int wu = (lane & 7) ^ (lane >> 4);
   uint32_t wrow = (uint32_t)(lane >> 3) * (uint32_t)k;
   int wcol = 16 * wu;
-  const auto load_w = [&](int kb, int j) __attribute__((always_inline)) {
+  const auto load_w = [&](int kb, int j, unsigned char* to) __attribute__((always_inline)) {
     asm volatile("" : "+v"(wrow), "+v"(wcol)::"memory");
     const uint32_t c0 = (uint32_t)kb * 128 + (uint32_t)(wcol ^ (j & 1) * 64);
     const int row = min(w.out_row(8 * j), n_out - 1);
     const uint32_t within = (uint32_t)min(n_out - 1 - row, 7) * (uint32_t)k;
-    stage16(c.codes + (size_t)(row + w.half(8 * j)) * k + (min(wrow, within) + min(c0, (uint32_t)k - 16)), wl + j * 1024);
+    stage16(c.codes + (size_t)(row + w.half(8 * j)) * k + (min(wrow, within) + min(c0, (uint32_t)k - 16)), to + j * 1024);
     asm volatile("" ::: "memory");
   };
-  const auto request_w = [&](int kb) __attribute__((always_inline)) {
+  const auto request_w = [&](int kb, unsigned char* to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < kWLoads; ++j) load_w(kb, j);
+    for (int j = 0; j < kWLoads; ++j) load_w(kb, j, to);
   };
   // x rows a wave stages: kPerLoad (MT * wave + j) + l / kUnits of the step's,
   // place l % kUnits with unit (l % kUnits) ^ row % 16 (of 8: row / 2 % 8 = 4
@@ -534,7 +541,7 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
     if constexpr (BORDER) return 8 * (v >> 2 & 1) + 4 * hh + (v & 3) < border[run] ? s[run] : s_after[run];
     return s[run];
   };
-  const auto take_w = [&](int kb, int next) __attribute__((always_inline)) {
+  const auto take_w = [&](int kb, int next, const unsigned char* wl) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < TW; ++t)
 #pragma unroll
@@ -637,13 +644,13 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
   const auto block = [&](unsigned char* x0, unsigned char* x1, unsigned char* x2) __attribute__((always_inline)) {
     here = turned;
     const int next = next_block();   // the last block asks for one nobody takes
-    take_w(kb, next);
+    take_w(kb, next, wl);
     const auto first = [&](int n) __attribute__((always_inline)) {   // 4 MT places for 8 + MT loads
       const int to = (n + 1) * (kWLoads + kXLoads) / (4 * MT);
 #pragma unroll
       for (int j = n * (kWLoads + kXLoads) / (4 * MT); j < to; ++j) {
         if (j < kWLoads)
-          load_w(next, j);
+          load_w(next, j, wl);
         else
           load_x(next, 0, j - kWLoads, x2);
       }
@@ -652,7 +659,7 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
       if (n % 4 == 0) load_x(next, 1, n / 4, x0);
     };
     if (TW == 1) {
-      request_w(next);
+      request_w(next, wl);
       request_x(next, 0, x2);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -666,20 +673,53 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
     kb = next;
   };
 
+  // The same with room for two: its steps' x are in x0 and x1, the next block's
+  // go to y0 and y1 and the second next's weights where its own are, so that
+  // weights have two blocks' time to arrive, and one barrier does.
+  const auto deep_block = [&](unsigned char* x0, unsigned char* x1, unsigned char* y0, unsigned char* y1,
+                              unsigned char* w) __attribute__((always_inline)) {
+    const auto none = [](int) {};
+    here = turned;
+    const int next = next_block(), after_next = turned + 1 < blocks ? turned + 1 : 0;
+    take_w(kb, next, w);
+    request_x(next, 0, y0);
+    request_x(next, 1, y1);
+    request_w(first_block + after_next < at.kb1 ? first_block + after_next : nkb, w);
+    __builtin_amdgcn_sched_barrier(0);
+    no_columns(0, x0);
+    no_columns(1, x1);
+    step(0, x0, none);
+    step(1, x1, none);
+    land_and_meet<kWLoads>();                     // all but the weights just asked for
+    kb = next;
+  };
+
   request_s(kb);
-  request_w(kb);
+  request_w(kb, wl);
   request_x(kb, 0, xs0);
   request_x(kb, 1, xs1);
-  land_and_meet<kXLoads>();
   int left = blocks;
+  if constexpr (kDeep) {
+    const int second = turned + 1 < blocks ? turned + 1 : 0;
+    request_w(first_block + second < at.kb1 ? first_block + second : nkb, wl1);
+    land_and_meet<kWLoads>();
 #pragma unroll 1
-  for (; left > 2; left -= 3) {
-    block(xs0, xs1, xs2);
-    block(xs2, xs0, xs1);
-    block(xs1, xs2, xs0);
+    for (; left > 1; left -= 2) {
+      deep_block(xs0, xs1, xs2, xs3, wl);
+      deep_block(xs2, xs3, xs0, xs1, wl1);
+    }
+    if (left > 0) deep_block(xs0, xs1, xs2, xs3, wl);
+  } else {
+    land_and_meet<kXLoads>();
+#pragma unroll 1
+    for (; left > 2; left -= 3) {
+      block(xs0, xs1, xs2);
+      block(xs2, xs0, xs1);
+      block(xs1, xs2, xs0);
+    }
+    if (left > 0) block(xs0, xs1, xs2);
+    if (left > 1) block(xs2, xs0, xs1);
   }
-  if (left > 0) block(xs0, xs1, xs2);
-  if (left > 1) block(xs2, xs0, xs1);
   vm_wait_all();   // nothing may land in LDS that is no longer ours
 
   if constexpr (KW > 1) {   // the groups' sums meet in the first's registers, in their order
@@ -713,13 +753,16 @@ __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile
 }
 
 template <int FMT, bool GATED, int MT, int TW, int KW, bool BORDER>
-__global__ __launch_bounds__(256 * KW, TW == 2 || BORDER ? 2 : 4) void k_linear_tile(LinearCall c, LinearGrid grid) {
+__global__ __launch_bounds__(256 * KW, TW == 2 || KW == 2 || BORDER ? 2 : 4) void k_linear_tile(LinearCall c, LinearGrid grid) {
   // separate arrays: the compiler then knows that reads of one need not wait
   // for what is on its way into another
   __shared__ __attribute__((aligned(16))) unsigned char ws[KW * 4 * 32 * TW * 128];
   __shared__ __attribute__((aligned(16))) unsigned char xs0[KW * 32 * MT * 128];
   __shared__ __attribute__((aligned(16))) unsigned char xs1[KW * 32 * MT * 128];
   __shared__ __attribute__((aligned(16))) unsigned char xs2[KW * 32 * MT * 128];
+  // (KW = 2 alone)
+  __shared__ __attribute__((aligned(16))) unsigned char xs3[KW * 32 * MT * 128];
+  __shared__ __attribute__((aligned(16))) unsigned char ws1[KW * 4 * 32 * TW * 128];
   const int part = KW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / 256);
   LinearTile at;
   int64_t id;
@@ -727,7 +770,8 @@ __global__ __launch_bounds__(256 * KW, TW == 2 || BORDER ? 2 : 4) void k_linear_
   float* partial = grid.splits == 1 ? nullptr
                                     : reinterpret_cast<float*>(static_cast<char*>(c.workspace) + id * slice_bytes<MT, TW>());
   linear_run<FMT, GATED, MT, TW, KW, BORDER>(c, at, partial, ws, xs0 + part * 32 * MT * 128,
-                                     xs1 + part * 32 * MT * 128, xs2 + part * 32 * MT * 128);
+                                     xs1 + part * 32 * MT * 128, xs2 + part * 32 * MT * 128,
+                                     KW == 2 ? xs3 + part * 32 * MT * 128 : xs0, KW == 2 ? ws1 : ws);
 }
 
 // The slices' sums added, in their order, and the tile's end.
