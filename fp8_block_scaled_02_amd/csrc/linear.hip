@@ -396,13 +396,13 @@ constexpr int64_t slice_bytes() { return (int64_t)TW * MT * 4 * 4096; }
 // 64 of them), and spilled 300.  MX scales multiply the codes as they become
 // bf16 (exact); row and tensor scales the results.
 //
-// Measured: 2048 x 24576 x 4096 gated 409 us with block scales (1010 TFLOP/s),
+// Measured: 2048 x 24576 x 4096 gated 400-410 us with block scales (1010 TFLOP/s),
 // 335 with row scales (1230; the library's bf16 product of dequantized weights
 // 320); 1777 x 4096 x 12288 row scales 172 (1040; 158).  There a wave's
 // products of a block take 2048 clocks, and its VALU 2000 (block) or 900 (row):
 // what is missing is their overlap at two waves a SIMD.  203 x 6144 x 4096 MX
-// 26 us: 192 tiles' 16 rounds of loads, products and barriers, 1.6 us each.
-// 32 x 24576 x 4096 gated 25.6 us: HBM, 3.9 TB/s.
+// 24-28 us by card: 192 tiles' 16 rounds of loads, products and barriers, 1.6 us
+// each.  32 x 24576 x 4096 gated 25.9 us: HBM, 3.9 TB/s.
 template <int FMT, bool GATED, int MT, int TW, int KW, bool BORDER>
 __device__ __forceinline__ void linear_run(const LinearCall& c, const LinearTile& at, float* partial, unsigned char* ws,
                                            unsigned char* xs0, unsigned char* xs1, unsigned char* xs2,
