@@ -435,6 +435,9 @@ struct Row {
   // stands before them
   uint32_t lo = 1, hi = 0, bin0 = 0, bin1 = 0, before = 0, length = 0;
   uint64_t before_mass = 0, mass = 0;
+  // what all bins, and all parts of one, hold
+  uint32_t all_count[2] = {0, 0};
+  uint64_t all_mass[2] = {0, 0};
 
   // The smallest bits for which `yes` holds, as it does for the largest logit's
   // and for all above the answer: 64 places of the range at a time, the same
@@ -467,8 +470,8 @@ struct Row {
   // those of bin `only`, or each of the bin that its place names.
   __device__ __forceinline__ void sum_up(int at, bool weights, uint32_t only = kSmBins) {
     const int tid = threadIdx.x;
-    uint32_t n[kPer], all, count = 0;
-    uint64_t m[kPer], all_mass, mass = 0;
+    uint32_t n[kPer], count = 0;
+    uint64_t m[kPer], mass = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int b = tid * kPer + j;
@@ -476,8 +479,9 @@ struct Row {
       count += n[j] = scale.count_of(word);
       mass += m[j] = weights ? scale.mass_of(word, only < kSmBins ? only : b) : 0;
     }
-    count = block_prefix<N>(count, s.wave_count, all);
-    mass = weights ? block_prefix<N>(mass, s.wave_mass, all_mass) : 0;
+    count = block_prefix<N>(count, s.wave_count, all_count[at]);
+    all_mass[at] = 0;
+    if (weights) mass = block_prefix<N>(mass, s.wave_mass, all_mass[at]);
 #pragma unroll
     for (int j = kPer - 1; j >= 0; --j) {
       const int b = tid * kPer + j;
@@ -494,17 +498,22 @@ struct Row {
   int turn = 0;
   __device__ __forceinline__ uint32_t& answer() { return s.found[turn ^= 1]; }
 
-  // The first bin that reaches the goal, which one does, with `n0` and `m0`
-  // before them all.
+  // The first bin that reaches the goal, with `n0` and `m0` before them all.
+  // Where none does, the last that holds a token: a goal may come from sums that
+  // were rounded otherwise, as those of a bin's parts and of the bin are.
   __device__ __forceinline__ uint32_t bin_of(int at, By by, uint64_t goal, uint32_t n0, uint64_t m0) {
     const int first = threadIdx.x * kPer;
     uint32_t& found = answer();
+    if (by == By::kMass && goal > m0 + all_mass[at]) {
+      by = By::kCount;
+      goal = n0 + all_count[at];
+    }
     const auto upto = [&](int b) { return b < 0 ? (by == By::kCount ? n0 : m0) : by == By::kCount ? n0 + s.count[at][b] : m0 + s.mass[at][b]; };
     uint64_t less = upto(first - 1);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const uint64_t now = upto(first + j);
-      if ((less < goal && now >= goal) || (first + j == kSmBins - 1 && now < goal)) found = first + j;
+      if (less < goal && now >= goal) found = first + j;
       less = now;
     }
     __syncthreads();
@@ -675,7 +684,7 @@ struct Row {
       __syncthreads();
       n = alike(found);
     }
-    if (n == 0) return Place{before, before_mass, top, -1};
+    if (n == 0) return Place{before, before_mass, (uint32_t)goal, -1};   // bits that none of these has
     const uint64_t e = alike(s.list[n - 1]);
     return Place{before + n, alike(s.list_mass[n - 1]), (uint32_t)(e >> 32), (int32_t)~(uint32_t)e};
   }
@@ -718,7 +727,7 @@ struct Row {
     uint64_t m0 = b ? alike(s.mass[0][b - 1]) : 0;
     const uint32_t first = b;
     uint32_t from = kFirstLive, to = top, b0 = b;
-    if (n0 + n <= kSmSmall || (n0 + n <= kSmCap && alike(s.mass[0][kSmBins - 1]) == 0)) {
+    if (n0 + n <= kSmSmall || (n0 + n <= kSmCap && all_mass[0] == 0)) {
       // all that stands before it too: the next goal is likely among them, and
       // is where no weights were counted
       b0 = 0;
@@ -893,7 +902,7 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
 #pragma unroll 1
   for (;;) {
     row.sum_up(0, weights);
-    live = alike(s.count[0][kSmBins - 1]);
+    live = row.all_count[0];
     if (weights) break;
     // more equal ones than the list holds: weights after all
     const uint32_t want = set.k < live ? (uint32_t)set.k : live;
@@ -903,13 +912,21 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
   }
   const int64_t k = set.k;
   // The places that cut the order, then the one that is drawn, by one copy of
-  // the search.  (What long functions need is taken before: the compiler would
-  // keep their constants in registers throughout.)
+  // the search.  Sums of the same tokens may differ by their roundings (a bin's
+  // and its parts', a crowd's of equal ones): no place behind a cut is taken for
+  // what is before it.  A uniform of 1 or more leaves no room for them and goes by
+  // counts, to the last kept token whose weight is not zero.  (What long
+  // functions need is taken before: the compiler would keep their constants in
+  // registers throughout.)
   double bound = 0.0;
   if (set.low > 0.0f) bound = log((double)set.low) * (double)set.temperature;
-  Place cut{live, alike(s.mass[0][kSmBins - 1]), ordered(least), -1}, drawn = cut;
+  Place cut{live, row.all_mass[0], ordered(least), -1}, drawn = cut;
+  // The steps: top-k, top-p, min-p, the draw; and seldom, by counts, the last
+  // place with weight, and the place that is drawn.
+  uint32_t end = 0;
+  int steps = alike((int)(u >= 1.0f)) ? 6 : 4;
 #pragma unroll 1
-  for (int step = 0; step < 4; ++step) {
+  for (int step = 0; step < steps; ++step) {
     By by = By::kMass;
     uint64_t goal = 0;   // none
     if (step == 0 && (set.few || (k > 0 && k < live))) {
@@ -918,21 +935,33 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
     } else if (step == 1 && set.p < 1.0f) {
       const double at = __builtin_ceil((double)set.p * (double)cut.mass);
       goal = at < 1.0 ? 1 : at >= (double)cut.mass ? cut.mass : (uint64_t)at;
-    } else if (step == 2 && set.low > 0.0f) {
+    } else if ((step == 2 && set.low > 0.0f) || step == 4) {
+      const double low = step == 2 ? bound : -(a.bits + 1) * 0.6931471805599453 * (double)set.temperature;   // half a unit
       const uint32_t key = row.least_key([&](uint32_t key) __attribute__((always_inline)) {
         const float x = unordered(key);
-        return x == most || (double)x - (double)most >= bound;
+        return x == most || RowScale::above(x) - row.scale.m >= low;
       });
       by = By::kKey;
-      goal = cut.key < key ? key : 0;
+      goal = cut.key < key ? key : step == 4 ? cut.key : 0;
     } else if (step == 3) {
       const double at = __builtin_floor((double)u * (double)cut.mass);
       const uint64_t below = !(at > 0.0) ? 0 : at >= (double)cut.mass ? cut.mass - 1 : (uint64_t)at;
       goal = (below < cut.mass ? below : cut.mass - 1) + 1;
+    } else if (step == 5) {
+      by = By::kCount;
+      goal = end;
     }
     if (goal == 0) continue;
     drawn = row.find(by, goal);
-    if (step < 3) cut = drawn;
+    if (step < 3) {
+      if (drawn.n <= cut.n) cut = drawn;
+    } else if (__builtin_expect(step < 5 && (step == 4 || drawn.n > cut.n), 0)) {
+      end = min(drawn.n, cut.n);
+      if (steps == 4) {
+        step = 4;
+        steps = 6;
+      }
+    }
   }
   if (tid == 0) {
     a.ids[t] = drawn.id;

@@ -721,8 +721,8 @@ fp8w_status fp8w_logprobs(const void* logits, fp8w_dtype dtype, int64_t stride, 
  *           min_p (0 or less: all)
  * but the first always.  Drawn is the first token whose weight and all before
  * it add up to more than u times the weights of the kept.  Uniforms outside
- * [0, 1) give the first or the last kept token, NaN the first; a setting that
- * is NaN is off.  A temperature of 0 (or less, or NaN) takes the first token
+ * [0, 1) give the first kept token or the last whose weight is not zero, NaN
+ * the first; a setting that is NaN is off.  A temperature of 0 (or less, or NaN) takes the first token
  * (log probability 0, one kept).  Masked tokens (-inf, NaN) are never drawn nor
  * counted; where +inf stands, only such tokens have weight.  A row masked
  * throughout gives token -1, log probability -inf and none kept.

@@ -1,0 +1,59 @@
+"""Drawn tokens at the ends of what may be drawn: random numbers of 1 and more,
+crowds of tokens whose bins are divided, and vocabularies whose sums are
+rounded by more than a random number's last place."""
+import pytest
+import torch
+
+from gpu_util import dev
+from test_gpu_sample import BF16, F32, F, _check  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _crowds(v):
+    """More tokens in a bin than a list holds, which is not the first bin: of
+    different values and of one, with a token far below and without, and two
+    crowds."""
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = -3 + 1e-3 * torch.randn(5, v, generator=g, device=dev())
+    x[2] = -3.0
+    x[3, ::2] -= 2.0
+    x[4, ::2] = -3.0
+    x[4, 1::2] = -4.0
+    x[:, v // 3] = 0.0
+    x[0, 5] = x[2, v - 1] = x[3, 0] = -200.0
+    return x
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("v", [7000, 60000])
+@pytest.mark.parametrize("u", [1 - 2.0 ** -24, 1.0, 1.5, float("inf")])
+def test_the_end_of_a_crowd(F, u, v, dtype):
+    x = _crowds(v).to(dtype)
+    for k in (dict(), dict(top_k=v - 1), dict(top_k=v - 2), dict(top_k=v // 2 + 1), dict(top_k=v // 2), dict(top_p=0.999),
+              dict(min_p=0.04), dict(min_p=1e-3), dict(temperature=2.0), dict(temperature=0.5, top_k=v - 1, top_p=0.9999),
+              dict(top_k=v - 1, min_p=1e-3), dict(top_k=100), dict(temperature=0.0)):
+        _check(F, x, u=u, **k)
+
+
+@pytest.mark.parametrize("v", [1 << 20, 1 << 22, 1 << 24])
+@pytest.mark.parametrize("u", [1 - 2.0 ** -24, 1.0])
+def test_never_past_what_is_kept(F, u, v):
+    """Sums of so many are known to 2^-27 ... 2^-19, so the last but a few may
+    be drawn in the last one's place; never one that was not kept."""
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = -3 + 1e-3 * torch.randn(3, v, generator=g, device=dev())
+    x[1] = -3.0
+    x[:, 9], x[2, 11] = 0.0, -200.0
+    token = torch.arange(v, device=dev())
+    for top_k in (None, v - 1, v - 2, v // 2):
+        k = None if top_k is None else torch.full((3,), top_k, dtype=torch.int32, device=dev())
+        r = F.fp8w_sample(x, torch.full((3,), u, device=dev()), top_k=k)
+        assert (r.kept == (v if top_k is None else top_k)).all()
+        for i in range(3):
+            t = int(r.tokens[i])
+            assert 0 <= t < v
+            rank = int((x[i] > x[i, t]).sum()) + int(((x[i] == x[i, t]) & (token < t)).sum())
+            room = 2.0 ** -19 * v + 1                                # what the sums leave open, in tokens of one weight
+            end = int(r.kept[i]) - (1 if i == 2 and top_k is None else 0)   # the token far below has no weight
+            assert rank < end and (rank == end - 1 if u == 1 else rank >= end - 1 - room), (i, rank, end)
