@@ -774,7 +774,7 @@ struct Settings {
   __device__ __forceinline__ Settings(const SampleArgs& a, int t)
       : temperature(a.temperature ? a.temperature[t] : 1.0f), p(a.top_p ? a.top_p[t] : 1.0f),
         low(a.min_p ? a.min_p[t] : 0.0f), k(a.top_k ? a.top_k[t] : 0) {
-    if (!(temperature > 0.0f)) {
+    if (!(temperature > 0.0f) || low > 1.0f) {   // the first alone (above 1 not even its equals stay)
       temperature = 1.0f;
       k = 1;
       p = 1.0f;
@@ -918,8 +918,8 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
   // counts, to the last kept token whose weight is not zero.  (What long
   // functions need is taken before: the compiler would keep their constants in
   // registers throughout.)
-  double bound = 0.0;
-  if (set.low > 0.0f) bound = log((double)set.low) * (double)set.temperature;
+  double bound = -(double)__builtin_inff();   // at an infinite temperature all are as likely
+  if (set.low > 0.0f && set.temperature < __builtin_inff()) bound = log((double)set.low) * (double)set.temperature;
   Place cut{live, row.all_mass[0], ordered(least), -1}, drawn = cut;
   // The steps: top-k, top-p, min-p, the draw; and seldom, by counts, the last
   // place with weight, and the place that is drawn.

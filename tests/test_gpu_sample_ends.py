@@ -1,6 +1,8 @@
 """Drawn tokens at the ends of what may be drawn: random numbers of 1 and more,
-crowds of tokens whose bins are divided, and vocabularies whose sums are
-rounded by more than a random number's last place."""
+crowds of tokens whose bins are divided, vocabularies whose sums are rounded by
+more than a random number's last place, and minimal probabilities of 1 and
+more."""
+import numpy as np
 import pytest
 import torch
 
@@ -57,3 +59,16 @@ def test_never_past_what_is_kept(F, u, v):
             room = 2.0 ** -19 * v + 1                                # what the sums leave open, in tokens of one weight
             end = int(r.kept[i]) - (1 if i == 2 and top_k is None else 0)   # the token far below has no weight
             assert rank < end and (rank == end - 1 if u == 1 else rank >= end - 1 - room), (i, rank, end)
+
+
+@pytest.mark.parametrize("v", [40, 7000, 60000])
+def test_a_minimal_probability_of_one_and_above(F, v):
+    """Of one the first and its equals, above the first alone."""
+    x = torch.zeros(3, v, device=dev())
+    x[1] = -torch.arange(v, device=dev()).remainder(3).float()
+    x[2, :5] = -np.inf
+    for low in (1.0, 1.0 + 2.0 ** -23, 2.0, float("inf")):
+        for k in (dict(), dict(top_k=7), dict(top_p=0.5), dict(temperature=3.0), dict(temperature=float("inf"))):
+            _check(F, x, u=0.7 if "top_p" not in k else 0.3, min_p=low, **k)
+    x[2, v - 2:] = np.inf
+    _check(F, x, u=0.75, min_p=2.0)
