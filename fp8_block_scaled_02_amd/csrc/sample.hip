@@ -782,6 +782,10 @@ struct Settings {
     }
     few = k > 0 && k <= kSmCap / 2;
   }
+  // Beside a logit of +inf no other has weight, at no temperature.
+  __device__ __forceinline__ void beside(float most) {
+    if (most > 3.4028234e38f) temperature = __builtin_fminf(temperature, 3.4028234e38f);
+  }
 };
 
 // The largest and smallest live logit, in every thread.
@@ -839,10 +843,11 @@ __global__ __launch_bounds__(kSmThreads) void k_sample_bins(SampleArgs a) {
   __shared__ uint64_t words[kSmBins];
   const int t = blockIdx.x / a.segs, seg = blockIdx.x - t * a.segs;
   const float2 piece = piece_range(a, t);
-  const Settings set(a, t);
+  Settings set(a, t);
   const Logits<T, kSmThreads> logits(a, t, seg);
   const float2 range = joined_range(piece);
   if (range.x == -__builtin_inff()) return;
+  set.beside(range.x);
   const RowScale scale(range.x, range.y, set.temperature, a);
   fill(logits, scale, words, !set.few, [](float, uint32_t b) { return b; });
   for (int b = threadIdx.x; b < kSmBins; b += kSmThreads) a.words[(size_t)blockIdx.x * kSmBins + b] = words[b];
@@ -869,7 +874,7 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
       for (int i = 0; i < kSmPieces; ++i)
         words[j][i] = a.words[((size_t)t * a.segs + (i < a.segs ? i : 0)) * kSmBins + tid + j * N];
   }
-  const Settings set(a, t);
+  Settings set(a, t);
   const float u = a.uniforms[t];
   if constexpr (PIECES)
     range = joined_range(range);
@@ -884,6 +889,7 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
     }
     return;
   }
+  set.beside(most);
   Row<T, N> row{a, t, s, logits, RowScale(most, least, set.temperature, a), ordered(most)};
   bool weights = !set.few;
   uint32_t live = 0;

@@ -96,8 +96,7 @@ def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=Non
             continue
         with np.errstate(invalid="ignore"):
             d = np.where(x == x[0], 0.0, x - x[0])
-            scaled = np.where(np.isinf(d), d if temp < np.inf else 0.0 * x, d / temp)
-            scaled = np.where(np.isnan(scaled), -np.inf, scaled)
+            scaled = np.where(np.isinf(d), d, d / temp)   # beside +inf nothing else has weight, at no temperature
         n = len(x)
         if top_k is not None and top_k[r] > 0:
             n = min(n, int(top_k[r]))

@@ -1,7 +1,7 @@
 """Drawn tokens at the ends of what may be drawn: random numbers of 1 and more,
 crowds of tokens whose bins are divided, vocabularies whose sums are rounded by
-more than a random number's last place, and minimal probabilities of 1 and
-more."""
+more than a random number's last place, minimal probabilities of 1 and more,
+and an infinite temperature."""
 import numpy as np
 import pytest
 import torch
@@ -72,3 +72,17 @@ def test_a_minimal_probability_of_one_and_above(F, v):
             _check(F, x, u=0.7 if "top_p" not in k else 0.3, min_p=low, **k)
     x[2, v - 2:] = np.inf
     _check(F, x, u=0.75, min_p=2.0)
+
+
+@pytest.mark.parametrize("v", [40, 7000, 60000])
+def test_an_infinite_temperature(F, v):
+    """All tokens weigh the same, but beside a logit of +inf no finite one has weight."""
+    x = torch.randn(4, v, generator=torch.Generator(device="cuda").manual_seed(v), device=dev())
+    x[1, 5:9] = -np.inf
+    x[2, 7], x[2, v - 3] = np.inf, np.inf
+    x[3] = torch.finfo(F32).max
+    x[3, 3] = np.inf
+    for k in (dict(), dict(min_p=1.0), dict(min_p=0.5), dict(top_p=0.5), dict(top_k=6), dict(top_k=6, top_p=0.9, min_p=1e-3)):
+        for u in (0.0, 0.3, 0.99, 1.0):
+            _check(F, x, u=u, temperature=float("inf"), **k)
+            _check(F, x, u=u, temperature=3e38, **k)
