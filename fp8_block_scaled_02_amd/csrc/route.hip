@@ -141,13 +141,16 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t at) {
   return bf16_lo(ld_global<uint16_t>(p, (size_t)at * 2));
 }
 
-// The experts' scores in fp64 (softmax: not yet divided by their sum).  Of few
+// The experts' scores in fp64 (softmax: not yet divided by their sum; +inf is
+// taken as 2^200, far above all others, so that it has a difference from itself
+// and a score of 1).  Of few
 // experts a lane by one copy of the exponential, with the registers moved on
 // under it: a lone token's time is that of fetching the code.
 template <int R>
 __device__ __forceinline__ void scores(const RouteArgs& a, const float (&x)[R], float top, double (&score)[R]) {
+  const double best = __builtin_fmin((double)top, 0x1p200);
   const auto of = [&](float v) {
-    const double e = exp(a.score == 0 ? (double)v - (double)top : -(double)v);
+    const double e = exp(a.score == 0 ? __builtin_fmin((double)v, 0x1p200) - best : -(double)v);
     return a.score == 0 ? e : 1.0 / (1.0 + e);
   };
   if constexpr (R > 4) {
@@ -190,10 +193,7 @@ __device__ __forceinline__ void shut_groups(const RouteArgs& a, const float (&x)
     double score[R];
     scores<R>(a, x, top, score);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const double s = a.score == 0 && x[r] == top ? 1.0 : score[r];   // infinities next to each other have no difference
-      meet(x[r] > -__builtin_inff() ? s : ninf, ninf);
-    }
+    for (int r = 0; r < R; ++r) meet(x[r] > -__builtin_inff() ? score[r] : ninf, ninf);
   } else {
 #pragma unroll
     for (int r = 0; r < R; ++r) meet((double)key[r], ninf);

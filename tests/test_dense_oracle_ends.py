@@ -27,3 +27,15 @@ def test_uniforms_of_one_give_the_last_with_weight():
     assert ids.tolist() == [3, 4] and kept.tolist() == [5, 5]
     ids, _, kept = D.sample(x, np.array([1.0, 7.0]), top_k=np.array([3, 3]))
     assert ids.tolist() == [2, 2] and kept.tolist() == [3, 3]
+
+
+def test_routing_with_infinite_logits_and_a_bias():
+    x = np.array([[0.0, INF, 1.0, 2.0], [INF, 0.0, INF, -INF]])
+    bias = np.array([0.1, 0.2, 0.3, -0.1])
+    with np.errstate(invalid="ignore"):
+        ids = D.route_grouped(x, 4, 1, 1, bias=bias)[0]              # keys .1 1.2 .3 -.1; .6 .2 .8
+        assert ids.tolist() == [[1, 2, 0, 3], [2, 0, 1, -1]]
+        ids = D.route_grouped(x, 2, 2, 1, bias=bias)[0]
+        assert ids.tolist() == [[1, 0], [2, -1]]
+        bias[1] = -INF
+        assert D.route_grouped(x, 2, 1, 1, bias=bias)[0].tolist() == [[2, 0], [2, 0]]
