@@ -13,10 +13,13 @@
 
 namespace fp8w {
 
-// g / (1 + exp(-t)) * u within a few units of the last place of fp32:
+// g / (1 + exp(-t)) * u within a few units of the last place of fp32, and zero
+// where 1 + exp(-t) is above 2^126 (t below -87.3): the hardware reciprocal gives
+// no subnormal numbers, and what is lost is below 88 * 2^-126 < 2^-119 of u.
 // exp(-t) as 2^s times a first-order correction for what rounding s = -t
 // log2 e lost, and the hardware reciprocal (an IEEE division of every output
-// cost as many instructions as a third of the products at k = 2048).
+// cost as many instructions as a third of the products at k = 2048).  A gate of
+// -inf gives -inf * 0, NaN.
 __device__ __forceinline__ float sigmoid_times(float g, float t, float u) {
   constexpr float kLog2E = 0x1.715476p+0f, kLog2ELow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
   // Beyond 200 either way 2^s is infinite and the result zero, or it is zero

@@ -649,9 +649,12 @@ fp8w_status fp8w_combine_experts(const uint16_t* y, int64_t slot_rows, const flo
  * same address and stride, y of bf16), and is then added to in place; any
  * other overlap is refused.  The space between y's rows is left as it was.
  * v meets the bound of fp8w_gemv (2^-7 sum |x| |deq| + 1e-6) with room: its
- * error is fp32 rounding of the sums alone.  An infinity or NaN of x reaches its own row
- * alone, as the formula has it; gates and values beyond fp32's range pass as
- * the formula's limit.
+ * error is fp32 rounding of the sums alone.  Activations are good to some last
+ * places of fp32; of silu and the gelus what is below 2^-119 (times u) may be
+ * zero.  An infinity or NaN of x reaches its own row alone, as the formula has
+ * it; sums beyond fp32's range are infinite, of which +inf passes as the
+ * formula's limit and -inf is NaN under all activations but NONE and RELU
+ * (-inf * 0).
  * Requires 0 <= m <= 2^30 (0: no launch), 1 <= n <= 2^28 (gated: even),
  * 16 <= k <= 2^28, k % 16 == 0, strides >= the columns and <= 2^31 - 1 (x's
  * <= 2^28).
