@@ -164,7 +164,9 @@ __device__ __forceinline__ void stage16(const void* from, unsigned char* to) {
 }
 
 // Block scale `at` (uniform), by a scalar load: there are none of two bytes, and
-// a vector load would be waited for with all that left before it.
+// a vector load would be waited for with all that left before it.  For a bf16
+// scale the aligned word it lies in is read: at either end of the buffer that may
+// be two bytes outside it, in the same page, whose value is dropped.
 template <int FMT>
 __device__ __forceinline__ float scalar_scale(const char* scales, int at) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(scales) + (size_t)at * (FMT == kFmtBlock ? 4 : 2);
@@ -831,7 +833,7 @@ __global__ __launch_bounds__(NW * kWave) void k_linear_stream(LinearCall c) {
   const int n_out = GATED ? c.n / 2 : c.n;
   const int k = c.k, nkb = (k + 127) / 128, ng = (k + 31) / 32;
   int kb0 = 0, blocks = nkb;
-  if (splits > 1) {   // nkb <= 2^21, splits <= 64
+  if (splits > 1) {   // nkb <= 2^21, splits <= kFill = 256: 32 bits hold the product
     kb0 = nkb * split / splits;
     blocks = nkb * (split + 1) / splits - kb0;
   }

@@ -14,9 +14,9 @@
 // Weights are whole numbers, 2^S w rounded (S = 62 - ceil(log2 vocab), at most
 // 50), from fp64 exponentials: their sums are the same in any order, so that
 // atomics may add them up.  Those of a whole bin are known to 2^-31 of their sum
-// (2^-19 for 2^24 tokens), as RowScale says.  fp32 sums would turn over one
-// choice of some thousand among 10^5 tokens.  (fp64 multiply-adds run at the
-// rate of fp32's.)
+// (2^-19 for 2^24 tokens), as RowScale says, and half a unit of each of its
+// tokens.  fp32 sums would turn over one choice of some thousand among 10^5
+// tokens.  (fp64 multiply-adds run at the rate of fp32's.)
 //
 // A row is taken in passes: its largest and smallest logit; a histogram of the
 // distance from the largest, counts and weights; and the tokens of the bins
@@ -97,8 +97,9 @@ struct SampleArgs {
 // (a bin is no wider than 62/1023 powers of two), as a whole number of
 // 2^-fraction, so that a bin's weight is that of its middle times (count + sum
 // of e).  Half a unit's rounding and the term left out, |ln2 wide/2|^5 / 120 <
-// 2^-34, make 2^-31 of a weight for up to 2^18 tokens, whose counts leave 31
-// bits of fraction; above, both give up a bit for each doubling.  The sum of e +
+// 2^-34, make 2^-31 of a weight (and that of the middle is a whole number, half a
+// unit off) for up to 2^18 tokens, whose counts leave 31 bits of fraction; above,
+// count and sum each take one of these for each doubling.  The sum of e +
 // 2^-5 stays below 2^(fraction - 4) times the count, and so below 2^shift.  An
 // exponential for every token would take twice as long, a second atomic as well.
 struct RowScale {

@@ -658,8 +658,8 @@ fp8w_status fp8w_combine_experts(const uint16_t* y, int64_t slot_rows, const flo
  * Requires 0 <= m <= 2^30 (0: no launch), 1 <= n <= 2^28 (gated: even),
  * 16 <= k <= 2^28, k % 16 == 0, strides >= the columns and <= 2^31 - 1 (x's
  * <= 2^28).
- * Errors: NULL, SHAPE (also: workspace too small), UNSUPPORTED (format, act,
- * dtype), ALIGN, OVERLAP, HIP. */
+ * Errors: NULL, SHAPE (also: workspace too small; 2^23 workgroups or more, which
+ * m = 2^30 takes), UNSUPPORTED (format, act, dtype), ALIGN, OVERLAP, HIP. */
 int64_t fp8w_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, fp8w_format format, fp8w_act act);
 fp8w_status fp8w_linear(const uint16_t* x, int64_t x_stride, int64_t m, const uint8_t* codes, const void* scales,
                         fp8w_format format, int64_t n, int64_t k, const void* bias, fp8w_dtype bias_dtype,
@@ -730,12 +730,13 @@ fp8w_status fp8w_logprobs(const void* logits, fp8w_dtype dtype, int64_t stride, 
  * counted; where +inf stands, only such tokens have weight.  A row masked
  * throughout gives token -1, log probability -inf and none kept.
  * Weights are fixed-point numbers of 38 to 50 bits below the largest out of
- * fp64 exponentials, and sums of many are within 2^-31 of themselves (2^-19
- * for 2^24 tokens), so that the choice does not depend on the order of sums,
- * and hardly on their rounding.
+ * fp64 exponentials, whose half units add up to no more than 2^-27 of a row's
+ * sum for up to 2^18 tokens (2^-15 for 2^24), and sums of many are within 2^-31
+ * of themselves besides (2^-19 for 2^24 tokens), so that the choice does not
+ * depend on the order of sums, and hardly on their rounding.
  * workspace: fp8w_sample_workspace_bytes(tokens, vocab) bytes, 16-byte
  * aligned (0 where rows are short, or enough to fill the chip).  tokens may be
- * 0.  Requires 1 <= vocab <= 2^24, stride >= vocab.
+ * 0.  Requires tokens < 2^22, 1 <= vocab <= 2^24, stride >= vocab.
  * Errors: NULL, SHAPE (also: workspace too small), UNSUPPORTED (dtype),
  * ALIGN, OVERLAP, HIP. */
 int64_t fp8w_sample_workspace_bytes(int64_t tokens, int64_t vocab);
