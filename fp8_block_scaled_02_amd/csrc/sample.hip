@@ -976,7 +976,7 @@ __global__ __launch_bounds__(N, 4) void k_sample(SampleArgs a) {
     if (a.logprob) {
       const float x = unordered(drawn.key);
       const double d = (RowScale::above(x) - row.scale.m) / (double)set.temperature;
-      a.logprob[t] = (float)(d - (log((double)cut.mass) - a.bits * 0.6931471805599453));
+      a.logprob[t] = (float)(d - log(__builtin_ldexp((double)cut.mass, -a.bits)));   // of one token 0, exactly
     }
   }
 }

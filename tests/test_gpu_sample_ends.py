@@ -86,3 +86,16 @@ def test_an_infinite_temperature(F, v):
         for u in (0.0, 0.3, 0.99, 1.0):
             _check(F, x, u=u, temperature=float("inf"), **k)
             _check(F, x, u=u, temperature=3e38, **k)
+
+
+@pytest.mark.parametrize("v", [1, 900, 5000, 9000, 20000, 40000, 70000, 151936, 300000, 600000, 1 << 20, 1 << 21, 1 << 22])
+def test_the_only_token_left_has_log_probability_zero(F, v):
+    """Whatever the fixed point of its weight."""
+    x = torch.randn(3, v, generator=torch.Generator(device="cuda").manual_seed(v), device=dev())
+    x[:, v // 2] = 9.0
+    u = torch.tensor([0.0, 0.4, 0.9], device=dev())
+    full = lambda value, dtype=F32: torch.full((3,), value, dtype=dtype, device=dev())   # noqa: E731
+    for k in (dict(temperature=full(0.0)), dict(top_k=full(1, torch.int32)), dict(top_p=full(1e-9)), dict(min_p=full(0.9)),
+              dict(min_p=full(2.0)), dict(temperature=full(0.01), top_k=full(1, torch.int32))):
+        r = F.fp8w_sample(x, u, **k)
+        assert (r.tokens == v // 2).all() and (r.kept == 1).all() and (r.logprob == 0).all(), (k, r)
