@@ -503,7 +503,11 @@ hipError_t route_by_experts(RouteArgs a, hipStream_t stream) {
     };
     if (a.top_k <= 16 && lanes(16) <= 16) return route_launch<T, Key, 16, 16, true>(a, stream);
     if (lanes(64) <= 8) return route_launch<T, Key, 64, 8, true>(a, stream);
-    return route_launch<T, Key, 64, 32, true>(a, stream);   // up to 1024 / groups over 64 / parts >= 32 / groups lanes
+    // Up to 1024 / groups over 64 / parts >= 32 / groups lanes.  32 experts a lane
+    // spill (with a bias 114 registers): 8 of 1024 experts in 16 groups 51-61 us
+    // without a bias and 107-156 with one for 32 ... 4096 tokens; 512 experts in 8
+    // groups, the form above, 22-27 and 32-38.
+    return route_launch<T, Key, 64, 32, true>(a, stream);
   }
   if (a.top_k <= 16) {
     if (a.experts <= 64) return route_launch<T, Key, 16, 4>(a, stream);

@@ -30,9 +30,9 @@
 // histograms.
 //
 // What bounds it is a chain of latencies: 4 x 151936 bf16 under top-k and top-p
-// takes 27 us, of which the range 3, the histogram 5.5 and the choice 17.5 (code
+// takes 27 us, of which the range 3, the histogram 6 and the choice 18 (code
 // that runs but once, and is fetched as it runs; some twenty barriers a place
-// that is looked for).  512 x 32000 43 us (0.8 TB/s): two rounds of the same.
+// that is looked for).  512 x 32000 44 us (0.75 TB/s): two rounds of the same.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
