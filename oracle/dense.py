@@ -111,7 +111,8 @@ def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=Non
         stop = max(stop, 1)
         u = float(uniforms[r])
         goal = 0.0 if not u > 0 else np.longdouble(u) * upto[stop - 1]
-        j = min(int((upto[:stop] <= goal).sum()), int((upto[:stop] < upto[stop - 1]).sum()))
+        some = int((w[:stop] >= 2.0 ** -(weight_bits(vocab) + 1)).sum())   # of a weight that is not zero
+        j = min(int((upto[:stop] <= goal).sum()), some - 1)
         tokens[r], kept[r] = order[j], stop
         logprob[r] = float(scaled[j] - np.log(upto[stop - 1]))
     return tokens, logprob, kept

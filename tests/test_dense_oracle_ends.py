@@ -27,6 +27,8 @@ def test_uniforms_of_one_give_the_last_with_weight():
     assert ids.tolist() == [3, 4] and kept.tolist() == [5, 5]
     ids, _, kept = D.sample(x, np.array([1.0, 7.0]), top_k=np.array([3, 3]))
     assert ids.tolist() == [2, 2] and kept.tolist() == [3, 3]
+    ids, _, kept = D.sample(np.array([[0.0, -36.0, -34.0]]), np.array([1.0]))   # half a unit: 2^-51 = e^-35.35
+    assert ids.tolist() == [2] and kept.tolist() == [3]
 
 
 def test_routing_with_infinite_logits_and_a_bias():

@@ -99,3 +99,14 @@ def test_the_only_token_left_has_log_probability_zero(F, v):
               dict(min_p=full(2.0)), dict(temperature=full(0.01), top_k=full(1, torch.int32))):
         r = F.fp8w_sample(x, u, **k)
         assert (r.tokens == v // 2).all() and (r.kept == 1).all() and (r.logprob == 0).all(), (k, r)
+
+
+@pytest.mark.parametrize("v", [50, 4096, 4097, 9000, 70000])
+def test_the_last_token_with_weight(F, v):
+    """Weights below half a unit are zero: such tokens are kept, and never drawn."""
+    x = -torch.arange(v, device=dev()).remainder(997).float() / 4 - 1
+    x = torch.stack([x, x / 2, x * 8])
+    x[:, 0] = 0.0
+    for u in (1.0, 3.0):
+        for k in (dict(), dict(top_k=v - 3), dict(top_k=40), dict(temperature=0.3), dict(temperature=5.0), dict(min_p=1e-18), dict(min_p=1e-9)):
+            _check(F, x, u=u, **k)
